@@ -94,6 +94,16 @@ def load(build_if_missing: bool = False):
             "calibatt_anchor_energy_workspace_size": (sz, [i32, i32, i32, i32, i32, i32]),
             "calibatt_anchor_block_energy": (i32, [P, P, i32, i32, i32, i32, i32, i32, f32, P, i32, P, sz, P, i32,
                                                    f64, P, P, P, P, f64, P]),
+            "calibatt_rope_plan_init": (i32, [P, f64, i32, i32, P]),
+            "calibatt_rope_fwd": (i32, [P, P, i64, i64, i32, P, i64, i64, i32, i64, i32, P, i32, i32, P, P, i64, i64,
+                                        P, i64, i64, P]),
+            "calibatt_rope_bwd": (i32, [P, P, i64, i64, i32, P, i64, i64, i32, i64, i32, P, i32, i32, P, P, i64, i64,
+                                        P, i64, i64, P]),
+            "calibatt_cache_write": (i32, [P, i64, i64, P, i64, i64, i32, i32, i32, P, P, i32, i32, P, i32, i32, P, P,
+                                           P, P, P]),
+            "calibatt_cache_attn_workspace_size": (sz, [i32, i32, i32, i32, i32, i32]),
+            "calibatt_cache_attn_fwd": (i32, [P, i32, i32, i32, i32, f32, i32, P, P, i32, i32, i32, P, i32, i32, P, P,
+                                              P, P, P, P, P, sz, P]),
             "calibatt_aggregate_rows_workspace_size": (sz, [i64]),
             "calibatt_aggregate_mask_rows": (i32, [P, i32, i64, i32, f64, P, P, P, i64, P, P, sz, P]),
         }
@@ -726,3 +736,232 @@ class MaskBank:
         e = self.get(t, l)
         return mixed_attn_fwd(q, k, v, F, H, W, e["row_ptr"], e["col_idx"], e["rep_heads"], e["work_list"],
                               k_anchor=k_anchor, o=o, lse=lse, stream=stream)
+
+
+# ------------------------------------------------------------------ streaming: rotary positions
+
+class RopePlan(ctypes.Structure):
+    """Axis and frequency of every rotated channel pair (calibatt_rope_plan)."""
+    _fields_ = [("pairs", ctypes.c_int32), ("pairing", ctypes.c_int32), ("turns", ctypes.c_double * 64),
+                ("axis", ctypes.c_uint8 * 64)]
+
+
+_PAIRINGS = {"interleaved": 0, "halves": 1}
+_LADDERS = {"axis": 0, "shared": 1}
+
+
+def rope_plan(dims=(44, 42, 42), theta=10000.0, pairing="interleaved", ladder="axis") -> RopePlan:
+    """Plan of a rotation of dims[0], dims[1], dims[2] channels by the time,
+    height and width position (calibatt_rope_plan_init)."""
+    if len(dims) != 3:
+        raise ValueError("dims must name the channels of three axes")
+    if pairing not in _PAIRINGS or ladder not in _LADDERS:
+        raise ValueError(f"pairing must be one of {sorted(_PAIRINGS)}, ladder one of {sorted(_LADDERS)}")
+    plan = RopePlan()
+    d = (ctypes.c_int32 * 3)(*[int(x) for x in dims])
+    _check(load().calibatt_rope_plan_init(d, float(theta), _PAIRINGS[pairing], _LADDERS[ladder], ctypes.byref(plan)),
+           "calibatt_rope_plan_init")
+    return plan
+
+
+def _rows(t, name, dev=None):
+    """A bf16 CUDA tensor of three dimensions with 128 contiguous channels; its strides may be any."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == torch.bfloat16):
+        raise TypeError(f"{name} must be a CUDA {torch.bfloat16} tensor")
+    if t.dim() != 3 or t.shape[2] != HEAD_DIM or t.stride(2) != 1:
+        raise ValueError(f"{name} must be three-dimensional with {HEAD_DIM} contiguous channels")
+    if dev is not None and t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, not on {dev}")
+    return t
+
+
+def _on_device(t, dtype, name, dev):
+    _cuda_tensor(t, dtype, name)
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, not on {dev}")
+    return t
+
+
+class _Device:
+    """Makes `dev` the current device for a call (a no-op when it already is)."""
+    __slots__ = ("dev", "prev")
+
+    def __init__(self, dev):
+        self.dev = dev.index
+
+    def __enter__(self):
+        self.prev = torch.cuda.current_device()
+        if self.prev != self.dev:
+            torch.cuda.set_device(self.dev)
+
+    def __exit__(self, *exc):
+        if self.prev != self.dev:
+            torch.cuda.set_device(self.prev)
+
+
+def _new(shape, dtype, dev, stream):
+    """A tensor of the stream's own memory pool: an allocation on the current
+    stream could still be in use there when another stream writes it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _rope(what, forward, q, k, plan, grid, start, pos, q_out, k_out, stream):
+    # forward: token-major in, head-major out; gradient: the other way round
+    dev = _rows(q, "q").device
+    tok = 0 if forward else 1
+    n = q.shape[tok]
+    args = []
+    outs = [q_out, k_out]
+    for i, (x, name) in enumerate(((q, "q"), (k, "k"))):
+        if x is None:
+            if outs[i] is not None:
+                raise ValueError(f"{name}_out without {name}")
+            args.append((None, 0, 0, 0, None, 0, 0))
+            continue
+        _rows(x, name, dev)
+        heads = x.shape[1 - tok]
+        if x.shape[tok] != n:
+            raise ValueError(f"{name} has {x.shape[tok]} tokens, q has {n}")
+        shape = (heads, n, HEAD_DIM) if forward else (n, heads, HEAD_DIM)
+        if outs[i] is None:
+            outs[i] = _new(shape, torch.bfloat16, dev, stream)
+        out = _rows(outs[i], f"{name}_out", dev)
+        if tuple(out.shape) != shape:
+            raise ValueError(f"{name}_out must be {list(shape)}")
+        args.append((x.data_ptr(), x.stride(tok), x.stride(1 - tok), heads, out.data_ptr(), out.stride(1 - tok),
+                     out.stride(tok)))
+    if (grid is None) == (pos is None):
+        raise ValueError("give the positions as a grid (H, W) or as a tensor pos [n][3]")
+    H, W = (0, 0) if grid is None else (int(grid[0]), int(grid[1]))
+    if pos is not None:
+        _on_device(pos, torch.int32, "pos", dev)
+        if tuple(pos.shape) != (n, 3):
+            raise ValueError(f"pos must be [{n}][3]")
+    st = (ctypes.c_int32 * 3)(*[int(x) for x in start])
+    a, b = args
+    with _Device(dev):
+        rc = getattr(load(), what)(ctypes.byref(plan), a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3], n, HEAD_DIM,
+                                   None if pos is None else pos.data_ptr(), H, W, st, a[4], a[5], a[6], b[4], b[5],
+                                   b[6], _stream(stream))
+    _check(rc, what)
+    return outs[0], outs[1]
+
+
+def rope_fwd(q, k, plan, grid=None, start=(0, 0, 0), pos=None, q_out=None, k_out=None, stream=None):
+    """Rotates queries [n][heads][128] and keys [n][heads_k][128] (or None) of
+    any strides by their positions: a grid (H, W) whose first token is at
+    `start` (time, height, width), or pos, int32 [n][3]. Returns them as
+    [heads][n][128], the layout of the attention calls."""
+    return _rope("calibatt_rope_fwd", True, q, k, plan, grid, start, pos, q_out, k_out, stream)
+
+
+def rope_bwd(dq_out, dk_out, plan, grid=None, start=(0, 0, 0), pos=None, dq=None, dk=None, stream=None):
+    """Gradients of rope_fwd's inputs, [n][heads][128], from those of its
+    outputs, [heads][n][128] of any strides (expanded ones too)."""
+    return _rope("calibatt_rope_bwd", False, dq_out, dk_out, plan, grid, start, pos, dq, dk, stream)
+
+
+# ------------------------------------------------------------------ streaming: 8-bit cache
+
+def _cache_args(k8, v8, k_scale, v_scale, tok_start, kv_len, table, dev):
+    for t, name in ((k8, "k8"), (v8, "v8")):
+        if not (isinstance(t, torch.Tensor) and t.dtype in (torch.float8_e4m3fn, torch.uint8)):
+            raise TypeError(f"{name} must be a contiguous CUDA float8_e4m3fn (or uint8) tensor")
+        _on_device(t, t.dtype, name, dev)
+        if t.dim() != 4 or t.shape[2:] != (BLOCK, HEAD_DIM):
+            raise ValueError(f"{name} must be [pages][heads][{BLOCK}][{HEAD_DIM}]")
+    if v8.shape != k8.shape:
+        raise ValueError("k8 and v8 differ in shape")
+    for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        _on_device(t, torch.float32, name, dev)
+        if t.shape != k8.shape[:2]:
+            raise ValueError(f"{name} must be [pages][heads]")
+    for t, name in ((tok_start, "tok_start"), (kv_len, "kv_len"), (table, "table")):
+        _on_device(t, torch.int32, name, dev)
+    batch = kv_len.numel()
+    if tok_start.numel() != batch + 1 or table.dim() != 2 or table.shape[0] != batch:
+        raise ValueError("tok_start must be [batch + 1], kv_len [batch], table [batch][pages of a stream]")
+    return batch
+
+
+def cache_write(k, v, k8, v8, k_scale, v_scale, tok_start, kv_len, table, max_new=None, stream=None):
+    """Appends keys and values [n][heads][128] (any strides) of the batch's new
+    tokens to the paged 8-bit cache (calibatt_cache_write). max_new: the most
+    new tokens of one stream (default: n)."""
+    dev = _rows(k, "k").device
+    _rows(v, "v", dev)
+    n, heads = k.shape[0], k.shape[1]
+    if v.shape != k.shape:
+        raise ValueError("k and v differ in shape")
+    batch = _cache_args(k8, v8, k_scale, v_scale, tok_start, kv_len, table, dev)
+    if k8.shape[1] != heads:
+        raise ValueError(f"the cache has {k8.shape[1]} heads, k has {heads}")
+    with _Device(dev):
+        rc = load().calibatt_cache_write(k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0),
+                                         v.stride(1), heads, n, HEAD_DIM, tok_start.data_ptr(), kv_len.data_ptr(),
+                                         batch, n if max_new is None else int(max_new), table.data_ptr(),
+                                         table.shape[1], k8.shape[0], k8.data_ptr(), v8.data_ptr(),
+                                         k_scale.data_ptr(), v_scale.data_ptr(), _stream(stream))
+    _check(rc, "calibatt_cache_write")
+
+
+def cache_attn_workspace_size(batch, heads_q, heads_kv, n, max_new, max_kv) -> int:
+    return load().calibatt_cache_attn_workspace_size(int(batch), int(heads_q), int(heads_kv), int(n), int(max_new),
+                                                     int(max_kv))
+
+
+def cache_attn_workspace(q, k8, table, max_new=None, max_kv=None):
+    """Workspace of cache_attn_fwd for these tensors (None when none is needed)."""
+    heads_q, n = _bhnd(q)
+    with _Device(q.device):
+        need = cache_attn_workspace_size(table.shape[0], heads_q, k8.shape[1], n, n if max_new is None else max_new,
+                                         table.shape[1] * BLOCK if max_kv is None else max_kv)
+    return torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+
+
+def cache_attn_fwd(q, k8, v8, k_scale, v_scale, tok_start, kv_len, table, max_new=None, max_kv=None, causal_unit=0,
+                   o=None, lse=None, ws=None, scale=None, want_lse=True, stream=None):
+    """Attention of the new tokens' queries [heads][n][128] over the paged
+    8-bit cache (calibatt_cache_attn_fwd); returns (o, lse). Rows of tokens
+    that belong to no stream keep what o and lse hold. max_new, max_kv: the
+    most new and cached tokens of one stream (default: n, the table's width)."""
+    heads_q, n = _bhnd(q)
+    dev = q.device
+    batch = _cache_args(k8, v8, k_scale, v_scale, tok_start, kv_len, table, dev)
+    heads_kv = k8.shape[1]
+    if heads_kv < 1 or heads_q % heads_kv:
+        raise ValueError(f"{heads_q} query heads do not share {heads_kv} key heads evenly")
+    if o is None:
+        o = _new(q.shape, torch.bfloat16, dev, stream)
+    else:
+        _on_device(o, torch.bfloat16, "o", dev)
+        if o.shape != q.shape:
+            raise ValueError("o and q differ in shape")
+    if lse is None and want_lse:
+        lse = _new((heads_q, n), torch.float32, dev, stream)
+    elif lse is not None:
+        _on_device(lse, torch.float32, "lse", dev)
+        if lse.shape != (heads_q, n):
+            raise ValueError(f"lse must be [{heads_q}][{n}]")
+    max_new = n if max_new is None else int(max_new)
+    max_kv = table.shape[1] * BLOCK if max_kv is None else int(max_kv)
+    scale = 1.0 / math.sqrt(HEAD_DIM) if scale is None else float(scale)
+    lib = load()
+    with _Device(dev):
+        if ws is None:
+            need = lib.calibatt_cache_attn_workspace_size(batch, heads_q, heads_kv, n, max_new, max_kv)
+            ws = _new(need, torch.uint8, dev, stream) if need else None
+        else:
+            _on_device(ws, torch.uint8, "ws", dev)
+        rc = lib.calibatt_cache_attn_fwd(q.data_ptr(), heads_q, heads_kv, n, HEAD_DIM, scale, int(causal_unit),
+                                         tok_start.data_ptr(), kv_len.data_ptr(), batch, max_new, max_kv,
+                                         table.data_ptr(), table.shape[1], k8.shape[0], k8.data_ptr(), v8.data_ptr(),
+                                         k_scale.data_ptr(), v_scale.data_ptr(), o.data_ptr(),
+                                         None if lse is None else lse.data_ptr(),
+                                         None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(),
+                                         _stream(stream))
+    _check(rc, "calibatt_cache_attn_fwd")
+    return o, lse

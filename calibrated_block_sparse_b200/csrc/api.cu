@@ -128,8 +128,8 @@ const char* calibatt_strerror(int code) {
   switch (code) {
     case CALIBATT_OK: return "ok";
     case CALIBATT_ERR_ARG: return "invalid argument";
-    case CALIBATT_ERR_CSR: return "malformed skip list (row_ptr / col_idx)";
-    case CALIBATT_ERR_ALIGN: return "device pointer not 16-byte aligned";
+    case CALIBATT_ERR_CSR: return "malformed skip list (row_ptr / col_idx), page table or token lists";
+    case CALIBATT_ERR_ALIGN: return "device pointer or stride not 16-byte aligned";
     case CALIBATT_ERR_UNSUPPORTED: return "unsupported shape (head dim must be 128; calibration needs nb <= 1024)";
     case CALIBATT_ERR_CUDA: return "CUDA call failed";
     case CALIBATT_ERR_TIMEOUT: return "bounded in-kernel wait ran out";
@@ -138,7 +138,7 @@ const char* calibatt_strerror(int code) {
   }
 }
 
-int calibatt_version(void) { return 200; }
+int calibatt_version(void) { return 201; }
 
 int calibatt_set_wait_limit(double seconds) {
   if (std::isnan(seconds) || seconds > 60.0) return CALIBATT_ERR_ARG;

@@ -46,8 +46,8 @@ typedef struct CUstream_st* calibatt_stream_t; /* same handle as cudaStream_t */
 typedef enum calibatt_status {
   CALIBATT_OK = 0,
   CALIBATT_ERR_ARG = -1,         /* null pointer, bad size or count, short workspace */
-  CALIBATT_ERR_CSR = -2,         /* malformed skip list (row_ptr / col_idx) */
-  CALIBATT_ERR_ALIGN = -3,       /* device pointer not 16-byte aligned */
+  CALIBATT_ERR_CSR = -2,         /* malformed skip list (row_ptr / col_idx), page table or token lists */
+  CALIBATT_ERR_ALIGN = -3,       /* device pointer or stride not 16-byte aligned */
   CALIBATT_ERR_UNSUPPORTED = -4, /* d != 128, or nb > 1024 for calibration */
   CALIBATT_ERR_CUDA = -5,        /* a CUDA runtime/driver call failed */
   CALIBATT_ERR_TIMEOUT = -6,     /* a bounded in-kernel wait ran out (device status) */
@@ -288,6 +288,131 @@ int calibatt_mixed_attn_fwd_host(const calibatt_bf16* q_host, const calibatt_bf1
                                  calibatt_bf16* q_dev, calibatt_bf16* k_dev, calibatt_bf16* v_dev,
                                  calibatt_bf16* o_dev, float* lse_dev, void* ws, size_t ws_bytes,
                                  calibatt_stream_t stream);
+
+/* ---------------------------------------------------------------- streaming: rotary positions */
+
+/* Pairing of channels: pair i is channels (2i, 2i+1), or (i, i + pairs). */
+#define CALIBATT_ROPE_INTERLEAVED 0
+#define CALIBATT_ROPE_HALVES 1
+/* Frequencies: theta^(-2j/dims[a]) for the j-th pair of axis a (each axis runs
+ * its own ladder), or theta^(-2i/(dims[0]+dims[1]+dims[2])) for the i-th of all
+ * pairs (one ladder that the axes share out). */
+#define CALIBATT_ROPE_LADDER_AXIS 0
+#define CALIBATT_ROPE_LADDER_SHARED 1
+
+/* Rotary positions over the axes time, height and width: which axis turns a
+ * pair of channels, and by which part of a full turn per step of position.
+ * Fill it with calibatt_rope_plan_init, or by hand for other frequencies.
+ * Channels behind the rotated 2*pairs pass through. Host memory. */
+typedef struct calibatt_rope_plan {
+  int32_t pairs;    /* rotated pairs, 1..64 */
+  int32_t pairing;  /* CALIBATT_ROPE_INTERLEAVED or CALIBATT_ROPE_HALVES (pairs a multiple of 8) */
+  double turns[64]; /* angle per step of position, in turns (2 pi = 1) */
+  uint8_t axis[64]; /* 0 time, 1 height, 2 width */
+} calibatt_rope_plan;
+
+/* dims: host int32 [3], channels rotated by each axis (even, sum 2..128; the
+ * pairs of the time axis come first, then height, then width). */
+int calibatt_rope_plan_init(const int32_t* dims, double theta, int pairing, int ladder, calibatt_rope_plan* plan);
+
+/* Rotates the queries and keys of n tokens: for pair i of channels (a, b) of a
+ * token at position p, with the angle w = 2 pi p[axis[i]] turns[i],
+ *   y_a = x_a cos w - x_b sin w,   y_b = x_a sin w + x_b cos w,
+ * in fp32 with the angle reduced in 64 bits, rounded once to bf16.
+ * Positions: pos (device int32 [n][3]: time, height, width of each token), or,
+ * with pos = NULL, tokens of a grid in the order t = f*H*W + r*W + c at
+ * (start[0]+f, start[1]+r, start[2]+c) (start: host int32 [3], or NULL for 0;
+ * start[0] is the first frame of a stream's new frames).
+ *   q, k     : device bf16, channel 0 of token t and head h at
+ *              t*token_stride + h*head_stride (elements, multiples of 8; a
+ *              projection's [n][heads][128] has 128*heads and 128, a fused
+ *              one a larger token stride); heads_k = 0: no keys, k may be NULL
+ *   q_out, k_out : the same with strides of their own, for the attention calls
+ *              [heads][n][128] (128 and n*128). An output may be its input (the
+ *              same pointer and strides); any other overlap is refused.
+ * n = 0 does nothing. */
+int calibatt_rope_fwd(const calibatt_rope_plan* plan, const calibatt_bf16* q, int64_t q_token_stride,
+                      int64_t q_head_stride, int heads_q, const calibatt_bf16* k, int64_t k_token_stride,
+                      int64_t k_head_stride, int heads_k, int64_t n, int d, const int32_t* pos, int H, int W,
+                      const int32_t* start, calibatt_bf16* q_out, int64_t q_out_token_stride,
+                      int64_t q_out_head_stride, calibatt_bf16* k_out, int64_t k_out_token_stride,
+                      int64_t k_out_head_stride, calibatt_stream_t stream);
+
+/* Gradient of calibatt_rope_fwd: the gradients of its outputs, turned back by
+ * the same angles, are the gradients of its inputs. Arguments as there, with
+ * the gradients of q_out and k_out in the place of the inputs (a stride of 0
+ * reads one row for all tokens or heads). */
+int calibatt_rope_bwd(const calibatt_rope_plan* plan, const calibatt_bf16* dq_out, int64_t dq_out_token_stride,
+                      int64_t dq_out_head_stride, int heads_q, const calibatt_bf16* dk_out,
+                      int64_t dk_out_token_stride, int64_t dk_out_head_stride, int heads_k, int64_t n, int d,
+                      const int32_t* pos, int H, int W, const int32_t* start, calibatt_bf16* dq,
+                      int64_t dq_token_stride, int64_t dq_head_stride, calibatt_bf16* dk, int64_t dk_token_stride,
+                      int64_t dk_head_stride, calibatt_stream_t stream);
+
+/* ---------------------------------------------------------------- streaming: 8-bit cache
+ *
+ * Keys and values of earlier tokens, for video that is generated frame by
+ * frame, in pages of 128 tokens shared by all streams:
+ *   k8, v8           : device uint8 [n_pages][heads_kv][128][128], e4m3 values
+ *   k_scale, v_scale : device fp32 [n_pages][heads_kv], powers of two: an
+ *                      entry stands for its e4m3 value times its page's scale
+ *   table            : device int32 [batch][table_stride]: the page of tokens
+ *                      128 j .. 128 j + 127 of a stream
+ * The new tokens of the batch's streams are packed one stream after the other:
+ *   tok_start        : device int32 [batch + 1], stream b's new tokens are
+ *                      tok_start[b] .. tok_start[b+1]-1 of n (tokens behind the
+ *                      last stream belong to none)
+ *   kv_len           : device int32 [batch], tokens cached by stream b, its new
+ *                      ones included: new token i is at position
+ *                      kv_len[b] - (tok_start[b+1] - tok_start[b]) + i
+ * The lists are read on the device, so a captured graph may be replayed after
+ * they were changed; the host gives bounds (max_new: new tokens of one stream;
+ * max_kv: cached tokens of one stream). A stream whose lists do not fit (a
+ * negative or decreasing start, more than max_new or n tokens, more cached
+ * tokens than its table names) is left out and a page outside [0, n_pages) is
+ * skipped; both are reported as CALIBATT_ERR_CSR through calibatt_get_status. */
+
+/* Appends the new tokens' keys and values to the cache. Per page and head,
+ *   q = round_e4m3(x / 2^e) (to nearest, ties to even),
+ *   e = max(-117, the least integer with max |x| <= 448 * 2^e),
+ * over the page's new tokens. Where a page already holds tokens of earlier
+ * calls (the first new slot is not slot 0), its scale only grows: the larger of
+ * the two is kept and the earlier entries are re-encoded when it changes. Values that
+ * are not finite become NaN and do not count for the scale. Slots behind the
+ * last token and other pages are not written.
+ *   k, v : device bf16, token t and head h at t*token_stride + h*head_stride
+ *          (elements, multiples of 8; see calibatt_rope_fwd)
+ * kv_len[b] less than stream b's new tokens is reported like a malformed list.
+ * A page must not be written through two table entries in one call. */
+int calibatt_cache_write(const calibatt_bf16* k, int64_t k_token_stride, int64_t k_head_stride,
+                         const calibatt_bf16* v, int64_t v_token_stride, int64_t v_head_stride, int heads, int n,
+                         int d, const int32_t* tok_start, const int32_t* kv_len, int batch, int max_new,
+                         const int32_t* table, int table_stride, int n_pages, uint8_t* k8, uint8_t* v8,
+                         float* k_scale, float* v_scale, calibatt_stream_t stream);
+
+/* Device workspace bytes of calibatt_cache_attn_fwd on the current device (0:
+ * none is needed, or bad sizes). */
+size_t calibatt_cache_attn_workspace_size(int batch, int heads_q, int heads_kv, int n, int max_new, int max_kv);
+
+/* Attention of the new tokens' queries over the cache:
+ *   o = softmax(scale * q K^T) V,  lse = ln sum exp(scale * q K^T)
+ * over the cached tokens that a query sees: all kv_len[b] of its stream
+ * (causal_unit = 0), or those before the end of its own unit of causal_unit
+ * positions, floor(pos / causal_unit) (1: earlier tokens and itself; H*W: its
+ * own frame and earlier ones). A query that sees no key gives o = 0 and
+ * lse = -inf. Query head h reads key head h / (heads_q / heads_kv).
+ *   q, o : device bf16 [heads_q][n][128]; lse: device fp32 [heads_q][n] or NULL
+ *   max_kv : the bound that the workspace and the split of the cache are
+ *            planned for; longer streams are still attended to in full
+ *   ws   : device scratch of calibatt_cache_attn_workspace_size bytes, 16-byte
+ *          aligned; calls that may run at the same time need one each
+ * Rows of tokens that belong to no stream are not written. New tokens may
+ * outnumber the cached ones when causal_unit = 0. */
+int calibatt_cache_attn_fwd(const calibatt_bf16* q, int heads_q, int heads_kv, int n, int d, float scale,
+                            int causal_unit, const int32_t* tok_start, const int32_t* kv_len, int batch, int max_new,
+                            int max_kv, const int32_t* table, int table_stride, int n_pages, const uint8_t* k8,
+                            const uint8_t* v8, const float* k_scale, const float* v_scale, calibatt_bf16* o,
+                            float* lse, void* ws, size_t ws_bytes, calibatt_stream_t stream);
 
 /* ---------------------------------------------------------------- calibration */
 

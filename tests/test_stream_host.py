@@ -1,0 +1,137 @@
+"""Host-side tests of the streaming entry points: plans, sizes and refusals
+(nothing is launched: every refused call returns before it enqueues work)."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+P = ctypes.c_void_p
+FAKE, ODD = 0x10000000, 0x10000008  # never dereferenced
+OK, ARG, ALIGN, UNSUPPORTED = 0, -1, -3, -4
+
+
+@pytest.fixture(scope="module")
+def binding():
+    from calibrated_block_sparse_b200 import binding as b, build
+    build.build()
+    b.load()
+    return b
+
+
+@pytest.mark.parametrize("dims", [(44, 42, 42), (16, 0, 0), (0, 64, 64), (48, 40, 24), (2, 0, 0)])
+@pytest.mark.parametrize("ladder", ["axis", "shared"])
+def test_rope_plan_matches_the_oracle(binding, dims, ladder):
+    from oracle import stream as so
+    plan = binding.rope_plan(dims, theta=10000.0, ladder=ladder)
+    freq, axis = so.rope_frequencies(dims, 10000.0, ladder)
+    assert plan.pairs == len(freq)
+    assert list(plan.axis[:plan.pairs]) == axis.tolist()
+    np.testing.assert_allclose(np.array(plan.turns[:plan.pairs]) * 2 * np.pi, freq, rtol=4e-16 * 4)
+
+
+@pytest.mark.parametrize("dims,kw,code", [((43, 42, 42), {}, ARG), ((0, 0, 0), {}, ARG), ((64, 64, 2), {}, ARG),
+                                          ((-2, 64, 64), {}, ARG), ((44, 42, 42), {"theta": 0.0}, ARG),
+                                          ((44, 42, 42), {"theta": float("nan")}, ARG),
+                                          ((44, 42, 40), {"pairing": "halves"}, UNSUPPORTED)])
+def test_rope_plan_refusals(binding, dims, kw, code):
+    with pytest.raises(binding.CalibattError) as e:
+        binding.rope_plan(dims, **kw)
+    assert e.value.code == code
+    with pytest.raises(ValueError):
+        binding.rope_plan(pairing="neighbours")
+
+
+def _rope(binding, fn="calibatt_rope_fwd", **kw):
+    plan = kw.pop("plan", None) or binding.rope_plan()
+    a = dict(q=FAKE, qts=512, qhs=128, hq=4, k=0, kts=0, khs=0, hk=0, n=10, d=128, pos=0, H=2, W=5, start=None,
+             qo=FAKE + (1 << 24), qots=128, qohs=1280, ko=0, kots=0, kohs=0)
+    a.update(kw)
+    v = list(a.values())
+    return getattr(binding.load(), fn)(ctypes.byref(plan), *v, None)
+
+
+@pytest.mark.parametrize("fn", ["calibatt_rope_fwd", "calibatt_rope_bwd"])
+def test_rope_refusals(binding, fn):
+    call = lambda **kw: _rope(binding, fn, **kw)  # noqa: E731
+    assert call(n=0) == OK
+    assert call(d=64) == UNSUPPORTED
+    for bad in (dict(q=0), dict(qo=0), dict(hq=0), dict(n=-1), dict(H=0), dict(W=0), dict(hk=2), dict(qts=-8),
+                dict(n=1 << 40), dict(qts=1 << 60)):
+        assert call(**bad) == ARG, bad
+    for bad in (dict(q=ODD), dict(qo=ODD), dict(qts=516), dict(qohs=1284), dict(pos=FAKE + 2)):
+        assert call(**bad) == ALIGN, bad
+    # outputs that name an element twice, or that another tensor of the call overlaps
+    for bad in (dict(qots=0), dict(qohs=0), dict(qots=64), dict(qohs=1024), dict(qo=FAKE),
+                dict(qo=FAKE + 256), dict(hk=1, k=FAKE, kts=512, khs=128, ko=FAKE + (1 << 24), kots=128, kohs=1280),
+                dict(hk=1, k=FAKE + (1 << 24) + 256, kts=512, khs=128, ko=FAKE + (1 << 25), kots=128, kohs=1280)):
+        assert call(**bad) == ARG, bad
+    plan = binding.rope_plan()
+    plan.pairs = 65
+    assert call(plan=plan) == ARG
+    plan = binding.rope_plan()
+    plan.axis[3] = 3
+    assert call(plan=plan) == ARG
+    plan = binding.rope_plan(pairing="halves")
+    plan.pairs = 60
+    assert call(plan=plan) == UNSUPPORTED
+
+
+def _write(binding, **kw):
+    a = dict(k=FAKE, kts=512, khs=128, v=FAKE, vts=512, vhs=128, heads=4, n=10, d=128, start=FAKE, kv=FAKE, batch=2,
+             max_new=5, table=FAKE, ts=3, pages=9, k8=FAKE, v8=FAKE + 4096, ks=FAKE, vs=FAKE + 64)
+    a.update(kw)
+    return binding.load().calibatt_cache_write(*a.values(), None)
+
+
+def test_cache_write_refusals(binding):
+    for fine in (dict(n=0), dict(batch=0), dict(max_new=0)):
+        assert _write(binding, **fine) == OK, fine
+    assert _write(binding, d=64) == UNSUPPORTED
+    assert _write(binding, batch=70000) == UNSUPPORTED
+    for bad in (dict(k=0), dict(v=0), dict(start=0), dict(kv=0), dict(table=0), dict(k8=0), dict(v8=0), dict(ks=0),
+                dict(vs=0), dict(heads=0), dict(n=-1), dict(batch=-1), dict(max_new=-1), dict(ts=0), dict(pages=0),
+                dict(kts=-8), dict(v8=FAKE), dict(vs=FAKE)):
+        assert _write(binding, **bad) == ARG, bad
+    for bad in (dict(k=ODD), dict(v8=ODD), dict(khs=4), dict(start=FAKE + 2)):
+        assert _write(binding, **bad) == ALIGN, bad
+
+
+def _attn(binding, **kw):
+    a = dict(q=FAKE, hq=8, hk=4, n=10, d=128, scale=0.1, unit=0, start=FAKE, kv=FAKE, batch=2, max_new=5, max_kv=300,
+             table=FAKE, ts=3, pages=9, k8=FAKE, v8=FAKE, ks=FAKE, vs=FAKE, o=FAKE, lse=0, ws=0, wsb=0)
+    a.update(kw)
+    return binding.load().calibatt_cache_attn_fwd(*a.values(), None)
+
+
+def test_cache_attn_refusals(binding):
+    for fine in (dict(n=0), dict(batch=0), dict(max_new=0)):
+        assert _attn(binding, **fine) == OK, fine
+    for bad in (dict(d=64), dict(batch=70000), dict(hq=70000, hk=1)):
+        assert _attn(binding, **bad) == UNSUPPORTED, bad
+    for bad in (dict(q=0), dict(o=0), dict(hq=7), dict(hk=0), dict(n=-1), dict(scale=0.0), dict(scale=float("inf")),
+                dict(scale=float("nan")), dict(unit=-1), dict(start=0), dict(kv=0), dict(table=0), dict(k8=0),
+                dict(vs=0), dict(max_kv=-1), dict(max_new=-2), dict(ts=-1), dict(pages=-1)):
+        assert _attn(binding, **bad) == ARG, bad
+    for bad in (dict(q=ODD), dict(o=ODD), dict(k8=ODD), dict(ws=ODD), dict(lse=FAKE + 1), dict(kv=FAKE + 2)):
+        assert _attn(binding, **bad) == ALIGN, bad
+    # a split cache needs its workspace
+    need = binding.cache_attn_workspace_size(2, 8, 4, 10, 5, 100000)
+    assert need > 0
+    assert _attn(binding, max_kv=100000) == ARG
+    assert _attn(binding, max_kv=100000, ws=FAKE, wsb=need - 1) == ARG
+
+
+def test_workspace_size_of_bad_shapes_is_zero(binding):
+    for bad in ((-1, 8, 4, 10, 5, 100), (1, 8, 3, 10, 5, 100000), (1, 0, 1, 10, 5, 100000), (0, 8, 4, 0, 0, 100000)):
+        assert binding.cache_attn_workspace_size(*bad) == 0
+
+
+def test_binding_wants_cuda_tensors(binding):
+    x = torch.zeros((3, 2, 128), dtype=torch.bfloat16)
+    with pytest.raises(TypeError):
+        binding.rope_fwd(x, x, binding.rope_plan(), grid=(1, 3))
+    with pytest.raises(TypeError):
+        binding.cache_write(x, x, None, None, None, None, None, None, None)
+    with pytest.raises(TypeError):
+        binding.cache_attn_fwd(x, None, None, None, None, None, None, None)
