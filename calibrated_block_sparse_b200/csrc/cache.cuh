@@ -54,4 +54,54 @@ __device__ __forceinline__ float2 e4m3x2_to_float2(uint32_t two) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// One row's power of two: 2^-x for a largest magnitude in [2^x, 2^(x+1)).
+__device__ __forceinline__ float row_shrink(float amax) {
+  const int x = (__float_as_int(amax) >> 23) - 127;  // amax >= 0; NaN and inf: 128
+  return x >= 128 ? 1.f : __int_as_float((min(max(-x, -126), 126) + 127) << 23);
+}
+
+// Factor of a raw score, never 0 (a masked score is -inf, and -inf * 0 is NaN).
+__device__ __forceinline__ float score_factor(float row, float key_scale) {
+  const float f = row * key_scale;
+  return f == 0.f ? 1.17549435e-38f : f;
+}
+
+struct CacheAttnParams {
+  const __nv_bfloat16* q;  // [heads_q][n][128]
+  __nv_bfloat16* o;
+  float* lse;              // [heads_q][n] or NULL
+  const int32_t* tok_start;
+  const int32_t* kv_len;
+  const int32_t* table;
+  const uint8_t* k8;
+  const uint8_t* v8;
+  const float* k_scale;
+  const float* v_scale;
+  int heads_q, heads_kv, group, n, batch, max_new, table_stride, n_pages, unit;
+  int tiles;               // row tiles of a stream and key head
+  int splits;              // of a row tile's pages
+  float scale_log2;
+  float* part_o;           // [splits][heads_q][n][128]
+  float2* part_ml;         // [splits][heads_q][n]: maximum (log2 units), sum
+  int* status;
+  uint64_t wait_limit_ns;
+};
+
+// Keys that the token at position pos sees (pos may be negative).
+__device__ __forceinline__ int visible(int pos, int len, int unit) {
+  if (unit == 0) return len;
+  const int u = pos >= 0 ? pos / unit : -((unit - 1 - pos) / unit);
+  const int64_t end = (static_cast<int64_t>(u) + 1) * unit;
+  return static_cast<int>(end < 0 ? 0 : end > len ? len : end);
+}
+
+// Many query rows: tiles of 128 rows (alternate: two slots of a CTA share
+// them and take every other page) or 256 rows on the tensor core.
+int launch_cache_attn_tiles(const CacheAttnParams& p, bool alternate, cudaStream_t stream);
+
 }  // namespace calibatt

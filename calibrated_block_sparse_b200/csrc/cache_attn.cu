@@ -33,34 +33,6 @@
 namespace calibatt {
 namespace {
 
-struct CacheAttnParams {
-  const __nv_bfloat16* q;  // [heads_q][n][128]
-  __nv_bfloat16* o;
-  float* lse;              // [heads_q][n] or NULL
-  const int32_t* tok_start;
-  const int32_t* kv_len;
-  const int32_t* table;
-  const uint8_t* k8;
-  const uint8_t* v8;
-  const float* k_scale;
-  const float* v_scale;
-  int heads_q, heads_kv, group, n, batch, max_new, table_stride, n_pages, unit;
-  int tiles;               // row tiles of a stream and key head
-  int splits;
-  float scale_log2;
-  float* part_o;           // [splits][heads_q][n][128]
-  float2* part_ml;         // [splits][heads_q][n]: maximum (log2 units), sum
-  int* status;
-};
-
-// Keys that the token at position pos sees (pos may be negative).
-__device__ __forceinline__ int visible(int pos, int len, int unit) {
-  if (unit == 0) return len;
-  const int u = pos >= 0 ? pos / unit : -((unit - 1 - pos) / unit);
-  const int64_t end = (static_cast<int64_t>(u) + 1) * unit;
-  return static_cast<int>(end < 0 ? 0 : end > len ? len : end);
-}
-
 // ------------------------------------------------------------------ few rows
 constexpr int kFewRows = 16;   // rows of one mma tile
 constexpr int kFewWarps = 4;   // each takes 32 of a page's 128 keys
@@ -74,11 +46,6 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
 // Makes the NaN bytes of a word zero; nonzero if there was one.
 __device__ __forceinline__ uint32_t take_nan(uint32_t& w) {
   const uint32_t hit = e4m3_nan_bytes(w);
@@ -88,12 +55,6 @@ __device__ __forceinline__ uint32_t take_nan(uint32_t& w) {
 
 __device__ __forceinline__ uint32_t word_of(const uint4& v, int i) {
   return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
-}
-
-// One row's power of two: 2^-x for a largest magnitude in [2^x, 2^(x+1)).
-__device__ __forceinline__ float row_shrink(float amax) {
-  const int x = (__float_as_int(amax) >> 23) - 127;  // amax >= 0; NaN and inf: 128
-  return x >= 128 ? 1.f : __int_as_float((min(max(-x, -126), 126) + 127) << 23);
 }
 
 // Loads a lane's 2 x 16 channels of a query row and returns their largest magnitude.
@@ -258,7 +219,7 @@ __global__ void __launch_bounds__(kFewThreads)
       for (int nt = 0; nt < 4; ++nt) mx = fmaxf(mx, fmaxf(s[nt][2 * i], s[nt][2 * i + 1]));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      const float ck = c[i] * ks;
+      const float ck = score_factor(c[i], ks);
       const float now = fmaxf(m[i], mx * ck);
       const float use = now == -INFINITY ? 0.f : now;
       alpha[i] = ex2_approx(m[i] - use);
@@ -397,20 +358,46 @@ __global__ void __launch_bounds__(128) cache_attn_join_kernel(const __grid_const
 
 // ------------------------------------------------------------------ plan
 struct CachePlan {
+  bool few, alternate;  // the kernel for up to 16 rows; tiles of 128 rows instead of 256
   int tiles, splits;
 };
 
-// Row tiles and splits from the host's bounds: enough CTAs to fill the card
-// twice, and at least 4 pages for a split to be worth its joining.
+// Which kernel, how many row tiles, and into how many splits a tile's pages
+// are cut, from the host's bounds alone.
+// Few rows: enough CTAs to fill the card twice, and at least 4 pages for a
+// split to be worth its joining.
+// Tiles: one CTA per SM, so the splits that give the shortest schedule: waves
+// of CTAs times the pages of one (plus its start and end, about 3 pages' time),
+// plus the joining's traffic (8 bytes per output value and split; a page takes
+// a tile about 1.1 us).
 CachePlan cache_plan(int batch, int heads_q, int heads_kv, int n, int max_new, int max_kv) {
   CachePlan c;
   const int64_t rows = static_cast<int64_t>(std::min(max_new, n)) * (heads_q / heads_kv);
-  c.tiles = static_cast<int>((rows + kFewRows - 1) / kFewRows);
+  c.few = rows <= kFewRows;
+  c.alternate = rows <= 128;
+  const int tile = c.few ? kFewRows : c.alternate ? 128 : 256;
+  c.tiles = static_cast<int>((rows + tile - 1) / tile);
   const int64_t units = static_cast<int64_t>(batch) * heads_kv * c.tiles;
-  const int64_t pages = (static_cast<int64_t>(max_kv) + kPage - 1) / kPage;
-  int64_t s = (4ll * sm_count() + units - 1) / std::max<int64_t>(units, 1);
-  s = std::min(s, pages / 4);
-  c.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(s, 128)));
+  const int64_t pages = std::max<int64_t>(1, (static_cast<int64_t>(max_kv) + kPage - 1) / kPage);
+  const int sms = sm_count();
+  if (c.few) {
+    int64_t s = (4ll * sms + units - 1) / std::max<int64_t>(units, 1);
+    s = std::min(s, pages / 4);
+    c.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(s, 128)));
+    return c;
+  }
+  const double join = static_cast<double>(heads_q) * std::min<int64_t>(static_cast<int64_t>(batch) * max_new, n) *
+                      1024.0 / 6.5e12 / 1.1e-6;
+  double best = 0.0;
+  c.splits = 1;
+  for (int s = 1; s <= 64 && s <= pages; ++s) {
+    const double waves = static_cast<double>((units * s + sms - 1) / sms);
+    const double time = waves * ((pages + s - 1) / s + 3.0) + (s > 1 ? 4.0 + s * join : 0.0);
+    if (s == 1 || time < best) {
+      best = time;
+      c.splits = s;
+    }
+  }
   return c;
 }
 
@@ -495,8 +482,14 @@ int calibatt_cache_attn_fwd(const calibatt_bf16* q, int heads_q, int heads_kv, i
   p.part_ml = reinterpret_cast<float2*>(p.part_o + static_cast<int64_t>(plan.splits) * heads_q * n * 128);
   const int64_t y = static_cast<int64_t>(heads_kv) * plan.tiles;
   if (y > 65535) return CALIBATT_ERR_UNSUPPORTED;
-  cache_attn_few_kernel<<<dim3(plan.splits, static_cast<unsigned>(y), batch), kFewThreads, 0, stream>>>(p);
-  if (cudaGetLastError() != cudaSuccess) return CALIBATT_ERR_CUDA;
+  p.wait_limit_ns = wait_limit_ns();
+  if (plan.few) {
+    cache_attn_few_kernel<<<dim3(plan.splits, static_cast<unsigned>(y), batch), kFewThreads, 0, stream>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return CALIBATT_ERR_CUDA;
+  } else {
+    rc = launch_cache_attn_tiles(p, plan.alternate, stream);
+    if (rc != CALIBATT_OK) return rc;
+  }
   if (plan.splits > 1) {
     const unsigned gx = (std::min(max_new, n) + 3) / 4;
     cache_attn_join_kernel<<<dim3(gx, heads_q, batch), 128, 0, stream>>>(p);

@@ -1,0 +1,709 @@
+// Attention over the paged 8-bit cache for many query rows (more than 16 that
+// share a key head), on the sm_100a tensor core.
+//
+// CTA (512 threads, one per SM; one row tile, key head and split of the pages):
+//   warps 0-3, 4-7   softmax of slot 0 and slot 1 (thread = query row = TMEM lane)
+//   warps 8-11       converters: read a page's e4m3 tile from global memory two
+//                    tiles ahead, write it as a 16-bit operand tile into a
+//                    5-stage shared-memory ring (128-byte swizzle)
+//   warp  12         MMA issuer (one thread): S = Q K^T and O += P V
+//   warps 13-15      idle (they complete the fourth warpgroup, whose registers
+//                    go to the softmax warpgroups)
+// A slot is 128 query rows. With more than 128 rows a CTA takes 256: each
+// converted tile feeds both slots, so the conversion (on the same issue slots
+// as the softmax) is paid once per two tensor-core tiles. With at most 128 the
+// slots hold the same rows and take every other page, and are joined at the
+// end: the chain S -> softmax -> P V of one slot then runs beside the other's.
+//
+// K is converted to fp16, which holds every e4m3 value, and Q is brought to
+// fp16 by a power of two per row; the scales multiply the fp32 score. V is
+// converted to bf16 with its page's scale: a power of two times an e4m3 value
+// is a bf16 value, whatever the scale's size, so O accumulates over pages with
+// different scales. P is bf16 then, as both operands of a product have one type.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+#include <mutex>
+
+#include "cache.cuh"
+#include "calibatt.h"
+#include "kernels.h"
+#include "ptx.cuh"
+#include "sched.cuh"
+#include "softmax.cuh"
+
+namespace calibatt {
+namespace {
+
+constexpr int kTileThreads = 512;
+// registers per thread after the split; their sum must fit in the launch
+// allotment of 128 x 512 (checked against the compiled count before a launch)
+constexpr int kTileSoftmaxRegs = 184;
+constexpr int kTileConvertRegs = 96;
+constexpr int kTileControlRegs = 40;
+constexpr int kTileRegs = 256 * kTileSoftmaxRegs + 128 * kTileConvertRegs + 128 * kTileControlRegs;
+static_assert(kTileRegs <= 128 * kTileThreads, "register split");
+constexpr int kTileRing = 5;
+constexpr float kTileRescale = 8.0f;   // log2 units: move the running max only if it grows by more
+constexpr float kBigScore = 65536.0f;  // log2 units: beyond it the rounding of the row max counts
+
+struct TileBarriers {
+  uint64_t ring_full[kTileRing];
+  uint64_t ring_empty[kTileRing];
+  uint64_t q_full[2];
+  uint64_t s_full[2];
+  uint64_t p_full[2];
+  uint64_t o_full[2];
+  uint64_t mma_done;
+  uint32_t tmem_base;
+  int abort;
+  int nan_seen;       // a NaN value was taken out of a page that some rows do not see whole
+  float2 slot_ml[128];  // slot 1's maximum and sum (alternate)
+};
+
+struct TileLayout {
+  static constexpr int kQOff = 0;
+  static constexpr int kRingOff = 2 * kTile;
+  static constexpr int kBarOff = kRingOff + kTileRing * kTile;
+  static constexpr int kBytes = kBarOff + static_cast<int>(sizeof(TileBarriers));
+  static constexpr int kDynSmem = kBytes + 1024;
+};
+static_assert(TileLayout::kDynSmem <= 232448, "shared memory budget");
+
+// fp16 operands, fp32 accumulation (formats 0); P V is bf16 (kIdescPV).
+constexpr uint32_t kIdescF16 = (1u << 4) | (16u << 17) | (8u << 24);
+
+__device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+__device__ __forceinline__ void st_shared16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+// Page numbers and one scale of 32 consecutive pages of a stream, one per
+// lane, fetched a chunk of 32 ahead. A page outside the pool gets id -1.
+struct PageWindow {
+  const int32_t* table;
+  const float* scale;
+  int n_pages, heads, head, count;  // pages of the range
+  int id, id_next;
+  float sc, sc_next;
+
+  __device__ __forceinline__ void fetch(int at, int& out_id, float& out_sc, int* status) {
+    out_id = -1;
+    out_sc = 0.f;
+    if (at < count) {
+      out_id = __ldg(table + at);
+      if (out_id < 0 || out_id >= n_pages) {
+        record_error(status, CALIBATT_ERR_CSR);
+        out_id = -1;
+      } else {
+        out_sc = __ldg(scale + static_cast<int64_t>(out_id) * heads + head);
+      }
+    }
+  }
+  __device__ __forceinline__ void start(int lane, int* status) {
+    fetch(lane, id, sc, status);
+    fetch(32 + lane, id_next, sc_next, status);
+  }
+  // call before using page i = 32, 64, ...
+  __device__ __forceinline__ void advance(int i, int lane, int* status) {
+    id = id_next;
+    sc = sc_next;
+    fetch(i + 32 + lane, id_next, sc_next, status);
+  }
+};
+
+// 16 e4m3 values (ch 0..15 of a 64-channel half's quarter) as two 16-byte
+// chunks of fp16.
+__device__ __forceinline__ void store_k(uint32_t row_addr, int r, int j, const uint4& w) {
+  const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+  uint32_t h[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    h[2 * i] = e4m3x2_to_half2(x[i] & 0xffffu);
+    h[2 * i + 1] = e4m3x2_to_half2(x[i] >> 16);
+  }
+  st_shared16(row_addr + ((j ^ (r & 7)) << 4), h[0], h[1], h[2], h[3]);
+  st_shared16(row_addr + (((j + 1) ^ (r & 7)) << 4), h[4], h[5], h[6], h[7]);
+}
+
+__device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t two, float scale) {
+  const float2 f = e4m3x2_to_float2(two);
+  return pack_bf16x2(f.x * scale, f.y * scale);
+}
+
+__device__ __forceinline__ void store_v(uint32_t row_addr, int r, int j, const uint4& w, float scale) {
+  const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+  uint32_t h[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    h[2 * i] = e4m3x2_to_bf16x2(x[i] & 0xffffu, scale);
+    h[2 * i + 1] = e4m3x2_to_bf16x2(x[i] >> 16, scale);
+  }
+  st_shared16(row_addr + ((j ^ (r & 7)) << 4), h[0], h[1], h[2], h[3]);
+  st_shared16(row_addr + (((j + 1) ^ (r & 7)) << 4), h[4], h[5], h[6], h[7]);
+}
+
+// Tile t of the ring's order -> (V?, page of the range). Both slots on one
+// page: K0 V0 K1 V1 ...; alternate: K0 K1 V0 K2 V1 ... (the issuer's order).
+template <bool kAlt>
+__device__ __forceinline__ void ring_tile(int t, int np, bool& is_v, int& page) {
+  if (!kAlt) {
+    is_v = t & 1;
+    page = t >> 1;
+  } else if (t & 1) {
+    page = (t + 1) >> 1;
+    is_v = page >= np;
+    if (is_v) page = (t - 1) >> 1;
+  } else {
+    is_v = t > 0;
+    page = t > 0 ? (t >> 1) - 1 : 0;
+  }
+}
+
+template <bool SW, bool kAlt>
+__global__ void __launch_bounds__(kTileThreads, 1)
+    cache_attn_tile_kernel(const __grid_constant__ CacheAttnParams p) {
+  using L = TileLayout;
+  constexpr int kRows = kAlt ? 128 : 256;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+  const uint32_t sbase = smem_u32(smem);
+  TileBarriers& bar = *reinterpret_cast<TileBarriers*>(smem + L::kBarOff);
+  volatile int* abort_flag = &bar.abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  // ------------------------------------------------------------ the CTA's work
+  const int split = blockIdx.x;
+  const int head = blockIdx.y / p.tiles;
+  const int tile = p.tiles - 1 - static_cast<int>(blockIdx.y) % p.tiles;  // causal: most keys first
+  const int b = blockIdx.z;
+  const Stream st = stream_of(p.tok_start, p.kv_len, b, p.n, p.table_stride);
+  if (st.bad || st.n_new > p.max_new) {
+    if (threadIdx.x == 0) record_error(p.status, CALIBATT_ERR_CSR);
+    return;
+  }
+  const int rows = st.n_new * p.group;
+  const int r0 = tile * kRows;
+  if (r0 >= rows) return;
+  const int r1 = min(rows, r0 + kRows);
+  const int first_pos = st.len - st.n_new;  // position of the first new token
+  const int least = visible(first_pos + r0 / p.group, st.len, p.unit);        // keys that every row sees
+  const int most = visible(first_pos + (r1 - 1) / p.group, st.len, p.unit);   // keys that any row sees
+  const int pages = (most + kPage - 1) / kPage;
+  const int per = (pages + p.splits - 1) / p.splits;
+  const int pg0 = min(pages, split * per);
+  const int np = min(pages, pg0 + per) - pg0;
+  const bool second = kAlt ? np > 1 : r1 - r0 > 128;  // slot 1 has work
+  const int32_t* table = p.table + static_cast<int64_t>(b) * p.table_stride + pg0;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kTileRing; ++i) {
+      mbar_init(&bar.ring_full[i], 128);
+      mbar_init(&bar.ring_empty[i], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&bar.q_full[s], 128);
+      mbar_init(&bar.s_full[s], 1);
+      mbar_init(&bar.p_full[s], 128);
+      mbar_init(&bar.o_full[s], 1);
+    }
+    mbar_init(&bar.mma_done, 1);
+    bar.abort = 0;
+    bar.nan_seen = 0;
+    fence_barrier_init();
+  }
+  if (warp == 12) tmem_alloc(&bar.tmem_base, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bar.tmem_base;
+
+  if (warp >= 8 && warp < 12) {
+    // ---------------------------------------------------------- converters
+    warpgroup_regs_dec<kTileConvertRegs>();
+    bool ok = true;
+    // lanes of a store phase: two rows (one even, one odd) of four quarters
+    // of a 64-channel half, so their 16-byte chunks fall into eight banks groups
+    const int row = (warp - 8) * 8 + (lane >> 2), quarter = lane & 3;
+    PageWindow win{table, p.v_scale, p.n_pages, p.heads_kv, head, np, 0, 0, 0.f, 0.f};
+    // pages are used in order by K (ahead) and V: windows move with K, and
+    // what V needs is remembered for the pages between
+    win.start(lane, p.status);
+    const int nt = 2 * np;
+    uint4 buf[2][8];
+    float vs[2];
+    int ids[2], k_seen = 0;
+    // page id and value scale of page i: i is at most one page behind K's
+    int id_ring[4];
+    float sc_ring[4];
+    auto page_info = [&](int i, bool is_v, int& id, float& sc) {
+      if (!is_v) {
+        if (i > 0 && (i & 31) == 0) win.advance(i, lane, p.status);
+        id = __shfl_sync(0xffffffffu, win.id, i & 31);
+        sc = __shfl_sync(0xffffffffu, win.sc, i & 31);
+#pragma unroll
+        for (int e = 3; e > 0; --e) {
+          id_ring[e] = id_ring[e - 1];
+          sc_ring[e] = sc_ring[e - 1];
+        }
+        id_ring[0] = id;
+        sc_ring[0] = sc;
+        k_seen = i;
+      } else {
+        const int back = k_seen - i;  // 0, 1 or 2
+        id = back == 0 ? id_ring[0] : back == 1 ? id_ring[1] : id_ring[2];
+        sc = back == 0 ? sc_ring[0] : back == 1 ? sc_ring[1] : sc_ring[2];
+      }
+    };
+    auto load = [&](int t, uint4 (&w)[8], int& id, float& sc) {
+      bool is_v;
+      int i;
+      ring_tile<kAlt>(t, np, is_v, i);
+      page_info(i, is_v, id, sc);
+      if (id < 0) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = make_uint4(0, 0, 0, 0);
+        return;
+      }
+      const uint8_t* src = (is_v ? p.v8 : p.k8) + (static_cast<int64_t>(id) * p.heads_kv + head) * (kPage * 128) +
+                           row * 128 + quarter * 16;
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        w[e] = __ldg(reinterpret_cast<const uint4*>(src + (e >> 1) * (32 * 128) + (e & 1) * 64));
+    };
+    uint32_t stage = 0, phase = 0;
+    auto convert = [&](int t, uint4 (&w)[8], float sc) -> bool {
+      bool is_v;
+      int i;
+      ring_tile<kAlt>(t, np, is_v, i);
+      if (!mbar_wait<SW>(&bar.ring_empty[stage], phase ^ 1, abort_flag, p.status, p.wait_limit_ns)) return false;
+      const uint32_t dst = sbase + L::kRingOff + stage * kTile + row * 128;
+      if (!is_v) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) store_k(dst + (e & 1) * kHalf + (e >> 1) * (32 * 128), row, 2 * quarter, w[e]);
+      } else {
+        const int key0 = (pg0 + i) * kPage;
+        if (key0 + kPage > least) {
+          // a page that some row does not see whole: a product takes every
+          // key for every row, and 0 * NaN is NaN. Slots behind the last
+          // token become zero, and so does a NaN, which the rows that see it
+          // get back at the end.
+          uint32_t nan = 0;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int key = key0 + (e >> 1) * 32 + row;
+            uint32_t* x = reinterpret_cast<uint32_t*>(&w[e]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              if (key >= st.len) x[k] = 0;
+              const uint32_t hit = e4m3_nan_bytes(x[k]);
+              x[k] &= ~((hit >> 7) * 0xffu);
+              nan |= hit;
+            }
+          }
+          if (nan) *const_cast<volatile int*>(&bar.nan_seen) = 1;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          store_v(dst + (e & 1) * kHalf + (e >> 1) * (32 * 128), row, 2 * quarter, w[e], sc);
+      }
+      fence_proxy_async();
+      mbar_arrive(&bar.ring_full[stage]);
+      if (++stage == kTileRing) {
+        stage = 0;
+        phase ^= 1;
+      }
+      return true;
+    };
+    // the wait's outcome is made the warp's, for the shuffles that follow
+    if (nt > 0) load(0, buf[0], ids[0], vs[0]);
+    if (nt > 1) load(1, buf[1], ids[1], vs[1]);
+    for (int t = 0; t < nt && ok; t += 2) {
+      ok = __all_sync(0xffffffffu, convert(t, buf[0], vs[0]));
+      if (t + 2 < nt) load(t + 2, buf[0], ids[0], vs[0]);
+      if (t + 1 < nt && ok) {
+        ok = __all_sync(0xffffffffu, convert(t + 1, buf[1], vs[1]));
+        if (t + 3 < nt) load(t + 3, buf[1], ids[1], vs[1]);
+      }
+    }
+  } else if (warp >= 12) {
+    warpgroup_regs_dec<kTileControlRegs>();
+    if (warp == 12 && lane == 0 && np > 0) {
+      // -------------------------------------------------------- MMA issuer
+      uint32_t stage = 0, phase = 0;
+      const uint64_t qdesc0 = desc_k_base(sbase + L::kQOff);
+      const uint64_t kdesc0 = desc_k_base(sbase + L::kRingOff);
+      const uint64_t vdesc0 = desc_v_base(sbase + L::kRingOff);
+      auto ring_wait = [&]() -> bool {
+        if (!mbar_wait<SW>(&bar.ring_full[stage], phase, abort_flag, p.status, p.wait_limit_ns)) return false;
+        tc_fence_after();
+        return true;
+      };
+      auto ring_next = [&]() {
+        mma_commit(&bar.ring_empty[stage]);
+        if (++stage == kTileRing) {
+          stage = 0;
+          phase ^= 1;
+        }
+      };
+      auto issue_s = [&](int s) {
+        const uint64_t qd = qdesc0 + (kAlt ? 0 : s) * (kTile >> 4), kd = kdesc0 + stage * (kTile >> 4);
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks)
+          mma_ss(tmem + s * 128, qd + desc_k_step(ks), kd + desc_k_step(ks), kIdescF16, ks > 0);
+        mma_commit(&bar.s_full[s]);
+      };
+      auto issue_pv = [&](int s, bool first) {
+        const uint64_t vd = vdesc0 + stage * (kTile >> 4);
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks)
+          mma_ts(tmem + 256 + s * 128, tmem + s * 128 + ks * 8, vd + desc_v_step(ks), kIdescPV,
+                 (!first || ks > 0) ? 1u : 0u);
+      };
+      bool go = mbar_wait<SW>(&bar.q_full[0], 0, abort_flag, p.status, p.wait_limit_ns);
+      if constexpr (kAlt) {
+        for (int i = 0; i < 2 && i < np && go; ++i) {
+          if (!(go = ring_wait())) break;
+          issue_s(i);
+          ring_next();
+        }
+        for (int i = 0; i < np && go; ++i) {
+          const int s = i & 1;
+          if (!(go = mbar_wait<SW>(&bar.p_full[s], (i >> 1) & 1, abort_flag, p.status, p.wait_limit_ns))) break;
+          if (!(go = ring_wait())) break;
+          issue_pv(s, i < 2);
+          ring_next();
+          if (i + 2 < np) {
+            if (!(go = ring_wait())) break;
+            issue_s(s);
+            ring_next();
+          } else {
+            mma_commit(&bar.o_full[s]);
+          }
+        }
+      } else {
+        const int ns = second ? 2 : 1;
+        if (go && second) go = mbar_wait<SW>(&bar.q_full[1], 0, abort_flag, p.status, p.wait_limit_ns);
+        if (go && (go = ring_wait())) {
+          for (int s = 0; s < ns; ++s) issue_s(s);
+          ring_next();
+        }
+        for (int i = 0; i < np && go; ++i) {
+          // stage holds V of page i; K of the next page is one stage on
+          for (int s = 0; s < ns && go; ++s) {
+            if (!(go = mbar_wait<SW>(&bar.p_full[s], i & 1, abort_flag, p.status, p.wait_limit_ns))) break;
+            if (!(go = ring_wait())) break;
+            issue_pv(s, i == 0);
+            const uint32_t v_stage = stage, v_phase = phase;
+            if (i + 1 < np) {
+              if (s == ns - 1) {
+                ring_next();
+              } else if (++stage == kTileRing) {
+                stage = 0;
+                phase ^= 1;
+              }
+              if (!(go = ring_wait())) break;
+              issue_s(s);
+              if (s == ns - 1) {
+                ring_next();
+              } else {
+                stage = v_stage;
+                phase = v_phase;
+              }
+            } else {
+              mma_commit(&bar.o_full[s]);
+            }
+          }
+        }
+      }
+      // every issued MMA has finished before tensor memory is released
+      mma_commit(&bar.mma_done);
+      volatile int never = 0;
+      mbar_wait(&bar.mma_done, 0, &never, p.status);
+    }
+  } else {
+    // ---------------------------------------------------------- softmax
+    warpgroup_regs_inc<kTileSoftmaxRegs>();
+    float m_run = -INFINITY, l_run = 0.f;
+    bool ok = true;  // warp-uniform
+    const int s = warp >> 2;
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const int r = r0 + (kAlt ? 0 : s * 128) + row;
+    const bool row_valid = r < r1;
+    const int tok = row_valid ? r / p.group : 0;
+    const int64_t at = static_cast<int64_t>(head * p.group + (row_valid ? r % p.group : 0)) * p.n + st.t0 + tok;
+    // a padded row sees all keys: it is computed and not stored
+    const int limit = row_valid ? visible(first_pos + tok, st.len, p.unit) : st.len;
+    float c_row = p.scale_log2;
+    if (np > 0 && (kAlt ? s == 0 : s == 0 || second)) {
+      // the row of Q to shared memory, as fp16 times a power of two
+      uint4 w[16];
+      const uint4* src = reinterpret_cast<const uint4*>(p.q + at * 128);
+      float amax = 0.f;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        w[j] = row_valid ? __ldg(src + j) : make_uint4(0, 0, 0, 0);
+        const uint32_t x[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          amax = max3f(amax, fabsf(__uint_as_float(x[e] << 16)), fabsf(__uint_as_float(x[e] & 0xffff0000u)));
+      }
+      const float shrink = row_shrink(amax);
+      c_row = p.scale_log2 / shrink;
+      const uint32_t dst = sbase + L::kQOff + s * kTile + row * 128;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const uint32_t x[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
+        uint32_t h[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          h[e] = pack_half2(__uint_as_float(x[e] << 16) * shrink, __uint_as_float(x[e] & 0xffff0000u) * shrink);
+        st_shared16(dst + (j >> 3) * kHalf + (((j & 7) ^ (row & 7)) << 4), h[0], h[1], h[2], h[3]);
+      }
+      fence_proxy_async();
+      mbar_arrive(&bar.q_full[s]);
+    }
+    if constexpr (kAlt) {
+      // slot 1 multiplies the same rows
+      if (s == 1 && np > 0) {
+        float amax = 0.f;
+        const uint4* src = reinterpret_cast<const uint4*>(p.q + at * 128);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const uint4 v = row_valid ? __ldg(src + j) : make_uint4(0, 0, 0, 0);
+          const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            amax = max3f(amax, fabsf(__uint_as_float(x[e] << 16)), fabsf(__uint_as_float(x[e] & 0xffff0000u)));
+        }
+        c_row = p.scale_log2 / row_shrink(amax);
+      }
+    }
+    auto wait_warp = [&](uint64_t* bb, uint32_t parity) -> bool {
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait<SW>(bb, parity, abort_flag, p.status, p.wait_limit_ns));
+      return ok;
+    };
+    const bool active = s == 0 || second;
+    if (active && np > 0) {
+      PageWindow win{table, p.k_scale, p.n_pages, p.heads_kv, head, np, 0, 0, 0.f, 0.f};
+      win.start(lane, p.status);
+      int turn = 0;  // pages this slot has taken
+      for (int i = kAlt ? s : 0; i < np; i += kAlt ? 2 : 1, ++turn) {
+        if (i >= 32 && (i & 31) < (kAlt ? 2 : 1)) win.advance(i & ~31, lane, p.status);
+        const int id = __shfl_sync(0xffffffffu, win.id, i & 31);
+        const float ck = score_factor(c_row, __shfl_sync(0xffffffffu, win.sc, i & 31));
+        if (!wait_warp(&bar.s_full[s], turn & 1)) break;
+        tc_fence_after();
+        const int key0 = (pg0 + i) * kPage;
+        const int cut = id < 0 ? 0 : min(limit - key0, kPage);  // keys of the page that the row sees
+        const bool masked = __any_sync(0xffffffffu, cut < kPage);
+        const uint32_t sc = tmem + lane_off + s * 128;
+        float sv[64];
+        // the second half first: P overwrites the first half's columns only
+        tmem_ld64_wait(sc + 64, sv);
+        if (masked) {
+#pragma unroll
+          for (int e = 0; e < 64; ++e)
+            if (64 + e >= cut) sv[e] = -INFINITY;
+        }
+        float mx = row_max64(sv);
+        tmem_ld64_wait(sc, sv);
+        if (masked) {
+#pragma unroll
+          for (int e = 0; e < 64; ++e)
+            if (e >= cut) sv[e] = -INFINITY;
+        }
+        mx = fmaxf(mx, row_max64(sv));
+        const float page_max = mx * ck;
+        const float m_new = fmaxf(m_run, page_max);
+        // keep a stale running max unless it grew by more than the threshold
+        const bool need = m_run == -INFINITY || m_new > m_run + kTileRescale;
+        const float m_prev = m_run;
+        if (need) m_run = m_new;
+        const float m_use = m_run == -INFINITY ? 0.f : m_run;
+        const float alpha = need ? ex2_approx(m_prev - m_use) : 1.f;
+        // exponent s * ck - m; for very large scores relative to the page's
+        // own maximum first, whose rounding would otherwise stay in it
+        const bool big = __any_sync(0xffffffffu, fabsf(m_use) > kBigScore);
+        const float mx0 = mx == -INFINITY ? 0.f : mx;
+        const float mul = big ? 1.f : ck, add = big ? page_max - m_use : -m_use;
+        const float2 c2 = make_float2(mul, mul), n2 = make_float2(add, add);
+        float2 a4[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (h == 1) {
+            tmem_ld64_wait(sc + 64, sv);
+            if (masked) {
+#pragma unroll
+              for (int e = 0; e < 64; ++e)
+                if (64 + e >= cut) sv[e] = -INFINITY;
+            }
+          }
+          if (big) {
+#pragma unroll
+            for (int e = 0; e < 64; ++e) sv[e] = (sv[e] - mx0) * ck;
+          }
+          uint32_t pk[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const float2 x = exp2_mufu2(ffma2(make_float2(sv[2 * e], sv[2 * e + 1]), c2, n2));
+            a4[e & 3] = fadd2(a4[e & 3], x);
+            pk[e] = pack_bf16x2(x.x, x.y);
+          }
+          tmem_st32(sc + h * 32, pk);
+        }
+        const float2 s01 = fadd2(a4[0], a4[1]), s23 = fadd2(a4[2], a4[3]);
+        l_run = l_run * alpha + ((s01.x + s01.y) + (s23.x + s23.y));
+        // O's product with the page before is complete: the commit that
+        // signalled S tracks every earlier MMA
+        if (turn > 0 && __any_sync(0xffffffffu, need)) {
+#pragma unroll
+          for (int cc = 0; cc < 4; ++cc) {
+            uint32_t o[32];
+            tmem_ld32_wait(tmem + lane_off + 256 + s * 128 + cc * 32, o);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+            tmem_st32(tmem + lane_off + 256 + s * 128 + cc * 32, o);
+          }
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&bar.p_full[s]);
+      }
+      wait_warp(&bar.o_full[s], 0);
+      // the ring is about to be reused: the other slot's products must be done too
+      if (kAlt && second) wait_warp(&bar.o_full[s ^ 1], 0);
+      tc_fence_after();
+    }
+
+    // ---------------------------------------------------------- results
+    const bool done = ok && *abort_flag == 0;
+    float f0 = 1.f, f1 = 0.f;
+    // alternate: slot 1 hands its rows to slot 0 through the ring's memory,
+    // [channel][row], which every MMA has finished reading
+    float* joined = reinterpret_cast<float*>(smem + L::kRingOff);
+    if constexpr (kAlt) {
+      if (s == 1 && second && done) {
+        bar.slot_ml[row] = make_float2(m_run, l_run);
+#pragma unroll
+        for (int cc = 0; cc < 4; ++cc) {
+          uint32_t o[32];
+          tmem_ld32_wait(tmem + lane_off + 256 + 128 + cc * 32, o);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) joined[(cc * 32 + e) * 128 + row] = __uint_as_float(o[e]);
+        }
+      }
+      named_bar_sync(1, 256);
+      if (s == 0 && second && done) {
+        const float2 o = bar.slot_ml[row];
+        const float mx = fmaxf(m_run, o.x);
+        const float use = mx == -INFINITY ? 0.f : mx;
+        f0 = ex2_approx(m_run - use);
+        f1 = ex2_approx(o.x - use);
+        l_run = l_run * f0 + o.y * f1;
+        m_run = mx;
+      }
+    }
+    if (done && (kAlt ? s == 0 : active)) {
+      const bool some = np > 0 && l_run != 0.f;
+      const float inv = some ? 1.f / l_run : 0.f;
+      const int64_t pt = static_cast<int64_t>(split) * p.heads_q * p.n + at;
+      if (row_valid) {
+        if (p.splits > 1)
+          p.part_ml[pt] = make_float2(m_run, some ? l_run : 0.f);
+        else if (p.lse)
+          p.lse[at] = some ? (m_run + log2f(l_run)) * kLn2 : -INFINITY;
+      }
+      const bool patch = *const_cast<volatile int*>(&bar.nan_seen) != 0;
+#pragma unroll 1
+      for (int cc = 0; cc < 4; ++cc) {
+        uint32_t o[32];
+        if (np > 0) {
+          tmem_ld32_wait(tmem + lane_off + 256 + s * 128 + cc * 32, o);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = 0;
+        }
+        if (kAlt && second) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            o[e] = __float_as_uint(__uint_as_float(o[e]) * f0 + joined[(cc * 32 + e) * 128 + row] * f1);
+        }
+        if (patch && row_valid) {
+          // NaN values that were taken out of pages that not every row sees whole
+          uint32_t bad = 0;
+          for (int key = max(least / kPage, pg0) * kPage; key < min(limit, (pg0 + np) * kPage); ++key) {
+            const int id = __ldg(table + key / kPage - pg0);
+            if (id < 0 || id >= p.n_pages) continue;
+            const uint8_t* v = p.v8 + ((static_cast<int64_t>(id) * p.heads_kv + head) * kPage + key % kPage) * 128;
+            for (int e = 0; e < 32; ++e)
+              if ((v[cc * 32 + e] & 0x7f) == 0x7f) bad |= 1u << e;
+          }
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (bad >> e & 1) o[e] = 0x7fffffffu;
+        }
+        if (!row_valid) continue;
+        if (p.splits > 1) {
+          if (some) {
+            uint4* dst = reinterpret_cast<uint4*>(p.part_o + pt * 128 + cc * 32);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) dst[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          }
+        } else {
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            pk[e] = some ? pack_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv) : 0u;
+          store_row_chunk(p.o + at * 128 + cc * 32, pk);
+        }
+      }
+    }
+  }
+
+  // ------------------------------------------------------------ teardown
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 12) {
+    __syncwarp();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <bool SW, bool kAlt>
+int launch(const CacheAttnParams& p, const dim3& grid, cudaStream_t stream) {
+  static PerDeviceOnce once;
+  const int rc = set_max_smem_once(reinterpret_cast<const void*>(cache_attn_tile_kernel<SW, kAlt>),
+                                   TileLayout::kDynSmem, once);
+  if (rc != CALIBATT_OK) return rc;
+  // the register split needs the allotment it was sized for
+  static std::once_flag regs_once;
+  static int launch_regs = 0;
+  std::call_once(regs_once, [] {
+    cudaFuncAttributes fa;
+    if (cudaFuncGetAttributes(&fa, cache_attn_tile_kernel<SW, kAlt>) == cudaSuccess) launch_regs = fa.numRegs;
+  });
+  if (launch_regs * kTileThreads < kTileRegs) return CALIBATT_ERR_CUDA;
+  cache_attn_tile_kernel<SW, kAlt><<<grid, kTileThreads, TileLayout::kDynSmem, stream>>>(p);
+  return cudaGetLastError() == cudaSuccess ? CALIBATT_OK : CALIBATT_ERR_CUDA;
+}
+
+}  // namespace
+
+int launch_cache_attn_tiles(const CacheAttnParams& p, bool alternate, cudaStream_t stream) {
+  const dim3 grid(p.splits, static_cast<unsigned>(p.heads_kv) * p.tiles, p.batch);
+  const bool short_waits = p.wait_limit_ns < kShortWaitNs;
+  if (alternate)
+    return short_waits ? launch<true, true>(p, grid, stream) : launch<false, true>(p, grid, stream);
+  return short_waits ? launch<true, false>(p, grid, stream) : launch<false, false>(p, grid, stream);
+}
+
+}  // namespace calibatt
