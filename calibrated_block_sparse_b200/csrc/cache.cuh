@@ -100,6 +100,18 @@ __device__ __forceinline__ int visible(int pos, int len, int unit) {
   return static_cast<int>(end < 0 ? 0 : end > len ? len : end);
 }
 
+// Few query rows (up to 16 that share a key head): the streams' pages, key
+// head by key head, cut into equal shares for `ctas` CTAs; or, with `whole`, a
+// CTA for each key head of each stream.
+constexpr int kFewRows = 16;
+struct FewPlan {
+  bool whole;
+  int ctas;
+};
+FewPlan few_plan(int batch, int heads_kv, int64_t pages, int sms);
+size_t few_workspace_bytes(const FewPlan& plan);
+int launch_cache_attn_few(const CacheAttnParams& p, const FewPlan& plan, void* ws, cudaStream_t stream);
+
 // Many query rows: tiles of 128 rows (alternate: two slots of a CTA share
 // them and take every other page) or 256 rows on the tensor core.
 int launch_cache_attn_tiles(const CacheAttnParams& p, bool alternate, cudaStream_t stream);
