@@ -764,90 +764,100 @@ def rope_plan(dims=(44, 42, 42), theta=10000.0, pairing="interleaved", ladder="a
     return plan
 
 
-def _rows(t, name, dev=None):
-    """A bf16 CUDA tensor of three dimensions with 128 contiguous channels; its strides may be any."""
-    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == torch.bfloat16):
-        raise TypeError(f"{name} must be a CUDA {torch.bfloat16} tensor")
-    if t.dim() != 3 or t.shape[2] != HEAD_DIM or t.stride(2) != 1:
+# The streaming calls are made per layer and frame, or per token, so their
+# checks are kept to a few attribute reads per tensor.
+
+def _refuse(t, name, dtype, index, contiguous=True):
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype and (not contiguous or t.is_contiguous()):
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{index}")
+    raise TypeError(f"{name} must be a {'contiguous ' if contiguous else ''}CUDA {dtype} tensor")
+
+
+def _want(t, dtype, name, index):
+    """A contiguous tensor of this type on device `index`."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != index or t.dtype is not dtype or not t.is_contiguous():
+        _refuse(t, name, dtype, index)
+
+
+def _want_rows(t, name, index=None):
+    """Shape and strides of a bf16 CUDA tensor of three dimensions with 128 contiguous channels."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16 or not t.is_cuda or \
+            (index is not None and t.get_device() != index):
+        _refuse(t, name, torch.bfloat16, index, contiguous=False)
+    shape, strides = t.shape, t.stride()
+    if len(shape) != 3 or shape[2] != HEAD_DIM or strides[2] != 1:
         raise ValueError(f"{name} must be three-dimensional with {HEAD_DIM} contiguous channels")
-    if dev is not None and t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, not on {dev}")
-    return t
+    return shape, strides
 
 
-def _on_device(t, dtype, name, dev):
-    _cuda_tensor(t, dtype, name)
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, not on {dev}")
-    return t
+def _raw_stream(stream, index):
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
-class _Device:
-    """Makes `dev` the current device for a call (a no-op when it already is)."""
-    __slots__ = ("dev", "prev")
-
-    def __init__(self, dev):
-        self.dev = dev.index
-
-    def __enter__(self):
-        self.prev = torch.cuda.current_device()
-        if self.prev != self.dev:
-            torch.cuda.set_device(self.dev)
-
-    def __exit__(self, *exc):
-        if self.prev != self.dev:
-            torch.cuda.set_device(self.prev)
-
-
-def _new(shape, dtype, dev, stream):
+def _new(like, shape, dtype, stream):
     """A tensor of the stream's own memory pool: an allocation on the current
     stream could still be in use there when another stream writes it."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return like.new_empty(shape, dtype=dtype)
 
 
-def _rope(what, forward, q, k, plan, grid, start, pos, q_out, k_out, stream):
-    # forward: token-major in, head-major out; gradient: the other way round
-    dev = _rows(q, "q").device
-    tok = 0 if forward else 1
-    n = q.shape[tok]
-    args = []
-    outs = [q_out, k_out]
-    for i, (x, name) in enumerate(((q, "q"), (k, "k"))):
-        if x is None:
-            if outs[i] is not None:
-                raise ValueError(f"{name}_out without {name}")
-            args.append((None, 0, 0, 0, None, 0, 0))
-            continue
-        _rows(x, name, dev)
-        heads = x.shape[1 - tok]
-        if x.shape[tok] != n:
-            raise ValueError(f"{name} has {x.shape[tok]} tokens, q has {n}")
-        shape = (heads, n, HEAD_DIM) if forward else (n, heads, HEAD_DIM)
-        if outs[i] is None:
-            outs[i] = _new(shape, torch.bfloat16, dev, stream)
-        out = _rows(outs[i], f"{name}_out", dev)
-        if tuple(out.shape) != shape:
-            raise ValueError(f"{name}_out must be {list(shape)}")
-        args.append((x.data_ptr(), x.stride(tok), x.stride(1 - tok), heads, out.data_ptr(), out.stride(1 - tok),
-                     out.stride(tok)))
+_NO_ROWS = (None, 0, 0, 0)
+
+
+def _rope(fn, tok, q, k, plan, grid, start, pos, q_out, k_out, stream):
+    # tok: the token dimension of the inputs (0: rotation, 1: gradient); the outputs have it in the other place
+    if not isinstance(q, torch.Tensor):
+        _refuse(q, "q", torch.bfloat16, None, contiguous=False)
+    index = q.get_device()
+    if index >= 0 and torch.cuda.current_device() != index:
+        with torch.cuda.device(index):
+            return _rope(fn, tok, q, k, plan, grid, start, pos, q_out, k_out, stream)
+    hd = 1 - tok
+    shape, st = _want_rows(q, "q")
+    n, heads = shape[tok], shape[hd]
+    a = (q.data_ptr(), st[tok], st[hd], heads)
+    out_shape = (n, heads, HEAD_DIM) if tok else (heads, n, HEAD_DIM)
+    if q_out is None:
+        q_out = _new(q, out_shape, torch.bfloat16, stream)
+    shape, st = _want_rows(q_out, "q_out", index)
+    if shape != out_shape:
+        raise ValueError(f"q_out must be {list(out_shape)}")
+    a_out = (q_out.data_ptr(), st[hd], st[tok])
+    b, b_out = _NO_ROWS, _NO_ROWS[:3]
+    if k is not None:
+        shape, st = _want_rows(k, "k", index)
+        if shape[tok] != n:
+            raise ValueError(f"k has {shape[tok]} tokens, q has {n}")
+        heads = shape[hd]
+        b = (k.data_ptr(), st[tok], st[hd], heads)
+        out_shape = (n, heads, HEAD_DIM) if tok else (heads, n, HEAD_DIM)
+        if k_out is None:
+            k_out = _new(k, out_shape, torch.bfloat16, stream)
+        shape, st = _want_rows(k_out, "k_out", index)
+        if shape != out_shape:
+            raise ValueError(f"k_out must be {list(out_shape)}")
+        b_out = (k_out.data_ptr(), st[hd], st[tok])
+    elif k_out is not None:
+        raise ValueError("k_out without k")
     if (grid is None) == (pos is None):
         raise ValueError("give the positions as a grid (H, W) or as a tensor pos [n][3]")
-    H, W = (0, 0) if grid is None else (int(grid[0]), int(grid[1]))
-    if pos is not None:
-        _on_device(pos, torch.int32, "pos", dev)
-        if tuple(pos.shape) != (n, 3):
+    if pos is None:
+        H, W = grid
+        at = (ctypes.c_int32 * 3)(*start)
+        rc = getattr(load(), fn)(ctypes.byref(plan), *a, *b, n, HEAD_DIM, None, int(H), int(W), at, *a_out, *b_out,
+                                 _raw_stream(stream, index))
+    else:
+        _want(pos, torch.int32, "pos", index)
+        if pos.shape != (n, 3):
             raise ValueError(f"pos must be [{n}][3]")
-    st = (ctypes.c_int32 * 3)(*[int(x) for x in start])
-    a, b = args
-    with _Device(dev):
-        rc = getattr(load(), what)(ctypes.byref(plan), a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3], n, HEAD_DIM,
-                                   None if pos is None else pos.data_ptr(), H, W, st, a[4], a[5], a[6], b[4], b[5],
-                                   b[6], _stream(stream))
-    _check(rc, what)
-    return outs[0], outs[1]
+        rc = getattr(load(), fn)(ctypes.byref(plan), *a, *b, n, HEAD_DIM, pos.data_ptr(), 0, 0, None, *a_out, *b_out,
+                                 _raw_stream(stream, index))
+    _check(rc, fn)
+    return q_out, k_out
 
 
 def rope_fwd(q, k, plan, grid=None, start=(0, 0, 0), pos=None, q_out=None, k_out=None, stream=None):
@@ -855,56 +865,63 @@ def rope_fwd(q, k, plan, grid=None, start=(0, 0, 0), pos=None, q_out=None, k_out
     any strides by their positions: a grid (H, W) whose first token is at
     `start` (time, height, width), or pos, int32 [n][3]. Returns them as
     [heads][n][128], the layout of the attention calls."""
-    return _rope("calibatt_rope_fwd", True, q, k, plan, grid, start, pos, q_out, k_out, stream)
+    return _rope("calibatt_rope_fwd", 0, q, k, plan, grid, start, pos, q_out, k_out, stream)
 
 
 def rope_bwd(dq_out, dk_out, plan, grid=None, start=(0, 0, 0), pos=None, dq=None, dk=None, stream=None):
     """Gradients of rope_fwd's inputs, [n][heads][128], from those of its
     outputs, [heads][n][128] of any strides (expanded ones too)."""
-    return _rope("calibatt_rope_bwd", False, dq_out, dk_out, plan, grid, start, pos, dq, dk, stream)
+    return _rope("calibatt_rope_bwd", 1, dq_out, dk_out, plan, grid, start, pos, dq, dk, stream)
 
 
 # ------------------------------------------------------------------ streaming: 8-bit cache
 
-def _cache_args(k8, v8, k_scale, v_scale, tok_start, kv_len, table, dev):
+_PAGE_TYPES = (torch.float8_e4m3fn, torch.uint8)
+
+
+def _cache_args(k8, v8, k_scale, v_scale, tok_start, kv_len, table, index):
+    """Checks the cache's tensors; pages, heads, batch, table width."""
     for t, name in ((k8, "k8"), (v8, "v8")):
-        if not (isinstance(t, torch.Tensor) and t.dtype in (torch.float8_e4m3fn, torch.uint8)):
-            raise TypeError(f"{name} must be a contiguous CUDA float8_e4m3fn (or uint8) tensor")
-        _on_device(t, t.dtype, name, dev)
-        if t.dim() != 4 or t.shape[2:] != (BLOCK, HEAD_DIM):
-            raise ValueError(f"{name} must be [pages][heads][{BLOCK}][{HEAD_DIM}]")
-    if v8.shape != k8.shape:
-        raise ValueError("k8 and v8 differ in shape")
-    for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-        _on_device(t, torch.float32, name, dev)
-        if t.shape != k8.shape[:2]:
-            raise ValueError(f"{name} must be [pages][heads]")
-    for t, name in ((tok_start, "tok_start"), (kv_len, "kv_len"), (table, "table")):
-        _on_device(t, torch.int32, name, dev)
-    batch = kv_len.numel()
-    if tok_start.numel() != batch + 1 or table.dim() != 2 or table.shape[0] != batch:
+        if not isinstance(t, torch.Tensor) or t.get_device() != index or t.dtype not in _PAGE_TYPES or \
+                not t.is_contiguous():
+            _refuse(t, name, torch.float8_e4m3fn, index)
+    shape = k8.shape
+    if len(shape) != 4 or shape[2] != BLOCK or shape[3] != HEAD_DIM or v8.shape != shape:
+        raise ValueError(f"k8 and v8 must be [pages][heads][{BLOCK}][{HEAD_DIM}]")
+    scales = shape[:2]
+    _want(k_scale, torch.float32, "k_scale", index)
+    _want(v_scale, torch.float32, "v_scale", index)
+    if k_scale.shape != scales or v_scale.shape != scales:
+        raise ValueError("k_scale and v_scale must be [pages][heads]")
+    _want(tok_start, torch.int32, "tok_start", index)
+    _want(kv_len, torch.int32, "kv_len", index)
+    _want(table, torch.int32, "table", index)
+    batch, rows = kv_len.numel(), table.shape
+    if tok_start.numel() != batch + 1 or len(rows) != 2 or rows[0] != batch:
         raise ValueError("tok_start must be [batch + 1], kv_len [batch], table [batch][pages of a stream]")
-    return batch
+    return shape[0], shape[1], batch, rows[1]
 
 
 def cache_write(k, v, k8, v8, k_scale, v_scale, tok_start, kv_len, table, max_new=None, stream=None):
     """Appends keys and values [n][heads][128] (any strides) of the batch's new
     tokens to the paged 8-bit cache (calibatt_cache_write). max_new: the most
     new tokens of one stream (default: n)."""
-    dev = _rows(k, "k").device
-    _rows(v, "v", dev)
-    n, heads = k.shape[0], k.shape[1]
-    if v.shape != k.shape:
+    shape, ks = _want_rows(k, "k")
+    index = k.get_device()
+    if torch.cuda.current_device() != index:
+        with torch.cuda.device(index):
+            return cache_write(k, v, k8, v8, k_scale, v_scale, tok_start, kv_len, table, max_new, stream)
+    v_shape, vs = _want_rows(v, "v", index)
+    if v_shape != shape:
         raise ValueError("k and v differ in shape")
-    batch = _cache_args(k8, v8, k_scale, v_scale, tok_start, kv_len, table, dev)
-    if k8.shape[1] != heads:
-        raise ValueError(f"the cache has {k8.shape[1]} heads, k has {heads}")
-    with _Device(dev):
-        rc = load().calibatt_cache_write(k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0),
-                                         v.stride(1), heads, n, HEAD_DIM, tok_start.data_ptr(), kv_len.data_ptr(),
-                                         batch, n if max_new is None else int(max_new), table.data_ptr(),
-                                         table.shape[1], k8.shape[0], k8.data_ptr(), v8.data_ptr(),
-                                         k_scale.data_ptr(), v_scale.data_ptr(), _stream(stream))
+    n, heads = shape[0], shape[1]
+    pages, cache_heads, batch, width = _cache_args(k8, v8, k_scale, v_scale, tok_start, kv_len, table, index)
+    if cache_heads != heads:
+        raise ValueError(f"the cache has {cache_heads} heads, k has {heads}")
+    rc = load().calibatt_cache_write(k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], heads, n, HEAD_DIM,
+                                     tok_start.data_ptr(), kv_len.data_ptr(), batch, n if max_new is None else max_new,
+                                     table.data_ptr(), width, pages, k8.data_ptr(), v8.data_ptr(), k_scale.data_ptr(),
+                                     v_scale.data_ptr(), _raw_stream(stream, index))
     _check(rc, "calibatt_cache_write")
 
 
@@ -916,7 +933,7 @@ def cache_attn_workspace_size(batch, heads_q, heads_kv, n, max_new, max_kv) -> i
 def cache_attn_workspace(q, k8, table, max_new=None, max_kv=None):
     """Workspace of cache_attn_fwd for these tensors (None when none is needed)."""
     heads_q, n = _bhnd(q)
-    with _Device(q.device):
+    with torch.cuda.device(q.device):
         need = cache_attn_workspace_size(table.shape[0], heads_q, k8.shape[1], n, n if max_new is None else max_new,
                                          table.shape[1] * BLOCK if max_kv is None else max_kv)
     return torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
@@ -928,40 +945,50 @@ def cache_attn_fwd(q, k8, v8, k_scale, v_scale, tok_start, kv_len, table, max_ne
     8-bit cache (calibatt_cache_attn_fwd); returns (o, lse). Rows of tokens
     that belong to no stream keep what o and lse hold. max_new, max_kv: the
     most new and cached tokens of one stream (default: n, the table's width)."""
+    if not isinstance(q, torch.Tensor):
+        _refuse(q, "q", torch.bfloat16, None)
+    index = q.get_device()
+    if index >= 0 and torch.cuda.current_device() != index:
+        with torch.cuda.device(index):
+            return cache_attn_fwd(q, k8, v8, k_scale, v_scale, tok_start, kv_len, table, max_new, max_kv, causal_unit,
+                                  o, lse, ws, scale, want_lse, stream)
     heads_q, n = _bhnd(q)
-    dev = q.device
-    batch = _cache_args(k8, v8, k_scale, v_scale, tok_start, kv_len, table, dev)
-    heads_kv = k8.shape[1]
+    pages, heads_kv, batch, width = _cache_args(k8, v8, k_scale, v_scale, tok_start, kv_len, table, index)
     if heads_kv < 1 or heads_q % heads_kv:
         raise ValueError(f"{heads_q} query heads do not share {heads_kv} key heads evenly")
     if o is None:
-        o = _new(q.shape, torch.bfloat16, dev, stream)
+        o = torch.empty_like(q) if stream is None else _new(q, q.shape, torch.bfloat16, stream)
     else:
-        _on_device(o, torch.bfloat16, "o", dev)
+        _want(o, torch.bfloat16, "o", index)
         if o.shape != q.shape:
             raise ValueError("o and q differ in shape")
-    if lse is None and want_lse:
-        lse = _new((heads_q, n), torch.float32, dev, stream)
-    elif lse is not None:
-        _on_device(lse, torch.float32, "lse", dev)
+    if lse is not None:
+        _want(lse, torch.float32, "lse", index)
         if lse.shape != (heads_q, n):
             raise ValueError(f"lse must be [{heads_q}][{n}]")
-    max_new = n if max_new is None else int(max_new)
-    max_kv = table.shape[1] * BLOCK if max_kv is None else int(max_kv)
-    scale = 1.0 / math.sqrt(HEAD_DIM) if scale is None else float(scale)
+    elif want_lse:
+        lse = _new(q, (heads_q, n), torch.float32, stream)
+    if max_new is None:
+        max_new = n
+    if max_kv is None:
+        max_kv = width * BLOCK
     lib = load()
-    with _Device(dev):
-        if ws is None:
-            need = lib.calibatt_cache_attn_workspace_size(batch, heads_q, heads_kv, n, max_new, max_kv)
-            ws = _new(need, torch.uint8, dev, stream) if need else None
-        else:
-            _on_device(ws, torch.uint8, "ws", dev)
-        rc = lib.calibatt_cache_attn_fwd(q.data_ptr(), heads_q, heads_kv, n, HEAD_DIM, scale, int(causal_unit),
-                                         tok_start.data_ptr(), kv_len.data_ptr(), batch, max_new, max_kv,
-                                         table.data_ptr(), table.shape[1], k8.shape[0], k8.data_ptr(), v8.data_ptr(),
-                                         k_scale.data_ptr(), v_scale.data_ptr(), o.data_ptr(),
-                                         None if lse is None else lse.data_ptr(),
-                                         None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(),
-                                         _stream(stream))
+    ws_bytes = 0
+    if ws is not None:
+        _want(ws, torch.uint8, "ws", index)
+        ws_bytes = ws.numel()
+    else:
+        ws_bytes = lib.calibatt_cache_attn_workspace_size(batch, heads_q, heads_kv, n, max_new, max_kv)
+        if ws_bytes:
+            ws = _new(q, (ws_bytes,), torch.uint8, stream)
+    rc = lib.calibatt_cache_attn_fwd(q.data_ptr(), heads_q, heads_kv, n, HEAD_DIM,
+                                     _SCALE if scale is None else scale, causal_unit, tok_start.data_ptr(),
+                                     kv_len.data_ptr(), batch, max_new, max_kv, table.data_ptr(), width, pages,
+                                     k8.data_ptr(), v8.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                                     o.data_ptr(), None if lse is None else lse.data_ptr(),
+                                     None if ws is None else ws.data_ptr(), ws_bytes, _raw_stream(stream, index))
     _check(rc, "calibatt_cache_attn_fwd")
     return o, lse
+
+
+_SCALE = 1.0 / math.sqrt(HEAD_DIM)
