@@ -47,12 +47,26 @@ struct WriteParams {
   int* status;
 };
 
-// Two fp32 values to packed e4m3, round to nearest even; what is not finite
-// becomes NaN (the conversion alone would turn an infinity into 448).
+// Two fp32 values to packed e4m3, round to nearest even. With kFinite false
+// what is not finite becomes NaN (the conversion alone would turn an infinity
+// into 448).
+template <bool kFinite>
 __device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
-  lo = fabsf(lo) <= 3.4028235e38f ? lo : __int_as_float(0x7fffffff);
-  hi = fabsf(hi) <= 3.4028235e38f ? hi : __int_as_float(0x7fffffff);
+  if (!kFinite) {
+    lo = fabsf(lo) <= 3.4028235e38f ? lo : __int_as_float(0x7fffffff);
+    hi = fabsf(hi) <= 3.4028235e38f ? hi : __int_as_float(0x7fffffff);
+  }
   return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+}
+
+template <bool kFinite>
+__device__ __forceinline__ uint2 to_e4m3x8(const uint4& v, float inv) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t q[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    q[j] = to_e4m3x2<kFinite>(__uint_as_float(w[j] << 16) * inv, __uint_as_float(w[j] & 0xffff0000u) * inv);
+  return make_uint2(q[0] | q[1] << 16, q[2] | q[3] << 16);
 }
 
 // The least exponent e >= kMinExp with a <= 448 * 2^e (a >= 0, finite).
@@ -65,7 +79,7 @@ __device__ __forceinline__ int page_exponent(float a) {
 
 __device__ __forceinline__ float exp2_int(int e) { return __int_as_float((e + 127) << 23); }
 
-__global__ void __launch_bounds__(kWriteThreads) cache_write_kernel(const __grid_constant__ WriteParams p) {
+__global__ void __launch_bounds__(kWriteThreads, 4) cache_write_kernel(const __grid_constant__ WriteParams p) {
   const int which = blockIdx.x & 1, head = blockIdx.x >> 1;
   const int b = blockIdx.z;
   const Stream st = stream_of(p.tok_start, p.kv_len, b, p.n, p.table_stride);
@@ -88,8 +102,11 @@ __global__ void __launch_bounds__(kWriteThreads) cache_write_kernel(const __grid
   const __nv_bfloat16* x = p.x[which] + head * p.hs[which] + chunk * 8;
   const int64_t ts = p.ts[which];
 
+  // The largest magnitude, as the bit pattern of a bf16 value without its sign
+  // (they are ordered like the values). 0x7f80 and more is not finite: then,
+  // rarely, the page is looked through again without those.
   uint4 v[kPasses];
-  float amax = 0.f;
+  uint32_t top = 0;  // two 16-bit maxima
 #pragma unroll
   for (int i = 0; i < kPasses; ++i) {
     const int r = row0 + i * kRowsPerPass;
@@ -98,42 +115,53 @@ __global__ void __launch_bounds__(kWriteThreads) cache_write_kernel(const __grid
   }
 #pragma unroll
   for (int i = 0; i < kPasses; ++i) {
-    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float a = fabsf(__uint_as_float(w[j] << 16)), c = fabsf(__uint_as_float(w[j] & 0xffff0000u));
-      if (a <= 3.4028235e38f) amax = fmaxf(amax, a);
-      if (c <= 3.4028235e38f) amax = fmaxf(amax, c);
-    }
+    top = __vmaxu2(top, __vmaxu2(v[i].x & 0x7fff7fffu, v[i].y & 0x7fff7fffu));
+    top = __vmaxu2(top, __vmaxu2(v[i].z & 0x7fff7fffu, v[i].w & 0x7fff7fffu));
   }
-  __shared__ float part[kWriteThreads / 32];
+  __shared__ uint32_t part[2][kWriteThreads / 32];
+  auto block_max = [&](uint32_t t, uint32_t* at) {
+    t = max(t & 0xffffu, t >> 16);
+    t = __reduce_max_sync(0xffffffffu, t);
+    if ((threadIdx.x & 31) == 0) at[threadIdx.x >> 5] = t;
+    __syncthreads();
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = amax;
+    for (int i = 0; i < kWriteThreads / 32; ++i) t = max(t, at[i]);
+    return t;
+  };
   // the page's scale is read by every thread before thread 0 replaces it
   float* scale = p.scale[which] + static_cast<int64_t>(page) * p.heads + head;
   const float old = lo > 0 ? *scale : 0.f;
-  __syncthreads();
+  top = block_max(top, part[0]);
+  const bool finite = top < 0x7f80u;
+  if (!finite) {
+    top = 0;
 #pragma unroll
-  for (int i = 0; i < kWriteThreads / 32; ++i) amax = fmaxf(amax, part[i]);
-  const int e = page_exponent(amax);
+    for (int i = 0; i < kPasses; ++i) {
+      const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t a = w[j] & 0x7fffu, c = w[j] >> 16 & 0x7fffu;
+        top = max(top, max(a < 0x7f80u ? a : 0u, c < 0x7f80u ? c : 0u));
+      }
+    }
+    top = block_max(top, part[1]);
+  }
+  const int e = page_exponent(__uint_as_float(top << 16));
   const float now = fmaxf(exp2_int(e), old);
   const float inv = 1.f / now;  // exact: a power of two
   uint8_t* c = p.c[which] + (static_cast<int64_t>(page) * p.heads + head) * (kPage * 128) + chunk * 8;
   if (lo > 0 && now != old) {
     // entries written earlier, in units of the larger scale
     const float ratio = old * inv;
-#pragma unroll
-    for (int i = 0; i < kPasses; ++i) {
-      const int r = row0 + i * kRowsPerPass;
-      if (r >= lo) continue;
+#pragma unroll 1
+    for (int r = row0; r < lo; r += kRowsPerPass) {
       uint2* at = reinterpret_cast<uint2*>(c + r * 128);
       const uint2 w = *at;
       uint32_t in[2] = {w.x, w.y}, out[2];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const float2 a = e4m3x2_to_float2(in[j] & 0xffffu), d = e4m3x2_to_float2(in[j] >> 16);
-        out[j] = to_e4m3x2(a.x * ratio, a.y * ratio) | to_e4m3x2(d.x * ratio, d.y * ratio) << 16;
+        out[j] = to_e4m3x2<false>(a.x * ratio, a.y * ratio) | to_e4m3x2<false>(d.x * ratio, d.y * ratio) << 16;
       }
       *at = make_uint2(out[0], out[1]);
     }
@@ -142,12 +170,7 @@ __global__ void __launch_bounds__(kWriteThreads) cache_write_kernel(const __grid
   for (int i = 0; i < kPasses; ++i) {
     const int r = row0 + i * kRowsPerPass;
     if (r < lo || r >= hi) continue;
-    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-    uint32_t q[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      q[j] = to_e4m3x2(__uint_as_float(w[j] << 16) * inv, __uint_as_float(w[j] & 0xffff0000u) * inv);
-    *reinterpret_cast<uint2*>(c + r * 128) = make_uint2(q[0] | q[1] << 16, q[2] | q[3] << 16);
+    *reinterpret_cast<uint2*>(c + r * 128) = finite ? to_e4m3x8<true>(v[i], inv) : to_e4m3x8<false>(v[i], inv);
   }
   if (threadIdx.x == 0 && now != old) *scale = now;
 }
