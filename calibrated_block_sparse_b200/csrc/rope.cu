@@ -14,6 +14,8 @@
 // (queries, then keys) with them, so their cost is shared by all heads; reads
 // and writes are whole 256-byte rows, which makes the change between the
 // projections' token-major layout and the attention's head-major one free.
+// Measured on B200: 32760 tokens x 80 heads (1.34 GB) in 215 us, 96 % of the
+// rate of a plain copy.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -30,7 +32,7 @@
 namespace calibatt {
 namespace {
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 128;
 
 struct RopeView {
   const __nv_bfloat16* in;
@@ -110,17 +112,15 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
   const bool on_h = lane < rot;
   const int c0 = kHalves ? (on_h ? lane : 2 * rot + 2 * (lane - rot)) : lane;
   const int c1 = kHalves ? (on_h ? lane + rot : c0 + 1) : 0;
-  float cs[kPairs], sn[kPairs];
-#pragma unroll
-  for (int i = 0; i < kPairs; ++i) pair_angle(p, pos, (kHalves ? lane * 8 : lane * 4) + i, cs[i], sn[i]);
-
   const int heads = p.t[0].heads + p.t[1].heads;
   const int h_end = min(heads, (static_cast<int>(blockIdx.y) + 1) * p.heads_per_cta);
-  // kBatch heads are loaded before the first is stored: the output may be the
-  // input's own memory, so the compiler cannot move a load over a store
+  // kBatch heads are loaded at a time, and the next ones before these are
+  // stored: the output may be the input's own memory, so the compiler cannot
+  // move a load over a store. The first loads run beside the sines.
   constexpr int kBatch = kHalves ? 2 : 4;
-  for (int h0 = blockIdx.y * p.heads_per_cta + head_lane; h0 < h_end; h0 += kBatch * p.head_lanes) {
-    uint4 v[kBatch], u[kHalves ? kBatch : 1];
+  constexpr int kChunks = kHalves ? 2 : 1;
+  uint4 v[kBatch][kChunks], next[kBatch][kChunks];
+  auto load = [&](int h0, uint4 (&w)[kBatch][kChunks]) {
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
       const int h = h0 + i * p.head_lanes;
@@ -128,9 +128,17 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
       const bool second = h >= p.t[0].heads;
       const __nv_bfloat16* in = second ? p.t[1].in + (h - p.t[0].heads) * p.t[1].in_hs + token * p.t[1].in_ts
                                        : p.t[0].in + h * p.t[0].in_hs + token * p.t[0].in_ts;
-      v[i] = reinterpret_cast<const uint4*>(in)[c0];
-      if constexpr (kHalves) u[i] = reinterpret_cast<const uint4*>(in)[c1];
+      w[i][0] = reinterpret_cast<const uint4*>(in)[c0];
+      if constexpr (kHalves) w[i][1] = reinterpret_cast<const uint4*>(in)[c1];
     }
+  };
+  int h0 = blockIdx.y * p.heads_per_cta + head_lane;
+  load(h0, v);
+  float cs[kPairs], sn[kPairs];
+#pragma unroll
+  for (int i = 0; i < kPairs; ++i) pair_angle(p, pos, (kHalves ? lane * 8 : lane * 4) + i, cs[i], sn[i]);
+  for (; h0 < h_end; h0 += kBatch * p.head_lanes) {
+    load(h0 + kBatch * p.head_lanes, next);
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
       const int h = h0 + i * p.head_lanes;
@@ -138,20 +146,26 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
       const bool second = h >= p.t[0].heads;
       __nv_bfloat16* out = second ? p.t[1].out + (h - p.t[0].heads) * p.t[1].out_hs + token * p.t[1].out_ts
                                   : p.t[0].out + h * p.t[0].out_hs + token * p.t[0].out_ts;
+      uint4& x = v[i][0];
       if constexpr (!kHalves) {
-        v[i].x = rotate_word(v[i].x, cs[0], sn[0], lane * 4 + 0 < p.pairs);
-        v[i].y = rotate_word(v[i].y, cs[1], sn[1], lane * 4 + 1 < p.pairs);
-        v[i].z = rotate_word(v[i].z, cs[2], sn[2], lane * 4 + 2 < p.pairs);
-        v[i].w = rotate_word(v[i].w, cs[3], sn[3], lane * 4 + 3 < p.pairs);
+        x.x = rotate_word(x.x, cs[0], sn[0], lane * 4 + 0 < p.pairs);
+        x.y = rotate_word(x.y, cs[1], sn[1], lane * 4 + 1 < p.pairs);
+        x.z = rotate_word(x.z, cs[2], sn[2], lane * 4 + 2 < p.pairs);
+        x.w = rotate_word(x.w, cs[3], sn[3], lane * 4 + 3 < p.pairs);
       } else if (on_h) {
-        rotate_words(v[i].x, u[i].x, cs + 0, sn + 0);
-        rotate_words(v[i].y, u[i].y, cs + 2, sn + 2);
-        rotate_words(v[i].z, u[i].z, cs + 4, sn + 4);
-        rotate_words(v[i].w, u[i].w, cs + 6, sn + 6);
+        uint4& y = v[i][1];
+        rotate_words(x.x, y.x, cs + 0, sn + 0);
+        rotate_words(x.y, y.y, cs + 2, sn + 2);
+        rotate_words(x.z, y.z, cs + 4, sn + 4);
+        rotate_words(x.w, y.w, cs + 6, sn + 6);
       }
-      reinterpret_cast<uint4*>(out)[c0] = v[i];
-      if constexpr (kHalves) reinterpret_cast<uint4*>(out)[c1] = u[i];
+      reinterpret_cast<uint4*>(out)[c0] = x;
+      if constexpr (kHalves) reinterpret_cast<uint4*>(out)[c1] = v[i][1];
     }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+      for (int j = 0; j < kChunks; ++j) v[i][j] = next[i][j];
   }
 }
 
@@ -258,7 +272,10 @@ int rope(const calibatt_rope_plan* plan, const void* q, int64_t q_ts, int64_t q_
   p.head_lanes = 1;
   while (p.head_lanes < slots && static_cast<int64_t>(slots / p.head_lanes) > n) p.head_lanes *= 2;
   const int64_t gx = (n * p.head_lanes + slots - 1) / slots;
-  // and the heads are spread over CTAs until the card is filled
+  // and the heads are spread over CTAs until there are 8 per SM: fewer leave
+  // SMs idle, more repeat the sines. Measured at 4680 tokens x 80 heads (192
+  // MB): 34.6 us with 8, 33.7 with 16, 36.7 with 32; at 7421 x 32 with halves
+  // paired: 24.5, 25.1, 31.0 (CTAs of 256 threads: 36.7 and 26.2 with 8).
   const int64_t want = 8ll * sm_count();
   int64_t gy = (want + gx - 1) / gx;
   const int64_t most = (all + p.head_lanes - 1) / p.head_lanes;
