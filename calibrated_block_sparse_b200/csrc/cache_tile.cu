@@ -15,11 +15,16 @@
 // slots hold the same rows and take every other page, and are joined at the
 // end: the chain S -> softmax -> P V of one slot then runs beside the other's.
 //
-// K is converted to fp16, which holds every e4m3 value, and Q is brought to
-// fp16 by a power of two per row; the scales multiply the fp32 score. V is
-// converted to bf16 with its page's scale: a power of two times an e4m3 value
-// is a bf16 value, whatever the scale's size, so O accumulates over pages with
-// different scales. P is bf16 then, as both operands of a product have one type.
+// K and V become fp16 without their scales: fp16 holds every e4m3 value, and
+// the conversion is one instruction per two values (with the scale in it, as
+// bf16, it took five and the converters, not the tensor core, set the pace).
+// Q is brought to fp16 by a power of two per row; that and the key scale
+// multiply the fp32 score. O is kept in units of a reference value scale: a
+// page whose value scale is 2^-6 .. 2 of it multiplies P by the ratio in the
+// exponent, at no cost, and where a page is outside that range the reference
+// moves and O is rescaled, as it is when the running maximum has grown. P is
+// fp16, 2^6 times the weight: with a maximum up to 2^8 stale and a ratio up to
+// 2 it stays below 2^15, and weights down to 2^-24 keep a bit.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -42,21 +47,25 @@ namespace {
 constexpr int kTileThreads = 512;
 // registers per thread after the split; their sum must fit in the launch
 // allotment of 128 x 512 (checked against the compiled count before a launch)
-constexpr int kTileSoftmaxRegs = 184;
-constexpr int kTileConvertRegs = 96;
+constexpr int kTileSoftmaxRegs = 192;
+constexpr int kTileConvertRegs = 88;
 constexpr int kTileControlRegs = 40;
 constexpr int kTileRegs = 256 * kTileSoftmaxRegs + 128 * kTileConvertRegs + 128 * kTileControlRegs;
 static_assert(kTileRegs <= 128 * kTileThreads, "register split");
 constexpr int kTileRing = 5;
 constexpr float kTileRescale = 8.0f;   // log2 units: move the running max only if it grows by more
 constexpr float kBigScore = 65536.0f;  // log2 units: beyond it the rounding of the row max counts
+constexpr float kPScale = 6.0f;        // log2 of P's factor
+// A reference scale is never more than this below the largest value scale met:
+// O, at most 2^55 in units of that (2^15 * 448 * 2^31 keys), stays finite.
+constexpr float kMostShrink = 8.470329472543003e-22f;  // 2^-70
 
 struct TileBarriers {
   uint64_t ring_full[kTileRing];
   uint64_t ring_empty[kTileRing];
   uint64_t q_full[2];
   uint64_t s_full[2];
-  uint64_t p_full[2];
+  uint64_t p_full[2][2];  // per slot, per half of the page's keys
   uint64_t o_full[2];
   uint64_t mma_done;
   uint32_t tmem_base;
@@ -74,8 +83,9 @@ struct TileLayout {
 };
 static_assert(TileLayout::kDynSmem <= 232448, "shared memory budget");
 
-// fp16 operands, fp32 accumulation (formats 0); P V is bf16 (kIdescPV).
-constexpr uint32_t kIdescF16 = (1u << 4) | (16u << 17) | (8u << 24);
+// fp16 operands, fp32 accumulation (operand formats 0); V has its channels (N) contiguous.
+constexpr uint32_t kIdescQK = (1u << 4) | (16u << 17) | (8u << 24);
+constexpr uint32_t kIdescPVh = kIdescQK | (1u << 16);
 
 __device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
@@ -83,66 +93,51 @@ __device__ __forceinline__ void st_shared16(uint32_t addr, uint32_t a, uint32_t 
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
-// Page numbers and one scale of 32 consecutive pages of a stream, one per
-// lane, fetched a chunk of 32 ahead. A page outside the pool gets id -1.
+// Page numbers of 32 consecutive pages of a stream, one per lane, fetched a
+// chunk of 32 ahead; kScales: with their key and value scales. A page outside
+// the pool gets id -1.
+template <bool kScales>
 struct PageWindow {
   const int32_t* table;
-  const float* scale;
+  const float* k_scale;
+  const float* v_scale;
   int n_pages, heads, head, count;  // pages of the range
   int id, id_next;
-  float sc, sc_next;
+  float ks, vs, ks_next, vs_next;
 
-  __device__ __forceinline__ void fetch(int at, int& out_id, float& out_sc, int* status) {
-    out_id = -1;
-    out_sc = 0.f;
+  __device__ __forceinline__ void fetch(int at, int* status) {
+    id_next = -1;
+    ks_next = vs_next = 1.f;
     if (at < count) {
-      out_id = __ldg(table + at);
-      if (out_id < 0 || out_id >= n_pages) {
+      id_next = __ldg(table + at);
+      if (id_next < 0 || id_next >= n_pages) {
         record_error(status, CALIBATT_ERR_CSR);
-        out_id = -1;
-      } else {
-        out_sc = __ldg(scale + static_cast<int64_t>(out_id) * heads + head);
+        id_next = -1;
+      } else if (kScales) {
+        const int64_t i = static_cast<int64_t>(id_next) * heads + head;
+        ks_next = __ldg(k_scale + i);
+        vs_next = __ldg(v_scale + i);
       }
     }
   }
-  __device__ __forceinline__ void start(int lane, int* status) {
-    fetch(lane, id, sc, status);
-    fetch(32 + lane, id_next, sc_next, status);
-  }
-  // call before using page i = 32, 64, ...
+  // call before using page i = 0, 32, 64, ...
   __device__ __forceinline__ void advance(int i, int lane, int* status) {
     id = id_next;
-    sc = sc_next;
-    fetch(i + 32 + lane, id_next, sc_next, status);
+    ks = ks_next;
+    vs = vs_next;
+    fetch(i + 32 + lane, status);
   }
 };
 
-// 16 e4m3 values (ch 0..15 of a 64-channel half's quarter) as two 16-byte
-// chunks of fp16.
-__device__ __forceinline__ void store_k(uint32_t row_addr, int r, int j, const uint4& w) {
+// 16 e4m3 values as two 16-byte chunks j, j + 1 of fp16 of row r, with the
+// 128-byte swizzle (chunk j is at j ^ (r & 7)).
+__device__ __forceinline__ void store_half(uint32_t row_addr, int r, int j, const uint4& w) {
   const uint32_t x[4] = {w.x, w.y, w.z, w.w};
   uint32_t h[8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     h[2 * i] = e4m3x2_to_half2(x[i] & 0xffffu);
     h[2 * i + 1] = e4m3x2_to_half2(x[i] >> 16);
-  }
-  st_shared16(row_addr + ((j ^ (r & 7)) << 4), h[0], h[1], h[2], h[3]);
-  st_shared16(row_addr + (((j + 1) ^ (r & 7)) << 4), h[4], h[5], h[6], h[7]);
-}
-
-__device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t two, float scale) {
-  const float2 f = e4m3x2_to_float2(two);
-  return pack_bf16x2(f.x * scale, f.y * scale);
-}
-
-__device__ __forceinline__ void store_v(uint32_t row_addr, int r, int j, const uint4& w, float scale) {
-  const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-  uint32_t h[8];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    h[2 * i] = e4m3x2_to_bf16x2(x[i] & 0xffffu, scale);
-    h[2 * i + 1] = e4m3x2_to_bf16x2(x[i] >> 16, scale);
   }
   st_shared16(row_addr + ((j ^ (r & 7)) << 4), h[0], h[1], h[2], h[3]);
   st_shared16(row_addr + (((j + 1) ^ (r & 7)) << 4), h[4], h[5], h[6], h[7]);
@@ -210,7 +205,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bar.q_full[s], 128);
       mbar_init(&bar.s_full[s], 1);
-      mbar_init(&bar.p_full[s], 128);
+      mbar_init(&bar.p_full[s][0], 128);
+      mbar_init(&bar.p_full[s][1], 128);
       mbar_init(&bar.o_full[s], 1);
     }
     mbar_init(&bar.mma_done, 1);
@@ -231,41 +227,24 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     // lanes of a store phase: two rows (one even, one odd) of four quarters
     // of a 64-channel half, so their 16-byte chunks fall into eight banks groups
     const int row = (warp - 8) * 8 + (lane >> 2), quarter = lane & 3;
-    PageWindow win{table, p.v_scale, p.n_pages, p.heads_kv, head, np, 0, 0, 0.f, 0.f};
-    // pages are used in order by K (ahead) and V: windows move with K, and
-    // what V needs is remembered for the pages between
-    win.start(lane, p.status);
+    PageWindow<false> win{table, nullptr, nullptr, p.n_pages, p.heads_kv, head, np, -1, -1, 1.f, 1.f, 1.f, 1.f};
+    win.fetch(lane, p.status);
+    // pages are met in order by K; V follows at most one page behind
+    int id_now = -1, id_before = -1, k_at = 0;
     const int nt = 2 * np;
     uint4 buf[2][8];
-    float vs[2];
-    int ids[2], k_seen = 0;
-    // page id and value scale of page i: i is at most one page behind K's
-    int id_ring[4];
-    float sc_ring[4];
-    auto page_info = [&](int i, bool is_v, int& id, float& sc) {
-      if (!is_v) {
-        if (i > 0 && (i & 31) == 0) win.advance(i, lane, p.status);
-        id = __shfl_sync(0xffffffffu, win.id, i & 31);
-        sc = __shfl_sync(0xffffffffu, win.sc, i & 31);
-#pragma unroll
-        for (int e = 3; e > 0; --e) {
-          id_ring[e] = id_ring[e - 1];
-          sc_ring[e] = sc_ring[e - 1];
-        }
-        id_ring[0] = id;
-        sc_ring[0] = sc;
-        k_seen = i;
-      } else {
-        const int back = k_seen - i;  // 0, 1 or 2
-        id = back == 0 ? id_ring[0] : back == 1 ? id_ring[1] : id_ring[2];
-        sc = back == 0 ? sc_ring[0] : back == 1 ? sc_ring[1] : sc_ring[2];
-      }
-    };
-    auto load = [&](int t, uint4 (&w)[8], int& id, float& sc) {
+    auto load = [&](int t, uint4 (&w)[8]) {
       bool is_v;
-      int i;
+      int i, id;
       ring_tile<kAlt>(t, np, is_v, i);
-      page_info(i, is_v, id, sc);
+      if (!is_v) {
+        if ((i & 31) == 0) win.advance(i, lane, p.status);
+        id_before = id_now;
+        id_now = id = __shfl_sync(0xffffffffu, win.id, i & 31);
+        k_at = i;
+      } else {
+        id = k_at == i ? id_now : id_before;
+      }
       if (id < 0) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) w[e] = make_uint4(0, 0, 0, 0);
@@ -278,41 +257,35 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         w[e] = __ldg(reinterpret_cast<const uint4*>(src + (e >> 1) * (32 * 128) + (e & 1) * 64));
     };
     uint32_t stage = 0, phase = 0;
-    auto convert = [&](int t, uint4 (&w)[8], float sc) -> bool {
+    auto convert = [&](int t, uint4 (&w)[8]) -> bool {
       bool is_v;
       int i;
       ring_tile<kAlt>(t, np, is_v, i);
+      const int key0 = (pg0 + i) * kPage;
+      if (is_v && key0 + kPage > least) {
+        // a page that some row does not see whole: a product takes every key
+        // for every row, and 0 * NaN is NaN. Slots behind the last token
+        // become zero, and so does a NaN, which the rows that see it get back
+        // at the end.
+        uint32_t nan = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int key = key0 + (e >> 1) * 32 + row;
+          uint32_t* x = reinterpret_cast<uint32_t*>(&w[e]);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if (key >= st.len) x[k] = 0;
+            const uint32_t hit = e4m3_nan_bytes(x[k]);
+            x[k] &= ~((hit >> 7) * 0xffu);
+            nan |= hit;
+          }
+        }
+        if (nan) *const_cast<volatile int*>(&bar.nan_seen) = 1;
+      }
       if (!mbar_wait<SW>(&bar.ring_empty[stage], phase ^ 1, abort_flag, p.status, p.wait_limit_ns)) return false;
       const uint32_t dst = sbase + L::kRingOff + stage * kTile + row * 128;
-      if (!is_v) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) store_k(dst + (e & 1) * kHalf + (e >> 1) * (32 * 128), row, 2 * quarter, w[e]);
-      } else {
-        const int key0 = (pg0 + i) * kPage;
-        if (key0 + kPage > least) {
-          // a page that some row does not see whole: a product takes every
-          // key for every row, and 0 * NaN is NaN. Slots behind the last
-          // token become zero, and so does a NaN, which the rows that see it
-          // get back at the end.
-          uint32_t nan = 0;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int key = key0 + (e >> 1) * 32 + row;
-            uint32_t* x = reinterpret_cast<uint32_t*>(&w[e]);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              if (key >= st.len) x[k] = 0;
-              const uint32_t hit = e4m3_nan_bytes(x[k]);
-              x[k] &= ~((hit >> 7) * 0xffu);
-              nan |= hit;
-            }
-          }
-          if (nan) *const_cast<volatile int*>(&bar.nan_seen) = 1;
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          store_v(dst + (e & 1) * kHalf + (e >> 1) * (32 * 128), row, 2 * quarter, w[e], sc);
-      }
+      for (int e = 0; e < 8; ++e) store_half(dst + (e & 1) * kHalf + (e >> 1) * (32 * 128), row, 2 * quarter, w[e]);
       fence_proxy_async();
       mbar_arrive(&bar.ring_full[stage]);
       if (++stage == kTileRing) {
@@ -322,14 +295,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       return true;
     };
     // the wait's outcome is made the warp's, for the shuffles that follow
-    if (nt > 0) load(0, buf[0], ids[0], vs[0]);
-    if (nt > 1) load(1, buf[1], ids[1], vs[1]);
+    if (nt > 0) load(0, buf[0]);
+    if (nt > 1) load(1, buf[1]);
     for (int t = 0; t < nt && ok; t += 2) {
-      ok = __all_sync(0xffffffffu, convert(t, buf[0], vs[0]));
-      if (t + 2 < nt) load(t + 2, buf[0], ids[0], vs[0]);
+      ok = __all_sync(0xffffffffu, convert(t, buf[0]));
+      if (t + 2 < nt) load(t + 2, buf[0]);
       if (t + 1 < nt && ok) {
-        ok = __all_sync(0xffffffffu, convert(t + 1, buf[1], vs[1]));
-        if (t + 3 < nt) load(t + 3, buf[1], ids[1], vs[1]);
+        ok = __all_sync(0xffffffffu, convert(t + 1, buf[1]));
+        if (t + 3 < nt) load(t + 3, buf[1]);
       }
     }
   } else if (warp >= 12) {
@@ -356,15 +329,24 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const uint64_t qd = qdesc0 + (kAlt ? 0 : s) * (kTile >> 4), kd = kdesc0 + stage * (kTile >> 4);
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks)
-          mma_ss(tmem + s * 128, qd + desc_k_step(ks), kd + desc_k_step(ks), kIdescF16, ks > 0);
+          mma_ss(tmem + s * 128, qd + desc_k_step(ks), kd + desc_k_step(ks), kIdescQK, ks > 0);
         mma_commit(&bar.s_full[s]);
       };
-      auto issue_pv = [&](int s, bool first) {
+      // the first half of P's keys is multiplied while the second is computed
+      auto issue_pv = [&](int s, bool first, uint32_t parity) -> bool {
+        if (!mbar_wait<SW>(&bar.p_full[s][0], parity, abort_flag, p.status, p.wait_limit_ns)) return false;
+        if (!ring_wait()) return false;
         const uint64_t vd = vdesc0 + stage * (kTile >> 4);
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks)
-          mma_ts(tmem + 256 + s * 128, tmem + s * 128 + ks * 8, vd + desc_v_step(ks), kIdescPV,
+        for (int ks = 0; ks < 4; ++ks)
+          mma_ts(tmem + 256 + s * 128, tmem + s * 128 + ks * 8, vd + desc_v_step(ks), kIdescPVh,
                  (!first || ks > 0) ? 1u : 0u);
+        if (!mbar_wait<SW>(&bar.p_full[s][1], parity, abort_flag, p.status, p.wait_limit_ns)) return false;
+        tc_fence_after();
+#pragma unroll
+        for (int ks = 4; ks < 8; ++ks)
+          mma_ts(tmem + 256 + s * 128, tmem + s * 128 + ks * 8, vd + desc_v_step(ks), kIdescPVh, 1u);
+        return true;
       };
       bool go = mbar_wait<SW>(&bar.q_full[0], 0, abort_flag, p.status, p.wait_limit_ns);
       if constexpr (kAlt) {
@@ -375,9 +357,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
         for (int i = 0; i < np && go; ++i) {
           const int s = i & 1;
-          if (!(go = mbar_wait<SW>(&bar.p_full[s], (i >> 1) & 1, abort_flag, p.status, p.wait_limit_ns))) break;
-          if (!(go = ring_wait())) break;
-          issue_pv(s, i < 2);
+          if (!(go = issue_pv(s, i < 2, (i >> 1) & 1))) break;
           ring_next();
           if (i + 2 < np) {
             if (!(go = ring_wait())) break;
@@ -397,9 +377,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         for (int i = 0; i < np && go; ++i) {
           // stage holds V of page i; K of the next page is one stage on
           for (int s = 0; s < ns && go; ++s) {
-            if (!(go = mbar_wait<SW>(&bar.p_full[s], i & 1, abort_flag, p.status, p.wait_limit_ns))) break;
-            if (!(go = ring_wait())) break;
-            issue_pv(s, i == 0);
+            if (!(go = issue_pv(s, i == 0, i & 1))) break;
             const uint32_t v_stage = stage, v_phase = phase;
             if (i + 1 < np) {
               if (s == ns - 1) {
@@ -431,6 +409,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     // ---------------------------------------------------------- softmax
     warpgroup_regs_inc<kTileSoftmaxRegs>();
     float m_run = -INFINITY, l_run = 0.f;
+    float v_ref = 1.f, v_top = 1.f;  // units of O: 2^-kPScale v_ref
     bool ok = true;  // warp-uniform
     const int s = warp >> 2;
     const int row = (warp & 3) * 32 + lane;
@@ -492,35 +471,40 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     };
     const bool active = s == 0 || second;
     if (active && np > 0) {
-      PageWindow win{table, p.k_scale, p.n_pages, p.heads_kv, head, np, 0, 0, 0.f, 0.f};
-      win.start(lane, p.status);
+      PageWindow<true> win{table, p.k_scale, p.v_scale, p.n_pages, p.heads_kv, head, np, -1, -1, 1.f, 1.f, 1.f, 1.f};
+      win.fetch(lane, p.status);
       int turn = 0;  // pages this slot has taken
       for (int i = kAlt ? s : 0; i < np; i += kAlt ? 2 : 1, ++turn) {
-        if (i >= 32 && (i & 31) < (kAlt ? 2 : 1)) win.advance(i & ~31, lane, p.status);
+        if ((i & 31) < (kAlt ? 2 : 1)) win.advance(i & ~31, lane, p.status);
         const int id = __shfl_sync(0xffffffffu, win.id, i & 31);
-        const float ck = score_factor(c_row, __shfl_sync(0xffffffffu, win.sc, i & 31));
+        const float ck = score_factor(c_row, __shfl_sync(0xffffffffu, win.ks, i & 31));
+        float vs = __shfl_sync(0xffffffffu, win.vs, i & 31);
+        if (vs == 0.f) vs = 1.17549435e-38f;
+        // the reference of O's units (the same for all rows)
+        float o_ratio = 1.f;
+        if (turn == 0) {
+          v_ref = v_top = vs;
+        } else if (vs > 2.f * v_ref || vs < 0.015625f * v_ref) {
+          v_top = fmaxf(v_top, vs);
+          const float now = fmaxf(vs, v_top * kMostShrink);
+          o_ratio = v_ref / now;
+          v_ref = now;
+        }
+        const float f = vs / v_ref;
         if (!wait_warp(&bar.s_full[s], turn & 1)) break;
         tc_fence_after();
         const int key0 = (pg0 + i) * kPage;
         const int cut = id < 0 ? 0 : min(limit - key0, kPage);  // keys of the page that the row sees
-        const bool masked = __any_sync(0xffffffffu, cut < kPage);
         const uint32_t sc = tmem + lane_off + s * 128;
-        float sv[64];
-        // the second half first: P overwrites the first half's columns only
-        tmem_ld64_wait(sc + 64, sv);
-        if (masked) {
+        float sv[2][64];
+        tmem_ld64_wait(sc, sv[0]);
+        tmem_ld64_wait(sc + 64, sv[1]);
+        if (__any_sync(0xffffffffu, cut < kPage)) {
 #pragma unroll
-          for (int e = 0; e < 64; ++e)
-            if (64 + e >= cut) sv[e] = -INFINITY;
+          for (int e = 0; e < 128; ++e)
+            if (e >= cut) sv[e >> 6][e & 63] = -INFINITY;
         }
-        float mx = row_max64(sv);
-        tmem_ld64_wait(sc, sv);
-        if (masked) {
-#pragma unroll
-          for (int e = 0; e < 64; ++e)
-            if (e >= cut) sv[e] = -INFINITY;
-        }
-        mx = fmaxf(mx, row_max64(sv));
+        const float mx = fmaxf(row_max64(sv[0]), row_max64(sv[1]));
         const float page_max = mx * ck;
         const float m_new = fmaxf(m_run, page_max);
         // keep a stale running max unless it grew by more than the threshold
@@ -531,51 +515,48 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const float alpha = need ? ex2_approx(m_prev - m_use) : 1.f;
         // exponent s * ck - m; for very large scores relative to the page's
         // own maximum first, whose rounding would otherwise stay in it
-        const bool big = __any_sync(0xffffffffu, fabsf(m_use) > kBigScore);
-        const float mx0 = mx == -INFINITY ? 0.f : mx;
-        const float mul = big ? 1.f : ck, add = big ? page_max - m_use : -m_use;
+        const float f_log = log2f(f) + kPScale;
+        float mul = ck, add = f_log - m_use;
+        if (__any_sync(0xffffffffu, fabsf(m_use) > kBigScore)) {
+          const float mx0 = mx == -INFINITY ? 0.f : mx;
+#pragma unroll
+          for (int e = 0; e < 128; ++e) sv[e >> 6][e & 63] = (sv[e >> 6][e & 63] - mx0) * ck;
+          mul = 1.f;
+          add = page_max - m_use + f_log;
+        }
+        // O is rescaled before P is handed on. Its product with the page
+        // before is complete: the commit that signalled S tracks every
+        // earlier MMA.
+        if (turn > 0 && (o_ratio != 1.f || __any_sync(0xffffffffu, need))) {
+          const float by = alpha * o_ratio;
+#pragma unroll 1
+          for (int cc = 0; cc < 8; ++cc) {
+            uint32_t o[16];
+            tmem_ld16_wait(tmem + lane_off + 256 + s * 128 + cc * 16, o);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * by);
+            tmem_st16(tmem + lane_off + 256 + s * 128 + cc * 16, o);
+          }
+        }
         const float2 c2 = make_float2(mul, mul), n2 = make_float2(add, add);
         float2 a4[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          if (h == 1) {
-            tmem_ld64_wait(sc + 64, sv);
-            if (masked) {
-#pragma unroll
-              for (int e = 0; e < 64; ++e)
-                if (64 + e >= cut) sv[e] = -INFINITY;
-            }
-          }
-          if (big) {
-#pragma unroll
-            for (int e = 0; e < 64; ++e) sv[e] = (sv[e] - mx0) * ck;
-          }
           uint32_t pk[32];
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
-            const float2 x = exp2_mufu2(ffma2(make_float2(sv[2 * e], sv[2 * e + 1]), c2, n2));
+            const float2 x = exp2_mufu2(ffma2(make_float2(sv[h][2 * e], sv[h][2 * e + 1]), c2, n2));
             a4[e & 3] = fadd2(a4[e & 3], x);
-            pk[e] = pack_bf16x2(x.x, x.y);
+            pk[e] = pack_half2(x.x, x.y);
           }
+          // P (fp16, two keys per column) over the first 64 columns of S
           tmem_st32(sc + h * 32, pk);
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(&bar.p_full[s][h]);
         }
         const float2 s01 = fadd2(a4[0], a4[1]), s23 = fadd2(a4[2], a4[3]);
-        l_run = l_run * alpha + ((s01.x + s01.y) + (s23.x + s23.y));
-        // O's product with the page before is complete: the commit that
-        // signalled S tracks every earlier MMA
-        if (turn > 0 && __any_sync(0xffffffffu, need)) {
-#pragma unroll
-          for (int cc = 0; cc < 4; ++cc) {
-            uint32_t o[32];
-            tmem_ld32_wait(tmem + lane_off + 256 + s * 128 + cc * 32, o);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-            tmem_st32(tmem + lane_off + 256 + s * 128 + cc * 32, o);
-          }
-        }
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(&bar.p_full[s]);
+        l_run = l_run * alpha + ((s01.x + s01.y) + (s23.x + s23.y)) * (0.015625f / f);
       }
       wait_warp(&bar.o_full[s], 0);
       // the ring is about to be reused: the other slot's products must be done too
@@ -585,19 +566,20 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 
     // ---------------------------------------------------------- results
     const bool done = ok && *abort_flag == 0;
-    float f0 = 1.f, f1 = 0.f;
+    float f0 = v_ref * 0.015625f, f1 = 0.f;
     // alternate: slot 1 hands its rows to slot 0 through the ring's memory,
     // [channel][row], which every MMA has finished reading
     float* joined = reinterpret_cast<float*>(smem + L::kRingOff);
     if constexpr (kAlt) {
       if (s == 1 && second && done) {
         bar.slot_ml[row] = make_float2(m_run, l_run);
+        const float unit = v_ref * 0.015625f;
 #pragma unroll
         for (int cc = 0; cc < 4; ++cc) {
           uint32_t o[32];
           tmem_ld32_wait(tmem + lane_off + 256 + 128 + cc * 32, o);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) joined[(cc * 32 + e) * 128 + row] = __uint_as_float(o[e]);
+          for (int e = 0; e < 32; ++e) joined[(cc * 32 + e) * 128 + row] = __uint_as_float(o[e]) * unit;
         }
       }
       named_bar_sync(1, 256);
@@ -605,9 +587,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const float2 o = bar.slot_ml[row];
         const float mx = fmaxf(m_run, o.x);
         const float use = mx == -INFINITY ? 0.f : mx;
-        f0 = ex2_approx(m_run - use);
+        const float g0 = ex2_approx(m_run - use);
         f1 = ex2_approx(o.x - use);
-        l_run = l_run * f0 + o.y * f1;
+        l_run = l_run * g0 + o.y * f1;
+        f0 *= g0;
         m_run = mx;
       }
     }
@@ -631,10 +614,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = 0;
         }
-        if (kAlt && second) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            o[e] = __float_as_uint(__uint_as_float(o[e]) * f0 + joined[(cc * 32 + e) * 128 + row] * f1);
+        for (int e = 0; e < 32; ++e) {
+          float x = __uint_as_float(o[e]) * f0;
+          if (kAlt && second) x += joined[(cc * 32 + e) * 128 + row] * f1;
+          o[e] = __float_as_uint(x);
         }
         if (patch && row_valid) {
           // NaN values that were taken out of pages that not every row sees whole
