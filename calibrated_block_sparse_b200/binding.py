@@ -790,10 +790,7 @@ def _want_rows(t, name, index=None):
     return shape, strides
 
 
-def _raw_stream(stream, index):
-    if stream is not None:
-        return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(index)
+_current_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _new(like, shape, dtype, stream):
@@ -805,58 +802,61 @@ def _new(like, shape, dtype, stream):
         return like.new_empty(shape, dtype=dtype)
 
 
-_NO_ROWS = (None, 0, 0, 0)
+_Int3 = ctypes.c_int32 * 3
 
 
-def _rope(fn, tok, q, k, plan, grid, start, pos, q_out, k_out, stream):
-    # tok: the token dimension of the inputs (0: rotation, 1: gradient); the outputs have it in the other place
+def _rope(forward, q, k, plan, grid, start, pos, q_out, k_out, stream):
+    # the token dimension is the first of the inputs and the second of the outputs; for the gradient the other way round
+    tok, hd = (0, 1) if forward else (1, 0)
     if not isinstance(q, torch.Tensor):
         _refuse(q, "q", torch.bfloat16, None, contiguous=False)
     index = q.get_device()
     if index >= 0 and torch.cuda.current_device() != index:
         with torch.cuda.device(index):
-            return _rope(fn, tok, q, k, plan, grid, start, pos, q_out, k_out, stream)
-    hd = 1 - tok
+            return _rope(forward, q, k, plan, grid, start, pos, q_out, k_out, stream)
     shape, st = _want_rows(q, "q")
     n, heads = shape[tok], shape[hd]
-    a = (q.data_ptr(), st[tok], st[hd], heads)
-    out_shape = (n, heads, HEAD_DIM) if tok else (heads, n, HEAD_DIM)
+    out_shape = (heads, n, HEAD_DIM) if forward else (n, heads, HEAD_DIM)
     if q_out is None:
         q_out = _new(q, out_shape, torch.bfloat16, stream)
-    shape, st = _want_rows(q_out, "q_out", index)
+    shape, ost = _want_rows(q_out, "q_out", index)
     if shape != out_shape:
         raise ValueError(f"q_out must be {list(out_shape)}")
-    a_out = (q_out.data_ptr(), st[hd], st[tok])
-    b, b_out = _NO_ROWS, _NO_ROWS[:3]
     if k is not None:
-        shape, st = _want_rows(k, "k", index)
+        shape, kst = _want_rows(k, "k", index)
         if shape[tok] != n:
             raise ValueError(f"k has {shape[tok]} tokens, q has {n}")
-        heads = shape[hd]
-        b = (k.data_ptr(), st[tok], st[hd], heads)
-        out_shape = (n, heads, HEAD_DIM) if tok else (heads, n, HEAD_DIM)
+        heads_k, k_ptr = shape[hd], k.data_ptr()
+        out_shape = (heads_k, n, HEAD_DIM) if forward else (n, heads_k, HEAD_DIM)
         if k_out is None:
             k_out = _new(k, out_shape, torch.bfloat16, stream)
-        shape, st = _want_rows(k_out, "k_out", index)
+        shape, kost = _want_rows(k_out, "k_out", index)
         if shape != out_shape:
             raise ValueError(f"k_out must be {list(out_shape)}")
-        b_out = (k_out.data_ptr(), st[hd], st[tok])
+        k_out_ptr = k_out.data_ptr()
     elif k_out is not None:
         raise ValueError("k_out without k")
-    if (grid is None) == (pos is None):
-        raise ValueError("give the positions as a grid (H, W) or as a tensor pos [n][3]")
-    if pos is None:
-        H, W = grid
-        at = (ctypes.c_int32 * 3)(*start)
-        rc = getattr(load(), fn)(ctypes.byref(plan), *a, *b, n, HEAD_DIM, None, int(H), int(W), at, *a_out, *b_out,
-                                 _raw_stream(stream, index))
     else:
+        heads_k, k_ptr, k_out_ptr, kst, kost = 0, None, None, (0, 0), (0, 0)
+    if pos is None:
+        if grid is None:
+            raise ValueError("give the positions as a grid (H, W) or as a tensor pos [n][3]")
+        H, W = grid
+        pos_ptr, at = None, _Int3(*start)
+    else:
+        if grid is not None:
+            raise ValueError("give the positions as a grid (H, W) or as a tensor pos [n][3], not as both")
         _want(pos, torch.int32, "pos", index)
         if pos.shape != (n, 3):
             raise ValueError(f"pos must be [{n}][3]")
-        rc = getattr(load(), fn)(ctypes.byref(plan), *a, *b, n, HEAD_DIM, pos.data_ptr(), 0, 0, None, *a_out, *b_out,
-                                 _raw_stream(stream, index))
-    _check(rc, fn)
+        H, W, pos_ptr, at = 0, 0, pos.data_ptr(), None
+    lib = _lib or load()
+    rc = (lib.calibatt_rope_fwd if forward else lib.calibatt_rope_bwd)(
+        ctypes.byref(plan), q.data_ptr(), st[tok], st[hd], heads, k_ptr, kst[tok], kst[hd], heads_k, n, HEAD_DIM,
+        pos_ptr, H, W, at, q_out.data_ptr(), ost[hd], ost[tok], k_out_ptr, kost[hd], kost[tok],
+        _current_raw_stream(index) if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc, "calibatt_rope_fwd" if forward else "calibatt_rope_bwd")
     return q_out, k_out
 
 
@@ -865,13 +865,13 @@ def rope_fwd(q, k, plan, grid=None, start=(0, 0, 0), pos=None, q_out=None, k_out
     any strides by their positions: a grid (H, W) whose first token is at
     `start` (time, height, width), or pos, int32 [n][3]. Returns them as
     [heads][n][128], the layout of the attention calls."""
-    return _rope("calibatt_rope_fwd", 0, q, k, plan, grid, start, pos, q_out, k_out, stream)
+    return _rope(True, q, k, plan, grid, start, pos, q_out, k_out, stream)
 
 
 def rope_bwd(dq_out, dk_out, plan, grid=None, start=(0, 0, 0), pos=None, dq=None, dk=None, stream=None):
     """Gradients of rope_fwd's inputs, [n][heads][128], from those of its
     outputs, [heads][n][128] of any strides (expanded ones too)."""
-    return _rope("calibatt_rope_bwd", 1, dq_out, dk_out, plan, grid, start, pos, dq, dk, stream)
+    return _rope(False, dq_out, dk_out, plan, grid, start, pos, dq, dk, stream)
 
 
 # ------------------------------------------------------------------ streaming: 8-bit cache
@@ -918,11 +918,13 @@ def cache_write(k, v, k8, v8, k_scale, v_scale, tok_start, kv_len, table, max_ne
     pages, cache_heads, batch, width = _cache_args(k8, v8, k_scale, v_scale, tok_start, kv_len, table, index)
     if cache_heads != heads:
         raise ValueError(f"the cache has {cache_heads} heads, k has {heads}")
-    rc = load().calibatt_cache_write(k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], heads, n, HEAD_DIM,
-                                     tok_start.data_ptr(), kv_len.data_ptr(), batch, n if max_new is None else max_new,
-                                     table.data_ptr(), width, pages, k8.data_ptr(), v8.data_ptr(), k_scale.data_ptr(),
-                                     v_scale.data_ptr(), _raw_stream(stream, index))
-    _check(rc, "calibatt_cache_write")
+    rc = (_lib or load()).calibatt_cache_write(
+        k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], heads, n, HEAD_DIM, tok_start.data_ptr(),
+        kv_len.data_ptr(), batch, n if max_new is None else max_new, table.data_ptr(), width, pages, k8.data_ptr(),
+        v8.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+        _current_raw_stream(index) if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc, "calibatt_cache_write")
 
 
 def cache_attn_workspace_size(batch, heads_q, heads_kv, n, max_new, max_kv) -> int:
@@ -972,8 +974,7 @@ def cache_attn_fwd(q, k8, v8, k_scale, v_scale, tok_start, kv_len, table, max_ne
         max_new = n
     if max_kv is None:
         max_kv = width * BLOCK
-    lib = load()
-    ws_bytes = 0
+    lib = _lib or load()
     if ws is not None:
         _want(ws, torch.uint8, "ws", index)
         ws_bytes = ws.numel()
@@ -981,13 +982,14 @@ def cache_attn_fwd(q, k8, v8, k_scale, v_scale, tok_start, kv_len, table, max_ne
         ws_bytes = lib.calibatt_cache_attn_workspace_size(batch, heads_q, heads_kv, n, max_new, max_kv)
         if ws_bytes:
             ws = _new(q, (ws_bytes,), torch.uint8, stream)
-    rc = lib.calibatt_cache_attn_fwd(q.data_ptr(), heads_q, heads_kv, n, HEAD_DIM,
-                                     _SCALE if scale is None else scale, causal_unit, tok_start.data_ptr(),
-                                     kv_len.data_ptr(), batch, max_new, max_kv, table.data_ptr(), width, pages,
-                                     k8.data_ptr(), v8.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-                                     o.data_ptr(), None if lse is None else lse.data_ptr(),
-                                     None if ws is None else ws.data_ptr(), ws_bytes, _raw_stream(stream, index))
-    _check(rc, "calibatt_cache_attn_fwd")
+    rc = lib.calibatt_cache_attn_fwd(
+        q.data_ptr(), heads_q, heads_kv, n, HEAD_DIM, _SCALE if scale is None else scale, causal_unit,
+        tok_start.data_ptr(), kv_len.data_ptr(), batch, max_new, max_kv, table.data_ptr(), width, pages, k8.data_ptr(),
+        v8.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), o.data_ptr(), None if lse is None else lse.data_ptr(),
+        None if ws is None else ws.data_ptr(), ws_bytes,
+        _current_raw_stream(index) if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc, "calibatt_cache_attn_fwd")
     return o, lse
 
 
