@@ -71,6 +71,42 @@ __device__ __forceinline__ float score_factor(float row, float key_scale) {
   return f == 0.f ? 1.17549435e-38f : f;
 }
 
+constexpr float kStaleMax = 8.0f;      // log2 units: the running maximum moves only if it grows by more
+constexpr float kBigScore = 65536.0f;  // log2 units: beyond it the rounding of the row maximum counts
+
+// Units of an output that is summed over pages with different value scales
+// (one state for all rows): it is kept as O / (2^-6 * ref). A page whose scale
+// is 2^-6 .. 2 of the reference multiplies P by 2^6 times the ratio, in the
+// exponent, at no cost; outside that range the reference moves and O is
+// multiplied by what page() returns. With a running maximum up to 2^8 stale P
+// stays below 2^15, inside fp16, and weights down to 2^-24 keep a bit. The
+// reference is never more than 2^-70 below the largest scale met: O, at most
+// 2^55 in units of that (2^15 * 448 * 2^31 keys), stays finite.
+struct VRef {
+  float ref = 0.f, top = 0.f;
+  float vs = -1.f, log = 0.f, inv = 0.f;  // the page's: its scale, P's factor as a log2, 1 / that factor
+
+  __device__ __forceinline__ float page(float scale) {
+    if (scale == vs) return 1.f;
+    vs = scale;
+    if (scale == 0.f) scale = 1.17549435e-38f;
+    float ratio = 1.f;
+    if (ref == 0.f) {
+      ref = top = scale;
+    } else if (scale > 2.f * ref || scale < 0.015625f * ref) {
+      top = fmaxf(top, scale);
+      const float now = fmaxf(scale, top * 8.470329472543003e-22f);
+      ratio = ref / now;
+      ref = now;
+    }
+    const float f = scale / ref;
+    log = log2f(f) + 6.f;
+    inv = 0.015625f / f;
+    return ratio;
+  }
+  __device__ __forceinline__ float unit() const { return ref * 0.015625f; }
+};
+
 struct CacheAttnParams {
   const __nv_bfloat16* q;  // [heads_q][n][128]
   __nv_bfloat16* o;

@@ -21,9 +21,10 @@
 // K and V are fp16 operands: every e4m3 value is an fp16 value. A row of Q is
 // brought to fp16 by a power of two that puts its largest value into [1, 2)
 // (rounding only what is below 2^-14 of it, by 2^-25 at most); that power, the
-// page's key scale and the softmax scale multiply the fp32 score. P is rounded
-// to fp16 (2^-11 relative), and a page's P V is summed in fp32 from zero and
-// added to the output with the page's value scale.
+// page's key scale and the softmax scale multiply the fp32 score. The output
+// stays in units of a reference value scale and relative to a running maximum
+// that may be up to 2^8 stale, so most pages add their products to it and
+// touch it in no other way (VRef below); P is fp16.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -38,6 +39,7 @@
 #include "kernels.h"
 #include "ptx.cuh"
 #include "sched.cuh"
+#include "softmax.cuh"
 
 namespace calibatt {
 namespace {
@@ -339,6 +341,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
       }
     }
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    VRef vref;
     float acc[16][4];
 #pragma unroll
     for (int j = 0; j < 16; ++j)
@@ -421,36 +424,66 @@ __global__ void __launch_bounds__(kFewThreads, 2)
             }
           }
         }
-        // online softmax of the warp's 32 keys
-        float alpha[2];
+        // online softmax of the warp's 32 keys. The running maximum is the
+        // quad's (all lanes of a row agree) and moves only if it grew by more
+        // than 2^8, or to a first value.
+        const float o_ratio = vref.page(vs);
+        float ck[2], page_max[2];
+        bool need = o_ratio != 1.f;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          ck[i] = score_factor(c[i], ks);
+          float mx = fmaxf(max3f(sc[0][2 * i], sc[0][2 * i + 1], sc[1][2 * i]),
+                           max3f(sc[1][2 * i + 1], sc[2][2 * i], sc[2][2 * i + 1]));
+          mx = max3f(mx, sc[3][2 * i], sc[3][2 * i + 1]);
+          page_max[i] = mx;
+          // a maximum of -inf is replaced by whatever is seen first
+          need |= mx * ck[i] > m[i] + kStaleMax;
+          need |= fabsf(mx * ck[i]) > kBigScore && mx != -INFINITY;
+        }
+        float add[2] = {vref.log - (m[0] == -INFINITY ? 0.f : m[0]), vref.log - (m[1] == -INFINITY ? 0.f : m[1])};
+        if (__any_sync(0xffffffffu, need)) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float mx = page_max[i];
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            const float now = fmaxf(m[i], mx * ck[i]);
+            const float use = now == -INFINITY ? 0.f : now;
+            const float alpha = ex2_approx(m[i] - use);
+            m[i] = now;
+            l[i] *= alpha;
+            const float by = alpha * o_ratio;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              acc[j][2 * i] *= by;
+              acc[j][2 * i + 1] *= by;
+            }
+            // relative to the page's own largest score: scores of 2^24 and
+            // more would leave the rounding of mx * ck in the exponent
+            const float mx0 = mx == -INFINITY ? 0.f : mx;
+            add[i] = (mx == -INFINITY ? 0.f : mx * ck[i] - use) + vref.log;
+#pragma unroll
+            for (int nt = 0; nt < 4; ++nt) {
+              sc[nt][2 * i] -= mx0;
+              sc[nt][2 * i + 1] -= mx0;
+            }
+          }
+        }
         uint32_t pa[2][4];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          float mx = -INFINITY;
-#pragma unroll
-          for (int nt = 0; nt < 4; ++nt) mx = fmaxf(mx, fmaxf(sc[nt][2 * i], sc[nt][2 * i + 1]));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-          const float ck = score_factor(c[i], ks);
-          const float now = fmaxf(m[i], mx * ck);
-          const float use = now == -INFINITY ? 0.f : now;
-          alpha[i] = ex2_approx(m[i] - use);
-          // relative to the page's own largest score first: scores of 2^24 and
-          // more would leave the rounding of mx * ck in the exponent
-          const float off = mx * ck - use;
-          if (mx == -INFINITY) mx = 0.f;
           float sum = 0.f;
 #pragma unroll
           for (int nt = 0; nt < 4; ++nt) {
-            const float e0 = ex2_approx((sc[nt][2 * i] - mx) * ck + off);
-            const float e1 = ex2_approx((sc[nt][2 * i + 1] - mx) * ck + off);
+            const float e0 = ex2_approx(__fmaf_rn(sc[nt][2 * i], ck[i], add[i]));
+            const float e1 = ex2_approx(__fmaf_rn(sc[nt][2 * i + 1], ck[i], add[i]));
             sum += e0 + e1;
             pa[nt >> 1][(nt & 1) * 2 + i] = pack_half2(e0, e1);
           }
-          l[i] = l[i] * alpha[i] + sum;
-          m[i] = now;
+          l[i] = __fmaf_rn(sum, vref.inv, l[i]);
         }
-        // O = O * alpha + (P V) * vs, four output tiles at a time
+        // O += P V, four output tiles at a time
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
           uint32_t pair[2][2][2][2];  // k16 step, operand half, pair of channels, packed fp16 of two keys
@@ -466,13 +499,10 @@ __global__ void __launch_bounds__(kFewThreads, 2)
               pair[k][hf][1][1] = e4m3x2_to_half2(hi >> 16);
             }
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            float d[4] = {0.f, 0.f, 0.f, 0.f};
+          for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int k = 0; k < 2; ++k) mma_f16(d, pa[k], pair[k][0][j >> 1][j & 1], pair[k][1][j >> 1][j & 1]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[w * 4 + j][i] = acc[w * 4 + j][i] * alpha[i >> 1] + d[i] * vs;
-          }
+            for (int k = 0; k < 2; ++k)
+              mma_f16(acc[w * 4 + j], pa[k], pair[k][0][j >> 1][j & 1], pair[k][1][j >> 1][j & 1]);
         }
       }
       __syncwarp();
@@ -497,7 +527,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
 #pragma unroll
       for (int e = 0; e < 2; ++e)
 #pragma unroll
-        for (int j = 0; j < 16; ++j) sh.o[warp][g + 8 * i][32 * t + 16 * e + j] = acc[j][2 * i + e];
+        for (int j = 0; j < 16; ++j) sh.o[warp][g + 8 * i][32 * t + 16 * e + j] = acc[j][2 * i + e] * vref.unit();
     }
     named_bar_sync(1, 32 * kFewWarps);
     const bool complete = s.count == s.pages;

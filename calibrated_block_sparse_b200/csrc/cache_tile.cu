@@ -19,12 +19,8 @@
 // the conversion is one instruction per two values (with the scale in it, as
 // bf16, it took five and the converters, not the tensor core, set the pace).
 // Q is brought to fp16 by a power of two per row; that and the key scale
-// multiply the fp32 score. O is kept in units of a reference value scale: a
-// page whose value scale is 2^-6 .. 2 of it multiplies P by the ratio in the
-// exponent, at no cost, and where a page is outside that range the reference
-// moves and O is rescaled, as it is when the running maximum has grown. P is
-// fp16, 2^6 times the weight: with a maximum up to 2^8 stale and a ratio up to
-// 2 it stays below 2^15, and weights down to 2^-24 keep a bit.
+// multiply the fp32 score. P is fp16; O is kept in units of a reference value
+// scale (VRef), so a page's value scale costs nothing either.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -53,13 +49,6 @@ constexpr int kTileControlRegs = 40;
 constexpr int kTileRegs = 256 * kTileSoftmaxRegs + 128 * kTileConvertRegs + 128 * kTileControlRegs;
 static_assert(kTileRegs <= 128 * kTileThreads, "register split");
 constexpr int kTileRing = 5;
-constexpr float kTileRescale = 8.0f;   // log2 units: move the running max only if it grows by more
-constexpr float kBigScore = 65536.0f;  // log2 units: beyond it the rounding of the row max counts
-constexpr float kPScale = 6.0f;        // log2 of P's factor
-// A reference scale is never more than this below the largest value scale met:
-// O, at most 2^55 in units of that (2^15 * 448 * 2^31 keys), stays finite.
-constexpr float kMostShrink = 8.470329472543003e-22f;  // 2^-70
-
 struct TileBarriers {
   uint64_t ring_full[kTileRing];
   uint64_t ring_empty[kTileRing];
@@ -409,7 +398,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     // ---------------------------------------------------------- softmax
     warpgroup_regs_inc<kTileSoftmaxRegs>();
     float m_run = -INFINITY, l_run = 0.f;
-    float v_ref = 1.f, v_top = 1.f;  // units of O: 2^-kPScale v_ref
+    VRef vref;
     bool ok = true;  // warp-uniform
     const int s = warp >> 2;
     const int row = (warp & 3) * 32 + lane;
@@ -478,19 +467,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         if ((i & 31) < (kAlt ? 2 : 1)) win.advance(i & ~31, lane, p.status);
         const int id = __shfl_sync(0xffffffffu, win.id, i & 31);
         const float ck = score_factor(c_row, __shfl_sync(0xffffffffu, win.ks, i & 31));
-        float vs = __shfl_sync(0xffffffffu, win.vs, i & 31);
-        if (vs == 0.f) vs = 1.17549435e-38f;
-        // the reference of O's units (the same for all rows)
-        float o_ratio = 1.f;
-        if (turn == 0) {
-          v_ref = v_top = vs;
-        } else if (vs > 2.f * v_ref || vs < 0.015625f * v_ref) {
-          v_top = fmaxf(v_top, vs);
-          const float now = fmaxf(vs, v_top * kMostShrink);
-          o_ratio = v_ref / now;
-          v_ref = now;
-        }
-        const float f = vs / v_ref;
+        const float o_ratio = vref.page(__shfl_sync(0xffffffffu, win.vs, i & 31));
         if (!wait_warp(&bar.s_full[s], turn & 1)) break;
         tc_fence_after();
         const int key0 = (pg0 + i) * kPage;
@@ -508,21 +485,20 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const float page_max = mx * ck;
         const float m_new = fmaxf(m_run, page_max);
         // keep a stale running max unless it grew by more than the threshold
-        const bool need = m_run == -INFINITY || m_new > m_run + kTileRescale;
+        const bool need = m_run == -INFINITY || m_new > m_run + kStaleMax;
         const float m_prev = m_run;
         if (need) m_run = m_new;
         const float m_use = m_run == -INFINITY ? 0.f : m_run;
         const float alpha = need ? ex2_approx(m_prev - m_use) : 1.f;
         // exponent s * ck - m; for very large scores relative to the page's
         // own maximum first, whose rounding would otherwise stay in it
-        const float f_log = log2f(f) + kPScale;
-        float mul = ck, add = f_log - m_use;
+        float mul = ck, add = vref.log - m_use;
         if (__any_sync(0xffffffffu, fabsf(m_use) > kBigScore)) {
           const float mx0 = mx == -INFINITY ? 0.f : mx;
 #pragma unroll
           for (int e = 0; e < 128; ++e) sv[e >> 6][e & 63] = (sv[e >> 6][e & 63] - mx0) * ck;
           mul = 1.f;
-          add = page_max - m_use + f_log;
+          add = page_max - m_use + vref.log;
         }
         // O is rescaled before P is handed on. Its product with the page
         // before is complete: the commit that signalled S tracks every
@@ -556,7 +532,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           mbar_arrive(&bar.p_full[s][h]);
         }
         const float2 s01 = fadd2(a4[0], a4[1]), s23 = fadd2(a4[2], a4[3]);
-        l_run = l_run * alpha + ((s01.x + s01.y) + (s23.x + s23.y)) * (0.015625f / f);
+        l_run = l_run * alpha + ((s01.x + s01.y) + (s23.x + s23.y)) * vref.inv;
       }
       wait_warp(&bar.o_full[s], 0);
       // the ring is about to be reused: the other slot's products must be done too
@@ -566,14 +542,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 
     // ---------------------------------------------------------- results
     const bool done = ok && *abort_flag == 0;
-    float f0 = v_ref * 0.015625f, f1 = 0.f;
+    float f0 = vref.unit(), f1 = 0.f;
     // alternate: slot 1 hands its rows to slot 0 through the ring's memory,
     // [channel][row], which every MMA has finished reading
     float* joined = reinterpret_cast<float*>(smem + L::kRingOff);
     if constexpr (kAlt) {
       if (s == 1 && second && done) {
         bar.slot_ml[row] = make_float2(m_run, l_run);
-        const float unit = v_ref * 0.015625f;
+        const float unit = vref.unit();
 #pragma unroll
         for (int cc = 0; cc < 4; ++cc) {
           uint32_t o[32];
