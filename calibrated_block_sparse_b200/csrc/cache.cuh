@@ -7,6 +7,9 @@
 
 #include <cstdint>
 
+#include "calibatt.h"
+#include "ptx.cuh"
+
 namespace calibatt {
 
 constexpr int kPage = 128;  // tokens per cache page
@@ -42,6 +45,16 @@ __device__ __forceinline__ uint32_t e4m3_nan_bytes(uint32_t four) {
   return ((four & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
 }
 
+// Makes the NaN bytes of a word zero; nonzero if there was one.
+__device__ __forceinline__ uint32_t take_nan(uint32_t& w) {
+  const uint32_t hit = e4m3_nan_bytes(w);
+  w &= ~((hit >> 7) * 0xffu);
+  return hit;
+}
+
+// Writes to shared memory become visible to TMA and the tensor core.
+__device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
 // Two packed e4m3 values to packed fp16: exact, NaN stays NaN.
 __device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t two) {
   uint32_t r;
@@ -59,10 +72,10 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// One row's power of two: 2^-x for a largest magnitude in [2^x, 2^(x+1)).
-__device__ __forceinline__ float row_shrink(float amax) {
+// One row's power of two: 2^(to - x) for a largest magnitude in [2^x, 2^(x+1)).
+__device__ __forceinline__ float row_shrink(float amax, int to) {
   const int x = (__float_as_int(amax) >> 23) - 127;  // amax >= 0; NaN and inf: 128
-  return x >= 128 ? 1.f : __int_as_float((min(max(-x, -126), 126) + 127) << 23);
+  return x >= 128 ? 1.f : __int_as_float((min(max(to - x, -126), 126) + 127) << 23);
 }
 
 // Factor of a raw score, never 0 (a masked score is -inf, and -inf * 0 is NaN).
@@ -71,21 +84,21 @@ __device__ __forceinline__ float score_factor(float row, float key_scale) {
   return f == 0.f ? 1.17549435e-38f : f;
 }
 
-constexpr float kStaleMax = 8.0f;      // log2 units: the running maximum moves only if it grows by more
-constexpr float kBigScore = 65536.0f;  // log2 units: beyond it the rounding of the row maximum counts
-
 // Units of an output that is summed over pages with different value scales
-// (one state for all rows): it is kept as O / (2^-6 * ref). A page whose scale
-// is 2^-6 .. 2 of the reference multiplies P by 2^6 times the ratio, in the
-// exponent, at no cost; outside that range the reference moves and O is
-// multiplied by what page() returns. With a running maximum up to 2^8 stale P
-// stays below 2^15, inside fp16, and weights down to 2^-24 keep a bit. The
-// reference is never more than 2^-70 below the largest scale met: O, at most
-// 2^55 in units of that (2^15 * 448 * 2^31 keys), stays finite.
+// (one state for all rows): it is kept as O / (2^-kLog * ref). A page whose
+// scale is 2^kLow .. 2 of the reference multiplies P by 2^kLog times the
+// ratio, in the exponent, at no cost; outside that range the reference moves
+// and O is multiplied by what page() returns. kLog leaves P room above 1 for a
+// running maximum that is up to kStale (a power of two) behind; kLow keeps
+// weights down to 2^-24 of the largest. The reference is never more than 2^-70
+// below the largest scale met: O, at most 2^55 in units of that
+// (2^15 * 448 * 2^31 keys), stays finite.
+template <int kLog, int kLow>
 struct VRef {
   float ref = 0.f, top = 0.f;
   float vs = -1.f, log = 0.f, inv = 0.f;  // the page's: its scale, P's factor as a log2, 1 / that factor
 
+  static constexpr float kUnit = 1.f / (1 << kLog);
   __device__ __forceinline__ float page(float scale) {
     if (scale == vs) return 1.f;
     vs = scale;
@@ -93,19 +106,36 @@ struct VRef {
     float ratio = 1.f;
     if (ref == 0.f) {
       ref = top = scale;
-    } else if (scale > 2.f * ref || scale < 0.015625f * ref) {
+    } else if (scale > 2.f * ref || scale * (1 << -kLow) < ref) {
       top = fmaxf(top, scale);
       const float now = fmaxf(scale, top * 8.470329472543003e-22f);
       ratio = ref / now;
       ref = now;
     }
     const float f = scale / ref;
-    log = log2f(f) + 6.f;
-    inv = 0.015625f / f;
+    log = log2f(f) + kLog;
+    inv = kUnit / f;
     return ratio;
   }
-  __device__ __forceinline__ float unit() const { return ref * 0.015625f; }
+  __device__ __forceinline__ float unit() const { return ref * kUnit; }
 };
+
+// Tile t of the ring's order -> (V?, page of the range): K0 V0 K1 V1 ..., or
+// with the next page's K before a page's V: K0 K1 V0 K2 V1 ...
+template <bool kAhead>
+__device__ __forceinline__ void ring_tile(int t, int np, bool& is_v, int& page) {
+  if (!kAhead) {
+    is_v = t & 1;
+    page = t >> 1;
+  } else if (t & 1) {
+    page = (t + 1) >> 1;
+    is_v = page >= np;
+    if (is_v) page = (t - 1) >> 1;
+  } else {
+    is_v = t > 0;
+    page = t > 0 ? (t >> 1) - 1 : 0;
+  }
+}
 
 struct CacheAttnParams {
   const __nv_bfloat16* q;  // [heads_q][n][128]
@@ -136,6 +166,46 @@ __device__ __forceinline__ int visible(int pos, int len, int unit) {
   return static_cast<int>(end < 0 ? 0 : end > len ? len : end);
 }
 
+// Page numbers of 32 consecutive pages of a stream, one per lane, fetched a
+// chunk of 32 ahead; kScales: with their key and value scales. A page outside
+// the pool is reported and gets id -1, and so does one behind the last token.
+template <bool kScales>
+struct PageWindow {
+  const CacheAttnParams& p;
+  const int32_t* table;
+  int head, count;
+  int id = -1, id_next = -1;
+  float ks = 1.f, vs = 1.f, ks_next = 1.f, vs_next = 1.f;
+
+  // `pages` pages of stream b from its page pg on
+  __device__ __forceinline__ PageWindow(const CacheAttnParams& params, int b, int key_head, int pg, int pages, int len)
+      : p(params), table(params.table + static_cast<int64_t>(b) * params.table_stride + pg), head(key_head) {
+    count = min(pages, (len + kPage - 1) / kPage - pg);
+  }
+  __device__ __forceinline__ void fetch(int at, int* status) {
+    id_next = -1;
+    ks_next = vs_next = 1.f;
+    if (at < count) {
+      id_next = __ldg(table + at);
+      if (id_next < 0 || id_next >= p.n_pages) {
+        record_error(status, CALIBATT_ERR_CSR);
+        id_next = -1;
+      } else if (kScales) {
+        const int64_t i = static_cast<int64_t>(id_next) * p.heads_kv + head;
+        ks_next = __ldg(p.k_scale + i);
+        vs_next = __ldg(p.v_scale + i);
+      }
+    }
+  }
+  // call before using page i = 0, 32, 64, ...
+  __device__ __forceinline__ void advance(int i, int lane, int* status) {
+    id = id_next;
+    ks = ks_next;
+    vs = vs_next;
+    fetch(i + 32 + lane, status);
+  }
+};
+
 // Few query rows (up to 16 that share a key head): the streams' pages, key
 // head by key head, cut into equal shares for `ctas` CTAs; or, with `whole`, a
 // CTA for each key head of each stream.
@@ -143,8 +213,9 @@ constexpr int kFewRows = 16;
 struct FewPlan {
   bool whole;
   int ctas;
+  int rows;  // the most that a key head has
 };
-FewPlan few_plan(int batch, int heads_kv, int64_t pages, int sms);
+FewPlan few_plan(int batch, int heads_kv, int rows, int64_t pages, int sms);
 size_t few_workspace_bytes(const FewPlan& plan);
 int launch_cache_attn_few(const CacheAttnParams& p, const FewPlan& plan, void* ws, cudaStream_t stream);
 

@@ -87,7 +87,7 @@ CachePlan cache_plan(int batch, int heads_q, int heads_kv, int n, int max_new, i
   const int sms = sm_count();
   if (c.few) {
     c.tiles = c.splits = 1;
-    c.fp = few_plan(batch, heads_kv, pages, sms);
+    c.fp = few_plan(batch, heads_kv, static_cast<int>(rows), pages, sms);
     return c;
   }
   const int tile = c.alternate ? 128 : 256;

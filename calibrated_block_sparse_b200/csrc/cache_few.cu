@@ -4,30 +4,33 @@
 // Bound by reading the cache once. Its pages are one list, stream by stream,
 // key head by key head, cut into equal shares: two CTAs per SM, whatever the
 // streams' lengths are (they are read on the device), so no SM waits for a
-// long stream. A CTA (4 warps) walks its share; each warp takes 32 of a page's
-// 128 keys, brings their K and V (8 KB) by TMA into a ring of its own, two
-// pages ahead, and keeps its own running softmax: the warps meet only when a
-// (stream, key head) or the share ends, and are joined there. (With a fifth
-// warp as the producer the registers of three warps would share one of the
-// SM's four partitions: 168 a thread instead of 255, and the rest spilled.)
-// A stretch that is not all of its stream's pages leaves maximum, sum and
-// unnormalised output in the workspace, and cache_few_join_kernel joins them.
+// long stream. A stretch of a share that is not all of its stream's pages
+// leaves maximum, sum and unnormalised output in the workspace, and
+// cache_few_join_kernel joins them.
 //
-// Products are mma.sync with the 16 rows as M. Fragments are read from shared
-// memory 16 bytes at a time: the order of the contracted channels, and of the
-// output channels, is free as long as both operands agree, so it is chosen to
-// make a lane's share 16 consecutive bytes of a row.
+// The tensor core multiplies the cache's bytes as they are: a page is the
+// 128-row operand A, K as it lies in memory and V transposed, and the few rows
+// are operand B:
+//   S^T [key][row] = K Q^T,   O^T [channel][row] += V^T P^T   (kind::f8f6f4)
+// so nothing of the cache passes through registers (converting it to fp16
+// there, for mma.sync, took ~500 ALU instructions per warp and 8 KB and held
+// the kernel at 52 % of the DRAM rate). Q and P are written as sums of e5m2
+// values, in columns of their own that are added up in fp32: three parts of 3
+// significant bits hold a bf16 value's 8 exactly, four parts hold P to 2^-12.
+// e5m2 spans 2^-16 .. 2^15, so a row of Q, scaled by a power of two to a
+// largest value in [2^13, 2^14), is exact down to 2^-22 of it and within 2^-31
+// of it below, and weights keep a bit down to 2^-24 of the largest.
 //
-// K and V are fp16 operands: every e4m3 value is an fp16 value. A row of Q is
-// brought to fp16 by a power of two that puts its largest value into [1, 2)
-// (rounding only what is below 2^-14 of it, by 2^-25 at most); that power, the
-// page's key scale and the softmax scale multiply the fp32 score. The output
-// stays in units of a reference value scale and relative to a running maximum
-// that may be up to 2^8 stale, so most pages add their products to it and
-// touch it in no other way (VRef below); P is fp16.
+// CTA (192 threads):
+//   warps 0-3  softmax; thread = key of the page = TMEM lane of S^T, and
+//              channel = TMEM lane of O^T at the end
+//   warp  4    TMA producer: K and V tiles (16 KB) into a 5-stage ring
+//   warp  5    MMA issuer: S^T of the next page before O^T of this one
+// The running maximum of a row moves only if it grew by more than 2^4, which a
+// page finds out with one vote of the four warps.
 #include <cuda.h>
 #include <cuda_bf16.h>
-#include <cuda_fp16.h>
+#include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -39,55 +42,107 @@
 #include "kernels.h"
 #include "ptx.cuh"
 #include "sched.cuh"
-#include "softmax.cuh"
 
 namespace calibatt {
 namespace {
 
-constexpr int kFewWarps = 4;
-constexpr int kFewThreads = 32 * kFewWarps;
-constexpr int kFewStages = 2;
-constexpr int kSliceKeys = kPage / kFewWarps;
-constexpr int kSliceBytes = kSliceKeys * 128;
+constexpr int kFewThreads = 192;
+constexpr int kFewRing = 5;
+constexpr int kPageBytes = kPage * 128;
 constexpr int kFewPartFloats = kFewRows * 128 + 2 * kFewRows;  // a partial result: O, then maximum and sum per row
+constexpr float kFewStale = 4.0f;                              // log2 units
+constexpr int kQParts = 3, kPParts = 4;
 
-__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+// Columns (N) of a product with `parts` columns per row: a multiple of 16.
+__host__ __device__ constexpr int few_cols(int rows, int parts) { return (rows * parts + 15) / 16 * 16; }
+
+struct FewBarriers {
+  uint64_t full[kFewRing], empty[kFewRing];
+  uint64_t q_full;
+  uint64_t s_full[2], p_full[2];  // per buffer of S^T and P^T
+  uint64_t pv_done;               // every page's O^T product
+  uint64_t o_full;                // the last one of a stretch
+  uint64_t mma_done;
+  uint32_t tmem_base;
+  int abort;
+  int nan_seen;
+  int limit[kFewRows];            // keys that a row sees
+  float c[kFewRows];              // a raw score's factor, without the key scale
+  float top[4][kFewRows];         // per warp, of a page
+  float sum[4][kFewRows];         // per warp, at a stretch's end
+};
+
+struct FewLayout {
+  static constexpr int kRingOff = 0;
+  static constexpr int kQOff = kFewRing * kPageBytes;                  // Q^T's operand: few_cols rows of 128 channels
+  static constexpr int kPOff = kQOff + few_cols(kFewRows, kQParts) * 128;  // P^T's: few_cols rows of 128 keys, two buffers
+  static constexpr int kPBytes = few_cols(kFewRows, kPParts) * 128;
+  static constexpr int kBarOff = kPOff + 2 * kPBytes;
+  static constexpr int kDynSmem = kBarOff + static_cast<int>(sizeof(FewBarriers)) + 1024;
+};
+// two CTAs on an SM (228 KB, of which each takes 1 KB more)
+static_assert(2 * (FewLayout::kDynSmem + 1024) <= 233472, "shared memory budget");
+
+// Tensor memory: S^T in two buffers of up to 48 columns, O^T in up to 64.
+constexpr uint32_t kFewCols = 256, kSBuf = 64, kOCol = 128;
+
+// kind::f8f6f4, A e4m3, B e5m2, fp32 accumulation, M = 128; V is A with its
+// channels (M) contiguous.
+__host__ __device__ constexpr uint32_t idesc_f8(int N, bool a_mn_major) {
+  return (1u << 4) | (0u << 7) | (1u << 10) | ((a_mn_major ? 1u : 0u) << 15) | (static_cast<uint32_t>(N >> 3) << 17) |
+         (8u << 24);
+}
+
+__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                       uint32_t accumulate) {
   asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
 }
 
-// Makes the NaN bytes of a word zero; nonzero if there was one.
-__device__ __forceinline__ uint32_t take_nan(uint32_t& w) {
-  const uint32_t hit = e4m3_nan_bytes(w);
-  w &= ~((hit >> 7) * 0xffu);
-  return hit;
+// 2D tiled load of one box into shared memory, completing on `bar`.
+__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y)
+      : "memory");
 }
 
-__device__ __forceinline__ uint32_t word_of(const uint4& v, int i) {
-  return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+// Vote of the four softmax warps.
+__device__ __forceinline__ bool vote_128(bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, 2, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(x))
+      : "memory");
+  return r != 0;
 }
 
-// Loads a lane's 2 x 16 channels of a query row and returns their largest magnitude.
-__device__ __forceinline__ float load_q_row(const __nv_bfloat16* row, int t, float (&x)[32]) {
-  float amax = 0.f;
+// The kParts columns of every row, added up: column part * RB + r, of one lane.
+template <int RB, int kParts>
+__device__ __forceinline__ void tmem_rows(uint32_t taddr, float (&x)[RB]) {
 #pragma unroll
-  for (int l = 0; l < 2; ++l)
+  for (int r = 0; r < RB; ++r) x[r] = 0.f;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint4 v = *reinterpret_cast<const uint4*>(row + l * 64 + t * 16 + i * 8);
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  for (int i = 0; i < kParts * RB; i += 16) {
+    uint32_t c[16];
+    tmem_ld16_wait(taddr + i, c);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        x[l * 16 + i * 8 + 2 * j] = __uint_as_float(w[j] << 16);
-        x[l * 16 + i * 8 + 2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-      }
-    }
-#pragma unroll
-  for (int i = 0; i < 32; ++i) amax = fmaxf(amax, fabsf(x[i]));
-  return amax;
+    for (int e = 0; e < 16; ++e)
+      if (i + e < kParts * RB) x[(i + e) % RB] += __uint_as_float(c[e]);
+  }
+}
+
+// The leading three significant bits of x, exactly an e5m2 value down to 2^-14.
+__device__ __forceinline__ float three_bits(float x) { return __uint_as_float(__float_as_uint(x) & 0xffe00000u); }
+
+__device__ __forceinline__ uint32_t to_e5m2x2(float lo, float hi) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E5M2);
 }
 
 // Normalises and stores a row's four channels of a lane; no key seen: 0 and -inf.
@@ -99,24 +154,6 @@ __device__ __forceinline__ void store_row(const CacheAttnParams& p, int64_t at, 
   if (!some) w = make_uint2(0, 0);
   *reinterpret_cast<uint2*>(p.o + at * 128 + lane * 4) = w;
   if (p.lse && lane == 0) p.lse[at] = some ? (mx + log2f(sum)) * kLn2 : -INFINITY;
-}
-
-struct FewShared {
-  uint64_t full[kFewWarps][kFewStages];
-  int abort;
-  float m[kFewWarps][kFewRows], l[kFewWarps][kFewRows];
-  alignas(16) float o[kFewWarps][kFewRows][132];  // padded: lanes of a quad write 32 channels apart
-};
-constexpr int kFewRingBytes = kFewWarps * kFewStages * 2 * kSliceBytes;
-constexpr int kFewDynSmem = kFewRingBytes + static_cast<int>(sizeof(FewShared)) + 1024;
-
-// 2D tiled load of one box into shared memory, completing on `bar`.
-__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y)
-      : "memory");
 }
 
 // Pages of stream b that its last new token sees (at least one, so that rows
@@ -224,346 +261,379 @@ struct Walk {
   }
 };
 
-template <bool SW>
+// Where V of page i of a stretch of `count` is in the ring's order.
+__device__ __forceinline__ uint32_t v_tile(int i, int count) { return i + 1 < count ? 2 * i + 2 : 2 * i + 1; }
+
+// Whether a row that sees `limit` keys has a NaN value in this channel among
+// the stretch's pages that not every row sees whole.
+__device__ __forceinline__ bool stretch_nan(const CacheAttnParams& p, const Stretch& s, int limit, int least,
+                                            int channel) {
+  const int32_t* table = p.table + static_cast<int64_t>(s.b) * p.table_stride;
+  for (int k = max(least / kPage, s.pg) * kPage; k < min(limit, (s.pg + s.count) * kPage); ++k) {
+    const int id = __ldg(table + k / kPage);
+    if (id < 0 || id >= p.n_pages) continue;
+    if ((p.v8[((static_cast<int64_t>(id) * p.heads_kv + s.head) * kPage + k % kPage) * 128 + channel] & 0x7f) == 0x7f)
+      return true;
+  }
+  return false;
+}
+
+template <bool SW, int RB>  // RB: rows that registers and columns are laid out for
 __global__ void __launch_bounds__(kFewThreads, 2)
     cache_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                      const __grid_constant__ CacheAttnParams p, bool whole, float* part) {
+  using L = FewLayout;
+  constexpr int kQCols = few_cols(RB, kQParts), kPCols = few_cols(RB, kPParts);
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
-  uint8_t* ring = smem_raw + (((raw + 1023u) & ~1023u) - raw);
-  FewShared& sh = *reinterpret_cast<FewShared*>(ring + kFewRingBytes);
-  volatile int* abort_flag = &sh.abort;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+  const uint32_t sbase = smem_u32(smem);
+  FewBarriers& bar = *reinterpret_cast<FewBarriers*>(smem + L::kBarOff);
+  volatile int* abort_flag = &bar.abort;
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
+  const int lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kFewWarps * kFewStages; ++i) mbar_init(&sh.full[0][0] + i, 1);
-    sh.abort = 0;
+    for (int i = 0; i < kFewRing; ++i) {
+      mbar_init(&bar.full[i], 1);
+      mbar_init(&bar.empty[i], 1);
+    }
+    mbar_init(&bar.q_full, 128);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar.s_full[i], 1);
+      mbar_init(&bar.p_full[i], 128);
+    }
+    mbar_init(&bar.pv_done, 1);
+    mbar_init(&bar.o_full, 1);
+    mbar_init(&bar.mma_done, 1);
+    bar.abort = 0;
+    bar.nan_seen = 0;
     fence_barrier_init();
   }
+  if (warp == 5) tmem_alloc(&bar.tmem_base, kFewCols);
+  tc_fence_before();
   __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, bar.tmem_base, 0);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // streams that do not fit are reported once
-  if (blockIdx.x == 0 && warp == 0)
+  if (blockIdx.x == 0 && warp == 4)
     for (int b = lane; b < p.batch; b += 32) {
       const Stream st = stream_of(p.tok_start, p.kv_len, b, p.n, p.table_stride);
       if (st.bad || st.n_new > p.max_new || st.n_new * static_cast<int64_t>(p.group) > kFewRows)
         record_error(p.status, CALIBATT_ERR_CSR);
     }
 
-  Walk walk, ahead;
+  Walk walk;
   walk.start(p, whole, lane);
-  ahead = walk;
-
-  // the warp's loads, kFewStages pages ahead of its products
-  uint8_t* slices = ring + warp * kFewStages * 2 * kSliceBytes;
-  uint64_t* full = sh.full[warp];
-  Stretch to;
-  int to_page = 0, to_ids = -1, to_next = -1, issued = 0;
-  auto page_id = [&](const Stretch& s, int i) {
-    return i < s.count && (s.pg + i) * kPage + warp * kSliceKeys < s.st.len
-               ? __ldg(p.table + static_cast<int64_t>(s.b) * p.table_stride + s.pg + i)
-               : -1;
-  };
-  bool more = ahead.next(p, to);
-  if (more) to_next = page_id(to, lane);
-  auto issue = [&]() {
-    if (!more) return;
-    if ((to_page & 31) == 0) {
-      to_ids = to_next;
-      to_next = page_id(to, to_page + 32 + lane);
-    }
-    const int id = __shfl_sync(0xffffffffu, to_ids, to_page & 31);
-    if (lane == 0) {
-      uint64_t* bar = full + issued % kFewStages;
-      if (id >= 0 && id < p.n_pages) {
-        uint8_t* dst = slices + (issued % kFewStages) * 2 * kSliceBytes;
-        const int y = (id * p.heads_kv + to.head) * kPage + warp * kSliceKeys;
-        mbar_arrive_expect_tx(bar, 2 * kSliceBytes);
-        tma_load_2d(dst, &tm_k, bar, 0, y);
-        tma_load_2d(dst + kSliceBytes, &tm_v, bar, 0, y);
-      } else {
-        mbar_arrive(bar);  // nothing to read: the products skip the page as well
-      }
-    }
-    ++issued;
-    if (++to_page == to.count) {
-      to_page = 0;
-      more = ahead.next(p, to);
-      if (more) to_next = page_id(to, lane);
-    }
-  };
-  for (int i = 0; i < kFewStages; ++i) issue();
-
-  const int g = lane >> 2, t = lane & 3;
-  int used = 0, seg = 0;
   Stretch s;
-  bool ok = true;  // warp-uniform
-  while (walk.next(p, s)) {
-    const int rows = s.st.n_new * p.group;
-    // pages' scales, one per lane, 32 pages at a time
-    const int32_t* table = p.table + static_cast<int64_t>(s.b) * p.table_stride;
-    int ids = -1, ids_next = -1;
-    float kss = 0.f, vss = 0.f, kss_next = 0.f, vss_next = 0.f;
-    auto fetch = [&](int i) {
-      ids_next = i < s.count && s.st.len > (s.pg + i) * kPage ? __ldg(table + s.pg + i) : -1;
-      if (ids_next >= p.n_pages) ids_next = -1;
-      if (ids_next < 0) {
-        if (i < s.count && s.st.len > (s.pg + i) * kPage) record_error(p.status, CALIBATT_ERR_CSR);
-        ids_next = -1;
-        return;
-      }
-      const int64_t at = static_cast<int64_t>(ids_next) * p.heads_kv + s.head;
-      kss_next = __ldg(p.k_scale + at);
-      vss_next = __ldg(p.v_scale + at);
-    };
-    fetch(lane);
-    // rows g and g + 8: token r / group, query head head * group + r % group
-    int limit[2];
-    float c[2];
-    uint32_t qa[8][4];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = min(g + 8 * i, rows - 1);
-      const int tok = r / p.group, h = s.head * p.group + r % p.group;
-      limit[i] = g + 8 * i < rows ? visible(s.st.len - s.st.n_new + tok, s.st.len, p.unit) : 0;
-      float x[32];
-      float amax = load_q_row(p.q + (static_cast<int64_t>(h) * p.n + s.st.t0 + tok) * 128, t, x);
-      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-      const float shrink = row_shrink(amax);
-      c[i] = p.scale_log2 / shrink;
-#pragma unroll
-      for (int ks = 0; ks < 8; ++ks) {
-        // step ks: slots 2t, 2t+1 hold channels 4w, 4w+1 of the lane's sixteen, slots 2t+8, 2t+9 the next two
-        const int at = (ks >> 2) * 16 + (ks & 3) * 4;
-        qa[ks][i] = pack_half2(x[at] * shrink, x[at + 1] * shrink);
-        qa[ks][2 + i] = pack_half2(x[at + 2] * shrink, x[at + 3] * shrink);
+  if (warp == 4) {
+    // ---------------------------------------------------------- TMA producer
+    uint32_t stage = 0, phase = 0;
+    int used = 0;
+    bool ok = true;
+    while (ok && walk.next(p, s)) {
+      PageWindow<false> win(p, s.b, s.head, s.pg, s.count, s.st.len);
+      win.fetch(lane, p.status);
+      int id_now = -1, id_before = -1, k_at = 0;
+      for (int t = 0; t < 2 * s.count && ok; ++t) {
+        bool is_v;
+        int i, id;
+        ring_tile<true>(t, s.count, is_v, i);
+        if (!is_v) {
+          if ((i & 31) == 0) win.advance(i, lane, p.status);
+          id_before = id_now;
+          id_now = id = __shfl_sync(0xffffffffu, win.id, i & 31);
+          k_at = i;
+        } else {
+          id = k_at == i ? id_now : id_before;
+        }
+        if (lane == 0) {
+          ok = mbar_wait<SW>(&bar.empty[stage], phase ^ 1, abort_flag, p.status, p.wait_limit_ns);
+          if (ok) {
+            if (id >= 0) {
+              mbar_arrive_expect_tx(&bar.full[stage], kPageBytes);
+              tma_load_2d(smem + L::kRingOff + stage * kPageBytes, is_v ? &tm_v : &tm_k, &bar.full[stage], 0,
+                          (id * p.heads_kv + s.head) * kPage);
+            } else {
+              mbar_arrive(&bar.full[stage]);  // nothing to read: the softmax warps leave the page out
+            }
+            ++used;
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (++stage == kFewRing) {
+          stage = 0;
+          phase ^= 1;
+        }
       }
     }
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-    VRef vref;
-    float acc[16][4];
-#pragma unroll
-    for (int j = 0; j < 16; ++j)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[j][i] = 0.f;
-
-    for (int pi = 0; pi < s.count; ++pi) {
-      if ((pi & 31) == 0) {
-        ids = ids_next;
-        kss = kss_next;
-        vss = vss_next;
-        fetch(pi + 32 + lane);
+    // no copy may still be landing when the CTA leaves
+    if (lane == 0)
+      for (int i = used > kFewRing ? used - kFewRing : 0; i < used; ++i) {
+        volatile int never = 0;
+        mbar_wait(&bar.full[i % kFewRing], (i / kFewRing) & 1, &never, p.status);
       }
-      const int id = __shfl_sync(0xffffffffu, ids, pi & 31);
-      const float ks = __shfl_sync(0xffffffffu, kss, pi & 31), vs = __shfl_sync(0xffffffffu, vss, pi & 31);
-      const int stage = used % kFewStages;
-      if (ok)
-        ok = __all_sync(0xffffffffu, mbar_wait<SW>(full + stage, (used / kFewStages) & 1, abort_flag, p.status,
-                                                   p.wait_limit_ns));
-      const int key0 = (s.pg + pi) * kPage + warp * kSliceKeys;
-      if (ok && id >= 0 && key0 < s.st.len) {
-        const uint8_t* kp = slices + stage * 2 * kSliceBytes;
-        const uint8_t* vp = kp + kSliceBytes;
-        // 16-byte chunk j of row r is at chunk j ^ (r & 7) (128-byte swizzle)
-        // S = Q K^T
-        float sc[4][4];
-#pragma unroll
-        for (int nt = 0; nt < 4; ++nt) {
-          const uint8_t* row = kp + (nt * 8 + g) * 128;
-          const uint4 kw[2] = {*reinterpret_cast<const uint4*>(row + ((t ^ g) << 4)),
-                               *reinterpret_cast<const uint4*>(row + (((4 + t) ^ g) << 4))};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) sc[nt][i] = 0.f;
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const uint32_t w = word_of(kw[k >> 2], k & 3);
-            mma_f16(sc[nt], qa[k], e4m3x2_to_half2(w & 0xffffu), e4m3x2_to_half2(w >> 16));
-          }
+  } else if (warp == 5) {
+    // ---------------------------------------------------------- MMA issuer
+    if (lane == 0) {
+      uint32_t stage = 0, phase = 0, turn = 0, stretch = 0;
+      const uint64_t ring0 = smem_desc_sw128(sbase + L::kRingOff, 16, 1024);
+      const uint64_t q0 = smem_desc_sw128(sbase + L::kQOff, 16, 1024);
+      const uint64_t p0 = smem_desc_sw128(sbase + L::kPOff, 16, 1024);
+      constexpr uint32_t kIdescS = idesc_f8(kQCols, false), kIdescO = idesc_f8(kPCols, true);
+      bool ok = true;
+      auto wait = [&](uint64_t* b, uint32_t parity) {
+        return mbar_wait<SW>(b, parity, abort_flag, p.status, p.wait_limit_ns);
+      };
+      auto ring_next = [&]() {
+        mma_commit(&bar.empty[stage]);
+        if (++stage == kFewRing) {
+          stage = 0;
+          phase ^= 1;
         }
-        uint4 vw[2][4];
+      };
+      // S^T of the page that is `turn` number t: 4 steps of 32 channels (32 bytes of a row)
+      auto issue_s = [&](uint32_t t) -> bool {
+        if (!wait(&bar.full[stage], phase)) return false;
+        tc_fence_after();
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
+        for (int k = 0; k < 4; ++k)
+          mma_f8(tmem + (t & 1) * kSBuf, ring0 + stage * (kPageBytes >> 4) + k * 2, q0 + k * 2, kIdescS, k > 0);
+        mma_commit(&bar.s_full[t & 1]);
+        ring_next();
+        return true;
+      };
+      while (ok && walk.next(p, s)) {
+        if (!(ok = wait(&bar.q_full, stretch & 1))) break;
+        ++stretch;
+        if (!(ok = issue_s(turn))) break;
+        for (int i = 0; i < s.count; ++i, ++turn) {
+          if (i + 1 < s.count && !(ok = issue_s(turn + 1))) break;
+          if (!(ok = wait(&bar.p_full[turn & 1], (turn >> 1) & 1))) break;
+          if (!(ok = wait(&bar.full[stage], phase))) break;
+          tc_fence_after();
+          // 4 steps of 32 keys: 32 rows of V (4 KB), 32 bytes of a row of P^T
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int r = k * 16 + 2 * t + (i & 1) + (i >> 1) * 8;
-            vw[k][i] = *reinterpret_cast<const uint4*>(vp + r * 128 + ((g ^ (r & 7)) << 4));
-          }
-        const bool all = __all_sync(0xffffffffu, key0 + 32 <= limit[0] && key0 + 32 <= limit[1]);
-        if (!all) {
-#pragma unroll
-          for (int nt = 0; nt < 4; ++nt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (key0 + nt * 8 + 2 * t + (i & 1) >= limit[i >> 1]) sc[nt][i] = -INFINITY;
-          // slots that no token has reached may hold anything. A product
-          // takes every key for every row, and 0 * NaN is NaN: a NaN value
-          // of a key that some rows do not see is taken out of the product
-          // and put into the rows that see it.
-          uint32_t nan = 0;
-#pragma unroll
-          for (int k = 0; k < 2; ++k)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              if (key0 + k * 16 + 2 * t + (i & 1) + (i >> 1) * 8 >= s.st.len) vw[k][i] = make_uint4(0, 0, 0, 0);
-              nan |= take_nan(vw[k][i].x) | take_nan(vw[k][i].y);
-              nan |= take_nan(vw[k][i].z) | take_nan(vw[k][i].w);
-            }
-          if (__any_sync(0xffffffffu, nan != 0)) {
-            for (int key = 0; key < 32 && key0 + key < s.st.len; ++key) {
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const uint8_t* row = vp + key * 128 + (((2 * t + e) ^ (key & 7)) << 4);
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-                  if ((row[j] & 0x7f) == 0x7f) {
-                    if (key0 + key < limit[0]) acc[j][e] = NAN;
-                    if (key0 + key < limit[1]) acc[j][2 + e] = NAN;
-                  }
-              }
-            }
-          }
+          for (int k = 0; k < 4; ++k)
+            mma_f8(tmem + kOCol, ring0 + stage * (kPageBytes >> 4) + k * (4096 >> 4),
+                   p0 + (turn & 1) * (L::kPBytes >> 4) + k * 2, kIdescO, (i > 0 || k > 0) ? 1u : 0u);
+          mma_commit(&bar.pv_done);
+          if (i + 1 == s.count) mma_commit(&bar.o_full);
+          ring_next();
         }
-        // online softmax of the warp's 32 keys. The running maximum is the
-        // quad's (all lanes of a row agree) and moves only if it grew by more
-        // than 2^8, or to a first value.
-        const float o_ratio = vref.page(vs);
-        float ck[2], page_max[2];
+      }
+      // every issued MMA has finished before tensor memory is released
+      mma_commit(&bar.mma_done);
+      volatile int never = 0;
+      mbar_wait(&bar.mma_done, 0, &never, p.status);
+    }
+  } else {
+    // ---------------------------------------------------------- softmax
+    const int key = threadIdx.x;  // of a page; channel of the output
+    const uint32_t lane_off = static_cast<uint32_t>(warp * 32) << 16;
+    uint32_t turn = 0;
+    int seg = 0;
+    // after a failed wait the warps go on without waiting or touching tensor
+    // memory, so that they still meet at every barrier
+    bool ok = true;  // warp-uniform
+    auto wait_warp = [&](uint64_t* b, uint32_t parity) -> bool {
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait<SW>(b, parity, abort_flag, p.status, p.wait_limit_ns));
+      return ok;
+    };
+    uint32_t stage_v = 0;  // ring stages passed: V of this page, for the pages that are cleaned
+    while (walk.next(p, s)) {
+      const int rows = s.st.n_new * p.group;
+      PageWindow<true> win(p, s.b, s.head, s.pg, s.count, s.st.len);
+      win.fetch(lane, p.status);
+      // the rows of Q as operand B: row part * RB + r, channels contiguous
+      for (int r = warp; r < rows; r += 4) {
+        const int tok = r / p.group, h = s.head * p.group + r % p.group;
+        const uint2 w = *reinterpret_cast<const uint2*>(
+            p.q + (static_cast<int64_t>(h) * p.n + s.st.t0 + tok) * 128 + lane * 4);
+        float x[4] = {__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
+                      __uint_as_float(w.y & 0xffff0000u)};
+        float amax = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        const float shrink = row_shrink(amax, 13);
+        if (lane == 0) {
+          bar.c[r] = p.scale_log2 / shrink;
+          bar.limit[r] = visible(s.st.len - s.st.n_new + tok, s.st.len, p.unit);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] *= shrink;
+#pragma unroll
+        for (int part_i = 0; part_i < kQParts; ++part_i) {
+          float y[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            y[e] = part_i + 1 < kQParts ? three_bits(x[e]) : x[e];
+            x[e] -= y[e];
+          }
+          const int row = part_i * RB + r;
+          *reinterpret_cast<uint32_t*>(smem + L::kQOff + row * 128 + ((lane * 4) ^ ((row & 7) << 4))) =
+              to_e5m2x2(y[0], y[1]) | to_e5m2x2(y[2], y[3]) << 16;
+        }
+      }
+      fence_proxy_async();
+      mbar_arrive(&bar.q_full);
+      named_bar_sync(1, 128);  // c and limit
+      float m[RB], l[RB];
+      int least = INT32_MAX;
+#pragma unroll
+      for (int r = 0; r < RB; ++r) {
+        m[r] = -INFINITY;
+        l[r] = 0.f;
+        if (r < rows) least = min(least, bar.limit[r]);
+      }
+      VRef<10, -3> vref;  // P below 2^4 (stale maximum) * 2^10 * 2; 2^-24 * 2^10 * 2^-3 is below its smallest value
+      const uint32_t ring_base = stage_v;
+      for (int i = 0; i < s.count; ++i, ++turn) {
+        if ((i & 31) == 0) win.advance(i, lane, p.status);
+        const int id = __shfl_sync(0xffffffffu, win.id, i & 31);
+        const float ks = __shfl_sync(0xffffffffu, win.ks, i & 31);
+        const float o_ratio = vref.page(__shfl_sync(0xffffffffu, win.vs, i & 31));
+        const int key0 = (s.pg + i) * kPage;
+        const bool partial = id < 0 || key0 + kPage > least;
+        wait_warp(&bar.s_full[turn & 1], (turn >> 1) & 1);
+        tc_fence_after();
+        float t[RB];
+        if (ok) tmem_rows<RB, kQParts>(tmem + lane_off + (turn & 1) * kSBuf, t);
         bool need = o_ratio != 1.f;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          ck[i] = score_factor(c[i], ks);
-          float mx = fmaxf(max3f(sc[0][2 * i], sc[0][2 * i + 1], sc[1][2 * i]),
-                           max3f(sc[1][2 * i + 1], sc[2][2 * i], sc[2][2 * i + 1]));
-          mx = max3f(mx, sc[3][2 * i], sc[3][2 * i + 1]);
-          page_max[i] = mx;
-          // a maximum of -inf is replaced by whatever is seen first
-          need |= mx * ck[i] > m[i] + kStaleMax;
-          need |= fabsf(mx * ck[i]) > kBigScore && mx != -INFINITY;
+        for (int r = 0; r < RB; ++r) {
+          t[r] *= score_factor(bar.c[r], ks);
+          if (partial && (id < 0 || r >= rows || key0 + key >= bar.limit[r])) t[r] = -INFINITY;
+          need |= r < rows && t[r] > m[r] + kFewStale;
         }
-        float add[2] = {vref.log - (m[0] == -INFINITY ? 0.f : m[0]), vref.log - (m[1] == -INFINITY ? 0.f : m[1])};
-        if (__any_sync(0xffffffffu, need)) {
+        if (partial) {
+          // Slots that no token has reached may hold anything, and a product
+          // takes every key for every row although 0 * NaN is NaN: those
+          // slots become zero in the tile, and so does a NaN, which the rows
+          // that see it get back at the end.
+          const uint32_t at = ring_base + v_tile(i, s.count);
+          wait_warp(&bar.full[at % kFewRing], (at / kFewRing) & 1);
+          uint4* row = reinterpret_cast<uint4*>(smem + L::kRingOff + (at % kFewRing) * kPageBytes + key * 128);
+          const bool drop = id < 0 || key0 + key >= s.st.len;
+          uint32_t nan = 0;
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            float mx = page_max[i];
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-            const float now = fmaxf(m[i], mx * ck[i]);
-            const float use = now == -INFINITY ? 0.f : now;
-            const float alpha = ex2_approx(m[i] - use);
-            m[i] = now;
-            l[i] *= alpha;
-            const float by = alpha * o_ratio;
+          for (int j = 0; j < 8; ++j) {
+            if (!ok) break;
+            uint4 v = drop ? make_uint4(0, 0, 0, 0) : row[j];
+            uint32_t hit = take_nan(v.x) | take_nan(v.y);
+            hit |= take_nan(v.z) | take_nan(v.w);
+            if (drop || hit) row[j] = v;
+            nan |= hit;
+          }
+          if (nan) *const_cast<volatile int*>(&bar.nan_seen) = 1;
+        }
+        if (vote_128(need)) {
+          // new maxima over the page, the same for the four warps; O is
+          // rescaled, once its product with the page before is complete (the
+          // one before that is: S^T of this page was issued after it)
+          float top[RB];
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              acc[j][2 * i] *= by;
-              acc[j][2 * i + 1] *= by;
+          for (int r = 0; r < RB; ++r) {
+            top[r] = t[r];
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], o));
+            if (lane == 0) bar.top[warp][r] = top[r];
+          }
+          named_bar_sync(1, 128);
+          float by[RB];
+#pragma unroll
+          for (int r = 0; r < RB; ++r) {
+            const float now =
+                fmaxf(fmaxf(m[r], fmaxf(bar.top[0][r], bar.top[1][r])), fmaxf(bar.top[2][r], bar.top[3][r]));
+            const float alpha = ex2_approx(m[r] - (now == -INFINITY ? 0.f : now));
+            m[r] = now;
+            l[r] *= alpha;
+            by[r] = alpha * o_ratio;
+          }
+          if (i > 0 && wait_warp(&bar.pv_done, (turn - 1) & 1)) {
+            tc_fence_after();
+#pragma unroll
+            for (int j = 0; j < kPCols; j += 16) {
+              uint32_t o[16];
+              tmem_ld16_wait(tmem + lane_off + kOCol + j, o);
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                if (j + e < kPParts * RB) o[e] = __float_as_uint(__uint_as_float(o[e]) * by[(j + e) % RB]);
+              tmem_st16(tmem + lane_off + kOCol + j, o);
             }
-            // relative to the page's own largest score: scores of 2^24 and
-            // more would leave the rounding of mx * ck in the exponent
-            const float mx0 = mx == -INFINITY ? 0.f : mx;
-            add[i] = (mx == -INFINITY ? 0.f : mx * ck[i] - use) + vref.log;
+            tmem_wait_st();
+          }
+          named_bar_sync(1, 128);  // top has been read
+        }
+        // P^T as operand B: row part * RB + r, keys contiguous
+        uint8_t* pt = smem + L::kPOff + (turn & 1) * L::kPBytes;
 #pragma unroll
-            for (int nt = 0; nt < 4; ++nt) {
-              sc[nt][2 * i] -= mx0;
-              sc[nt][2 * i + 1] -= mx0;
-            }
+        for (int r = 0; r < RB; ++r) {
+          if (r >= rows) break;
+          const float use = m[r] == -INFINITY ? 0.f : m[r];
+          const float w = ex2_approx((t[r] - use) + vref.log);
+          l[r] = __fmaf_rn(w, vref.inv, l[r]);
+          const float a = three_bits(w), ra = w - a, b = three_bits(ra), rb = ra - b, d = three_bits(rb);
+          const uint32_t ab = to_e5m2x2(a, b), de = to_e5m2x2(d, rb - d);
+#pragma unroll
+          for (int part_i = 0; part_i < kPParts; ++part_i) {
+            const int row = part_i * RB + r;
+            pt[row * 128 + (key ^ ((row & 7) << 4))] =
+                static_cast<uint8_t>((part_i < 2 ? ab : de) >> (part_i & 1 ? 8 : 0));
           }
         }
-        uint32_t pa[2][4];
+        fence_proxy_async();
+        tc_fence_before();
+        mbar_arrive(&bar.p_full[turn & 1]);
+      }
+      stage_v += 2 * s.count;
+      // the stretch's result: every lane has its channel of all rows
+      wait_warp(&bar.o_full, seg & 1);
+      tc_fence_after();
+      float o[RB];
+      if (ok) tmem_rows<RB, kPParts>(tmem + lane_off + kOCol, o);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          float sum = 0.f;
+      for (int r = 0; r < RB; ++r) {
 #pragma unroll
-          for (int nt = 0; nt < 4; ++nt) {
-            const float e0 = ex2_approx(__fmaf_rn(sc[nt][2 * i], ck[i], add[i]));
-            const float e1 = ex2_approx(__fmaf_rn(sc[nt][2 * i + 1], ck[i], add[i]));
-            sum += e0 + e1;
-            pa[nt >> 1][(nt & 1) * 2 + i] = pack_half2(e0, e1);
+        for (int x = 16; x > 0; x >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], x);
+        if (lane == 0) bar.sum[warp][r] = l[r];
+      }
+      named_bar_sync(1, 128);
+      const bool complete = s.count == s.pages;
+      const bool patch = *const_cast<volatile int*>(&bar.nan_seen) != 0;
+      float* out = part + (2 * static_cast<int64_t>(blockIdx.x) + (seg > 0)) * kFewPartFloats;
+      if (ok && *abort_flag == 0) {
+#pragma unroll
+        for (int r = 0; r < RB; ++r) {
+          if (r >= rows) break;
+          const float sum = (bar.sum[0][r] + bar.sum[1][r]) + (bar.sum[2][r] + bar.sum[3][r]);
+          float x = o[r] * vref.unit();
+          if (patch && stretch_nan(p, s, bar.limit[r], least, key)) x = NAN;
+          if (complete) {
+            const int64_t at = static_cast<int64_t>(s.head * p.group + r % p.group) * p.n + s.st.t0 + r / p.group;
+            const bool some = sum != 0.f;
+            p.o[at * 128 + key] = __float2bfloat16_rn(some ? x / sum : 0.f);
+            if (p.lse && key == 0) p.lse[at] = some ? (m[r] + log2f(sum)) * kLn2 : -INFINITY;
+          } else {
+            out[r * 128 + key] = sum != 0.f ? x : 0.f;
+            if (key == 0) *reinterpret_cast<float2*>(out + kFewRows * 128 + 2 * r) = make_float2(m[r], sum);
           }
-          l[i] = __fmaf_rn(sum, vref.inv, l[i]);
-        }
-        // O += P V, four output tiles at a time
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          uint32_t pair[2][2][2][2];  // k16 step, operand half, pair of channels, packed fp16 of two keys
-#pragma unroll
-          for (int k = 0; k < 2; ++k)
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-              const uint32_t x = word_of(vw[k][2 * hf], w), y = word_of(vw[k][2 * hf + 1], w);
-              const uint32_t lo = __byte_perm(x, y, 0x5140), hi = __byte_perm(x, y, 0x7362);
-              pair[k][hf][0][0] = e4m3x2_to_half2(lo & 0xffffu);
-              pair[k][hf][0][1] = e4m3x2_to_half2(lo >> 16);
-              pair[k][hf][1][0] = e4m3x2_to_half2(hi & 0xffffu);
-              pair[k][hf][1][1] = e4m3x2_to_half2(hi >> 16);
-            }
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-              mma_f16(acc[w * 4 + j], pa[k], pair[k][0][j >> 1][j & 1], pair[k][1][j >> 1][j & 1]);
         }
       }
-      __syncwarp();
-      if (ok) {
-        ++used;
-        issue();
-      }
+      tc_fence_before();
+      named_bar_sync(1, 128);  // limit, sum and nan_seen have been read
+      if (key == 0) bar.nan_seen = 0;
+      ++seg;
     }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-    }
-    // join the four warps: lane t of a quad holds channels 32t .. 32t+31
-    named_bar_sync(1, 32 * kFewWarps);  // the last stretch's rows have been read
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      if (t == 0) {
-        sh.m[warp][g + 8 * i] = m[i];
-        sh.l[warp][g + 8 * i] = l[i];
-      }
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-#pragma unroll
-        for (int j = 0; j < 16; ++j) sh.o[warp][g + 8 * i][32 * t + 16 * e + j] = acc[j][2 * i + e] * vref.unit();
-    }
-    named_bar_sync(1, 32 * kFewWarps);
-    const bool complete = s.count == s.pages;
-    float* out = part + (2 * static_cast<int64_t>(blockIdx.x) + (seg > 0)) * kFewPartFloats;
-    for (int r = warp; r < rows && *abort_flag == 0; r += kFewWarps) {
-      float mx = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < kFewWarps; ++w) mx = fmaxf(mx, sh.m[w][r]);
-      const float use = mx == -INFINITY ? 0.f : mx;
-      float sum = 0.f;
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < kFewWarps; ++w) {
-        const float f = ex2_approx(sh.m[w][r] - use);
-        const float4 x = *reinterpret_cast<const float4*>(&sh.o[w][r][lane * 4]);
-        sum += sh.l[w][r] * f;
-        o.x += x.x * f;
-        o.y += x.y * f;
-        o.z += x.z * f;
-        o.w += x.w * f;
-      }
-      if (complete) {
-        const int64_t at =
-            static_cast<int64_t>(s.head * p.group + r % p.group) * p.n + s.st.t0 + r / p.group;
-        store_row(p, at, lane, mx, sum, o);
-      } else {
-        *reinterpret_cast<float4*>(out + r * 128 + lane * 4) = o;
-        if (lane == 0) *reinterpret_cast<float2*>(out + kFewRows * 128 + 2 * r) = make_float2(mx, sum);
-      }
-    }
-    ++seg;
   }
-  // no copy may still be landing when the CTA leaves
-  for (; used < issued; ++used) {
-    volatile int never = 0;
-    mbar_wait(full + used % kFewStages, (used / kFewStages) & 1, &never, p.status);
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 5) {
+    __syncwarp();
+    tmem_dealloc(tmem, kFewCols);
   }
 }
 
@@ -622,13 +692,13 @@ __global__ void __launch_bounds__(128)
   }
 }
 
-// 128-byte rows of the cache's pages, boxes of a warp's share of a page with the 128-byte swizzle.
+// 128-byte rows of the cache's pages, boxes of one page with the 128-byte swizzle.
 int make_page_map(CUtensorMap* map, const void* base, int64_t rows) {
   EncodeTiledFn enc = get_encode();
   if (!enc) return CALIBATT_ERR_CUDA;
   cuuint64_t dims[2] = {128, static_cast<cuuint64_t>(rows)};
   cuuint64_t strides[1] = {128};
-  cuuint32_t box[2] = {128, kSliceKeys};
+  cuuint32_t box[2] = {128, kPage};
   cuuint32_t estr[2] = {1, 1};
   const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -636,23 +706,33 @@ int make_page_map(CUtensorMap* map, const void* base, int64_t rows) {
   return r == CUDA_SUCCESS ? CALIBATT_OK : CALIBATT_ERR_CUDA;
 }
 
-template <bool SW>
+template <bool SW, int RB>
 int launch_few(const CUtensorMap& mk, const CUtensorMap& mv, const CacheAttnParams& p, const FewPlan& plan, float* ws,
                cudaStream_t stream) {
   static PerDeviceOnce once;
   const int rc =
-      set_max_smem_once(reinterpret_cast<const void*>(cache_few_kernel<SW>), kFewDynSmem, once);
+      set_max_smem_once(reinterpret_cast<const void*>(cache_few_kernel<SW, RB>), FewLayout::kDynSmem, once);
   if (rc != CALIBATT_OK) return rc;
-  cache_few_kernel<SW><<<plan.ctas, kFewThreads, kFewDynSmem, stream>>>(mk, mv, p, plan.whole, ws);
+  cache_few_kernel<SW, RB><<<plan.ctas, kFewThreads, FewLayout::kDynSmem, stream>>>(mk, mv, p, plan.whole, ws);
   return cudaGetLastError() == cudaSuccess ? CALIBATT_OK : CALIBATT_ERR_CUDA;
+}
+
+template <bool SW>
+int launch_few_rows(const CUtensorMap& mk, const CUtensorMap& mv, const CacheAttnParams& p, const FewPlan& plan,
+                    float* ws, cudaStream_t stream) {
+  if (plan.rows <= 1) return launch_few<SW, 1>(mk, mv, p, plan, ws, stream);
+  if (plan.rows <= 4) return launch_few<SW, 4>(mk, mv, p, plan, ws, stream);
+  if (plan.rows <= 8) return launch_few<SW, 8>(mk, mv, p, plan, ws, stream);
+  return launch_few<SW, 16>(mk, mv, p, plan, ws, stream);
 }
 
 }  // namespace
 
-FewPlan few_plan(int batch, int heads_kv, int64_t pages, int sms) {
+FewPlan few_plan(int batch, int heads_kv, int rows, int64_t pages, int sms) {
   const int64_t units = static_cast<int64_t>(batch) * heads_kv;
   FewPlan f;
   // up to 4 pages the join costs more than the split saves
+  f.rows = rows;
   f.whole = pages <= 4;
   f.ctas = static_cast<int>(f.whole ? units : std::min<int64_t>(2ll * sms, units * ((pages + 1) / 2)));
   return f;
@@ -671,8 +751,8 @@ int launch_cache_attn_few(const CacheAttnParams& p, const FewPlan& plan, void* w
   if (rc == CALIBATT_OK) rc = make_page_map(&mv, rows ? static_cast<const void*>(p.v8) : p.q, rows ? rows : kPage);
   if (rc != CALIBATT_OK) return rc;
   float* part = static_cast<float*>(ws);
-  rc = p.wait_limit_ns < kShortWaitNs ? launch_few<true>(mk, mv, p, plan, part, stream)
-                                      : launch_few<false>(mk, mv, p, plan, part, stream);
+  rc = p.wait_limit_ns < kShortWaitNs ? launch_few_rows<true>(mk, mv, p, plan, part, stream)
+                                      : launch_few_rows<false>(mk, mv, p, plan, part, stream);
   if (rc != CALIBATT_OK || plan.whole) return rc;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(p.heads_kv, p.batch);

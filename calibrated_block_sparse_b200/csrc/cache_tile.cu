@@ -49,6 +49,9 @@ constexpr int kTileControlRegs = 40;
 constexpr int kTileRegs = 256 * kTileSoftmaxRegs + 128 * kTileConvertRegs + 128 * kTileControlRegs;
 static_assert(kTileRegs <= 128 * kTileThreads, "register split");
 constexpr int kTileRing = 5;
+constexpr float kStaleMax = 8.0f;      // log2 units: move the running max only if it grows by more
+constexpr float kBigScore = 65536.0f;  // log2 units: beyond it the rounding of the row max counts
+
 struct TileBarriers {
   uint64_t ring_full[kTileRing];
   uint64_t ring_empty[kTileRing];
@@ -76,47 +79,9 @@ static_assert(TileLayout::kDynSmem <= 232448, "shared memory budget");
 constexpr uint32_t kIdescQK = (1u << 4) | (16u << 17) | (8u << 24);
 constexpr uint32_t kIdescPVh = kIdescQK | (1u << 16);
 
-__device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-
 __device__ __forceinline__ void st_shared16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
-
-// Page numbers of 32 consecutive pages of a stream, one per lane, fetched a
-// chunk of 32 ahead; kScales: with their key and value scales. A page outside
-// the pool gets id -1.
-template <bool kScales>
-struct PageWindow {
-  const int32_t* table;
-  const float* k_scale;
-  const float* v_scale;
-  int n_pages, heads, head, count;  // pages of the range
-  int id, id_next;
-  float ks, vs, ks_next, vs_next;
-
-  __device__ __forceinline__ void fetch(int at, int* status) {
-    id_next = -1;
-    ks_next = vs_next = 1.f;
-    if (at < count) {
-      id_next = __ldg(table + at);
-      if (id_next < 0 || id_next >= n_pages) {
-        record_error(status, CALIBATT_ERR_CSR);
-        id_next = -1;
-      } else if (kScales) {
-        const int64_t i = static_cast<int64_t>(id_next) * heads + head;
-        ks_next = __ldg(k_scale + i);
-        vs_next = __ldg(v_scale + i);
-      }
-    }
-  }
-  // call before using page i = 0, 32, 64, ...
-  __device__ __forceinline__ void advance(int i, int lane, int* status) {
-    id = id_next;
-    ks = ks_next;
-    vs = vs_next;
-    fetch(i + 32 + lane, status);
-  }
-};
 
 // 16 e4m3 values as two 16-byte chunks j, j + 1 of fp16 of row r, with the
 // 128-byte swizzle (chunk j is at j ^ (r & 7)).
@@ -130,23 +95,6 @@ __device__ __forceinline__ void store_half(uint32_t row_addr, int r, int j, cons
   }
   st_shared16(row_addr + ((j ^ (r & 7)) << 4), h[0], h[1], h[2], h[3]);
   st_shared16(row_addr + (((j + 1) ^ (r & 7)) << 4), h[4], h[5], h[6], h[7]);
-}
-
-// Tile t of the ring's order -> (V?, page of the range). Both slots on one
-// page: K0 V0 K1 V1 ...; alternate: K0 K1 V0 K2 V1 ... (the issuer's order).
-template <bool kAlt>
-__device__ __forceinline__ void ring_tile(int t, int np, bool& is_v, int& page) {
-  if (!kAlt) {
-    is_v = t & 1;
-    page = t >> 1;
-  } else if (t & 1) {
-    page = (t + 1) >> 1;
-    is_v = page >= np;
-    if (is_v) page = (t - 1) >> 1;
-  } else {
-    is_v = t > 0;
-    page = t > 0 ? (t >> 1) - 1 : 0;
-  }
 }
 
 template <bool SW, bool kAlt>
@@ -216,7 +164,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     // lanes of a store phase: two rows (one even, one odd) of four quarters
     // of a 64-channel half, so their 16-byte chunks fall into eight banks groups
     const int row = (warp - 8) * 8 + (lane >> 2), quarter = lane & 3;
-    PageWindow<false> win{table, nullptr, nullptr, p.n_pages, p.heads_kv, head, np, -1, -1, 1.f, 1.f, 1.f, 1.f};
+    PageWindow<false> win(p, b, head, pg0, np, st.len);
     win.fetch(lane, p.status);
     // pages are met in order by K; V follows at most one page behind
     int id_now = -1, id_before = -1, k_at = 0;
@@ -264,9 +212,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             if (key >= st.len) x[k] = 0;
-            const uint32_t hit = e4m3_nan_bytes(x[k]);
-            x[k] &= ~((hit >> 7) * 0xffu);
-            nan |= hit;
+            nan |= take_nan(x[k]);
           }
         }
         if (nan) *const_cast<volatile int*>(&bar.nan_seen) = 1;
@@ -398,7 +344,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     // ---------------------------------------------------------- softmax
     warpgroup_regs_inc<kTileSoftmaxRegs>();
     float m_run = -INFINITY, l_run = 0.f;
-    VRef vref;
+    VRef<6, -6> vref;  // P below 2^8 (stale maximum) * 2^6 * 2, fp16; 2^-24 * 2^6 * 2^-6 is its smallest value
+
     bool ok = true;  // warp-uniform
     const int s = warp >> 2;
     const int row = (warp & 3) * 32 + lane;
@@ -423,7 +370,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         for (int e = 0; e < 4; ++e)
           amax = max3f(amax, fabsf(__uint_as_float(x[e] << 16)), fabsf(__uint_as_float(x[e] & 0xffff0000u)));
       }
-      const float shrink = row_shrink(amax);
+      const float shrink = row_shrink(amax, 0);
       c_row = p.scale_log2 / shrink;
       const uint32_t dst = sbase + L::kQOff + s * kTile + row * 128;
 #pragma unroll
@@ -451,7 +398,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           for (int e = 0; e < 4; ++e)
             amax = max3f(amax, fabsf(__uint_as_float(x[e] << 16)), fabsf(__uint_as_float(x[e] & 0xffff0000u)));
         }
-        c_row = p.scale_log2 / row_shrink(amax);
+        c_row = p.scale_log2 / row_shrink(amax, 0);
       }
     }
     auto wait_warp = [&](uint64_t* bb, uint32_t parity) -> bool {
@@ -460,7 +407,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     };
     const bool active = s == 0 || second;
     if (active && np > 0) {
-      PageWindow<true> win{table, p.k_scale, p.v_scale, p.n_pages, p.heads_kv, head, np, -1, -1, 1.f, 1.f, 1.f, 1.f};
+      PageWindow<true> win(p, b, head, pg0, np, st.len);
       win.fetch(lane, p.status);
       int turn = 0;  // pages this slot has taken
       for (int i = kAlt ? s : 0; i < np; i += kAlt ? 2 : 1, ++turn) {
