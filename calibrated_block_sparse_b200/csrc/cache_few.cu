@@ -30,6 +30,7 @@
 // page finds out with one vote of the four warps.
 #include <cuda.h>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
@@ -51,6 +52,7 @@ constexpr int kFewRing = 5;
 constexpr int kPageBytes = kPage * 128;
 constexpr int kFewPartFloats = kFewRows * 128 + 2 * kFewRows;  // a partial result: O, then maximum and sum per row
 constexpr float kFewStale = 4.0f;                              // log2 units
+constexpr float kNoMax = -3e38f;                               // of a row that has seen no key
 constexpr int kQParts = 3, kPParts = 4;
 
 // Columns (N) of a product with `parts` columns per row: a multiple of 16.
@@ -126,15 +128,14 @@ __device__ __forceinline__ bool vote_128(bool x) {
 // The kParts columns of every row, added up: column part * RB + r, of one lane.
 template <int RB, int kParts>
 __device__ __forceinline__ void tmem_rows(uint32_t taddr, float (&x)[RB]) {
+  uint32_t c[few_cols(RB, kParts)];
+  tmem_ld16s_wait(taddr, c);
 #pragma unroll
-  for (int r = 0; r < RB; ++r) x[r] = 0.f;
+  for (int r = 0; r < RB; ++r) {
+    float sum = __uint_as_float(c[(kParts - 1) * RB + r]);  // the small parts first
 #pragma unroll
-  for (int i = 0; i < kParts * RB; i += 16) {
-    uint32_t c[16];
-    tmem_ld16_wait(taddr + i, c);
-#pragma unroll
-    for (int e = 0; e < 16; ++e)
-      if (i + e < kParts * RB) x[(i + e) % RB] += __uint_as_float(c[e]);
+    for (int i = kParts - 2; i >= 0; --i) sum += __uint_as_float(c[i * RB + r]);
+    x[r] = sum;
   }
 }
 
@@ -446,6 +447,11 @@ __global__ void __launch_bounds__(kFewThreads, 2)
       const int rows = s.st.n_new * p.group;
       PageWindow<true> win(p, s.b, s.head, s.pg, s.count, s.st.len);
       win.fetch(lane, p.status);
+      // rows that the stretch does not have see no key
+      if (key >= rows && key < RB) {
+        bar.c[key] = 0.f;
+        bar.limit[key] = 0;
+      }
       // the rows of Q as operand B: row part * RB + r, channels contiguous
       for (int r = warp; r < rows; r += 4) {
         const int tok = r / p.group, h = s.head * p.group + r % p.group;
@@ -483,7 +489,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
       int least = INT32_MAX;
 #pragma unroll
       for (int r = 0; r < RB; ++r) {
-        m[r] = -INFINITY;
+        m[r] = kNoMax;
         l[r] = 0.f;
         if (r < rows) least = min(least, bar.limit[r]);
       }
@@ -502,16 +508,15 @@ __global__ void __launch_bounds__(kFewThreads, 2)
         if (ok) tmem_rows<RB, kQParts>(tmem + lane_off + (turn & 1) * kSBuf, t);
         bool need = o_ratio != 1.f;
 #pragma unroll
-        for (int r = 0; r < RB; ++r) {
-          t[r] *= score_factor(bar.c[r], ks);
-          if (partial && (id < 0 || r >= rows || key0 + key >= bar.limit[r])) t[r] = -INFINITY;
-          need |= r < rows && t[r] > m[r] + kFewStale;
-        }
+        for (int r = 0; r < RB; ++r) t[r] *= bar.c[r] * ks;
         if (partial) {
           // Slots that no token has reached may hold anything, and a product
           // takes every key for every row although 0 * NaN is NaN: those
           // slots become zero in the tile, and so does a NaN, which the rows
           // that see it get back at the end.
+#pragma unroll
+          for (int r = 0; r < RB; ++r)
+            if (id < 0 || key0 + key >= bar.limit[r]) t[r] = -INFINITY;
           const uint32_t at = ring_base + v_tile(i, s.count);
           wait_warp(&bar.full[at % kFewRing], (at / kFewRing) & 1);
           uint4* row = reinterpret_cast<uint4*>(smem + L::kRingOff + (at % kFewRing) * kPageBytes + key * 128);
@@ -527,6 +532,12 @@ __global__ void __launch_bounds__(kFewThreads, 2)
             nan |= hit;
           }
           if (nan) *const_cast<volatile int*>(&bar.nan_seen) = 1;
+        }
+        float d[RB];
+#pragma unroll
+        for (int r = 0; r < RB; ++r) {
+          d[r] = t[r] - m[r];
+          need |= d[r] > kFewStale;
         }
         if (vote_128(need)) {
           // new maxima over the page, the same for the four warps; O is
@@ -546,8 +557,9 @@ __global__ void __launch_bounds__(kFewThreads, 2)
           for (int r = 0; r < RB; ++r) {
             const float now =
                 fmaxf(fmaxf(m[r], fmaxf(bar.top[0][r], bar.top[1][r])), fmaxf(bar.top[2][r], bar.top[3][r]));
-            const float alpha = ex2_approx(m[r] - (now == -INFINITY ? 0.f : now));
+            const float alpha = ex2_approx(m[r] - now);
             m[r] = now;
+            d[r] = t[r] - now;
             l[r] *= alpha;
             by[r] = alpha * o_ratio;
           }
@@ -566,21 +578,27 @@ __global__ void __launch_bounds__(kFewThreads, 2)
           }
           named_bar_sync(1, 128);  // top has been read
         }
-        // P^T as operand B: row part * RB + r, keys contiguous
+        // P^T as operand B: row part * RB + r, keys contiguous. An e5m2 value is
+        // the upper byte of an fp16 value, so the parts are that byte of the
+        // fp16 weight, of what remains, and so on, the last one rounded; two
+        // rows at a time.
         uint8_t* pt = smem + L::kPOff + (turn & 1) * L::kPBytes;
 #pragma unroll
-        for (int r = 0; r < RB; ++r) {
-          if (r >= rows) break;
-          const float use = m[r] == -INFINITY ? 0.f : m[r];
-          const float w = ex2_approx((t[r] - use) + vref.log);
-          l[r] = __fmaf_rn(w, vref.inv, l[r]);
-          const float a = three_bits(w), ra = w - a, b = three_bits(ra), rb = ra - b, d = three_bits(rb);
-          const uint32_t ab = to_e5m2x2(a, b), de = to_e5m2x2(d, rb - d);
+        for (int r = 0; r < RB; r += 2) {
+          constexpr int kOne = RB == 1;
+          const float w0 = ex2_approx(d[r] + vref.log), w1 = kOne ? 0.f : ex2_approx(d[r + 1 - kOne] + vref.log);
+          l[r] = __fmaf_rn(w0, vref.inv, l[r]);
+          if (!kOne) l[r + 1 - kOne] = __fmaf_rn(w1, vref.inv, l[r + 1 - kOne]);
+          __half2 rest = __floats2half2_rn(w0, w1);
 #pragma unroll
           for (int part_i = 0; part_i < kPParts; ++part_i) {
+            uint32_t x = *reinterpret_cast<const uint32_t*>(&rest);
+            if (part_i + 1 == kPParts) x += 0x00800080u;
+            x &= 0xff00ff00u;
+            if (part_i + 1 < kPParts) rest = __hsub2(rest, *reinterpret_cast<const __half2*>(&x));
             const int row = part_i * RB + r;
-            pt[row * 128 + (key ^ ((row & 7) << 4))] =
-                static_cast<uint8_t>((part_i < 2 ? ab : de) >> (part_i & 1 ? 8 : 0));
+            pt[row * 128 + (key ^ ((row & 7) << 4))] = static_cast<uint8_t>(x >> 8);
+            if (!kOne) pt[(row + 1) * 128 + (key ^ (((row + 1) & 7) << 4))] = static_cast<uint8_t>(x >> 24);
           }
         }
         fence_proxy_async();
@@ -617,7 +635,8 @@ __global__ void __launch_bounds__(kFewThreads, 2)
             if (p.lse && key == 0) p.lse[at] = some ? (m[r] + log2f(sum)) * kLn2 : -INFINITY;
           } else {
             out[r * 128 + key] = sum != 0.f ? x : 0.f;
-            if (key == 0) *reinterpret_cast<float2*>(out + kFewRows * 128 + 2 * r) = make_float2(m[r], sum);
+            if (key == 0) *reinterpret_cast<float2*>(out + kFewRows * 128 + 2 * r) =
+                  make_float2(sum != 0.f ? m[r] : -INFINITY, sum);
           }
         }
       }
