@@ -21,13 +21,15 @@
 // largest value in [2^13, 2^14), is exact down to 2^-22 of it and within 2^-31
 // of it below, and weights keep a bit down to 2^-24 of the largest.
 //
-// CTA (192 threads):
-//   warps 0-3  softmax; thread = key of the page = TMEM lane of S^T, and
+// CTA:
+//   warp  0    TMA producer: K and V tiles (16 KB) into a 5-stage ring
+//   warp  1    MMA issuer: S^T of the next page before O^T of this one
+//   4 warps    softmax; thread = key of the page = TMEM lane of S^T, and
 //              channel = TMEM lane of O^T at the end
-//   warp  4    TMA producer: K and V tiles (16 KB) into a 5-stage ring
-//   warp  5    MMA issuer: S^T of the next page before O^T of this one
+// More than 8 rows are shared out to two such groups of 4 warps, 8 rows each:
+// the softmax of 16 rows in one thread is a chain of ~4000 cycles a page.
 // The running maximum of a row moves only if it grew by more than 2^4, which a
-// page finds out with one vote of the four warps.
+// page finds out with one vote of a group's warps.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -47,7 +49,7 @@
 namespace calibatt {
 namespace {
 
-constexpr int kFewThreads = 192;
+constexpr int few_threads(int groups) { return 64 + 128 * groups; }
 constexpr int kFewRing = 5;
 constexpr int kPageBytes = kPage * 128;
 constexpr int kFewPartFloats = kFewRows * 128 + 2 * kFewRows;  // a partial result: O, then maximum and sum per row
@@ -70,8 +72,8 @@ struct FewBarriers {
   int nan_seen;
   int limit[kFewRows];            // keys that a row sees
   float c[kFewRows];              // a raw score's factor, without the key scale
-  float top[4][kFewRows];         // per warp, of a page
-  float sum[4][kFewRows];         // per warp, at a stretch's end
+  float top[4][kFewRows];         // per warp of a group, of a page
+  float sum[4][kFewRows];         // per warp of a group, at a stretch's end
 };
 
 struct FewLayout {
@@ -113,28 +115,28 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, u
       : "memory");
 }
 
-// Vote of the four softmax warps.
-__device__ __forceinline__ bool vote_128(bool x) {
+// Vote of a group's four warps.
+__device__ __forceinline__ bool vote_128(int id, bool x) {
   uint32_t r;
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, 2, 128, p;\n\t"
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, %2, 128, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"(static_cast<uint32_t>(x))
+      : "r"(static_cast<uint32_t>(x)), "r"(id)
       : "memory");
   return r != 0;
 }
 
-// The kParts columns of every row, added up: column part * RB + r, of one lane.
-template <int RB, int kParts>
-__device__ __forceinline__ void tmem_rows(uint32_t taddr, float (&x)[RB]) {
-  uint32_t c[few_cols(RB, kParts)];
+// The kParts columns of RG rows, added up: column part * RG + r, of one lane.
+template <int RG, int kParts>
+__device__ __forceinline__ void tmem_rows(uint32_t taddr, float (&x)[RG]) {
+  uint32_t c[few_cols(RG, kParts)];
   tmem_ld16s_wait(taddr, c);
 #pragma unroll
-  for (int r = 0; r < RB; ++r) {
-    float sum = __uint_as_float(c[(kParts - 1) * RB + r]);  // the small parts first
+  for (int r = 0; r < RG; ++r) {
+    float sum = __uint_as_float(c[(kParts - 1) * RG + r]);  // the small parts first
 #pragma unroll
-    for (int i = kParts - 2; i >= 0; --i) sum += __uint_as_float(c[i * RB + r]);
+    for (int i = kParts - 2; i >= 0; --i) sum += __uint_as_float(c[i * RG + r]);
     x[r] = sum;
   }
 }
@@ -279,12 +281,13 @@ __device__ __forceinline__ bool stretch_nan(const CacheAttnParams& p, const Stre
   return false;
 }
 
-template <bool SW, int RB>  // RB: rows that registers and columns are laid out for
-__global__ void __launch_bounds__(kFewThreads, 2)
+template <bool SW, int RG, int G>  // G groups of softmax warps, each laid out for RG rows
+__global__ void __launch_bounds__(few_threads(G), 2)
     cache_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                      const __grid_constant__ CacheAttnParams p, bool whole, float* part) {
   using L = FewLayout;
-  constexpr int kQCols = few_cols(RB, kQParts), kPCols = few_cols(RB, kPParts);
+  constexpr int RB = RG * G, kAll = 128 * G;
+  constexpr int kQCols = few_cols(RG * G, kQParts), kPCols = few_cols(RG * G, kPParts);
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
@@ -298,10 +301,10 @@ __global__ void __launch_bounds__(kFewThreads, 2)
       mbar_init(&bar.full[i], 1);
       mbar_init(&bar.empty[i], 1);
     }
-    mbar_init(&bar.q_full, 128);
+    mbar_init(&bar.q_full, kAll);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar.s_full[i], 1);
-      mbar_init(&bar.p_full[i], 128);
+      mbar_init(&bar.p_full[i], kAll);
     }
     mbar_init(&bar.pv_done, 1);
     mbar_init(&bar.o_full, 1);
@@ -310,7 +313,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     bar.nan_seen = 0;
     fence_barrier_init();
   }
-  if (warp == 5) tmem_alloc(&bar.tmem_base, kFewCols);
+  if (warp == 1) tmem_alloc(&bar.tmem_base, kFewCols);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -318,7 +321,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // streams that do not fit are reported once
-  if (blockIdx.x == 0 && warp == 4)
+  if (blockIdx.x == 0 && warp == 0)
     for (int b = lane; b < p.batch; b += 32) {
       const Stream st = stream_of(p.tok_start, p.kv_len, b, p.n, p.table_stride);
       if (st.bad || st.n_new > p.max_new || st.n_new * static_cast<int64_t>(p.group) > kFewRows)
@@ -328,7 +331,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
   Walk walk;
   walk.start(p, whole, lane);
   Stretch s;
-  if (warp == 4) {
+  if (warp == 0) {
     // ---------------------------------------------------------- TMA producer
     uint32_t stage = 0, phase = 0;
     int used = 0;
@@ -375,7 +378,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
         volatile int never = 0;
         mbar_wait(&bar.full[i % kFewRing], (i / kFewRing) & 1, &never, p.status);
       }
-  } else if (warp == 5) {
+  } else if (warp == 1) {
     // ---------------------------------------------------------- MMA issuer
     if (lane == 0) {
       uint32_t stage = 0, phase = 0, turn = 0, stretch = 0;
@@ -431,8 +434,12 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     }
   } else {
     // ---------------------------------------------------------- softmax
-    const int key = threadIdx.x;  // of a page; channel of the output
-    const uint32_t lane_off = static_cast<uint32_t>(warp * 32) << 16;
+    // a warp reaches the 32 lanes of tensor memory that its number modulo 4 names
+    const int quarter = warp & 3, g = G == 1 ? 0 : (warp - 2) >> 2;
+    const int key = quarter * 32 + lane;  // of a page; channel of the output
+    const int r0 = g * RG;                // the group's first row
+    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+    const int all = threadIdx.x - 64;
     uint32_t turn = 0;
     int seg = 0;
     // after a failed wait the warps go on without waiting or touching tensor
@@ -448,12 +455,12 @@ __global__ void __launch_bounds__(kFewThreads, 2)
       PageWindow<true> win(p, s.b, s.head, s.pg, s.count, s.st.len);
       win.fetch(lane, p.status);
       // rows that the stretch does not have see no key
-      if (key >= rows && key < RB) {
-        bar.c[key] = 0.f;
-        bar.limit[key] = 0;
+      if (all >= rows && all < RB) {
+        bar.c[all] = 0.f;
+        bar.limit[all] = 0;
       }
-      // the rows of Q as operand B: row part * RB + r, channels contiguous
-      for (int r = warp; r < rows; r += 4) {
+      // the rows of Q as operand B: row part * RG + r of a group, channels contiguous
+      for (int r = warp - 2; r < rows; r += 4 * G) {
         const int tok = r / p.group, h = s.head * p.group + r % p.group;
         const uint2 w = *reinterpret_cast<const uint2*>(
             p.q + (static_cast<int64_t>(h) * p.n + s.st.t0 + tok) * 128 + lane * 4);
@@ -477,22 +484,21 @@ __global__ void __launch_bounds__(kFewThreads, 2)
             y[e] = part_i + 1 < kQParts ? three_bits(x[e]) : x[e];
             x[e] -= y[e];
           }
-          const int row = part_i * RB + r;
+          const int row = (r / RG * kQParts + part_i) * RG + r % RG;
           *reinterpret_cast<uint32_t*>(smem + L::kQOff + row * 128 + ((lane * 4) ^ ((row & 7) << 4))) =
               to_e5m2x2(y[0], y[1]) | to_e5m2x2(y[2], y[3]) << 16;
         }
       }
       fence_proxy_async();
       mbar_arrive(&bar.q_full);
-      named_bar_sync(1, 128);  // c and limit
-      float m[RB], l[RB];
-      int least = INT32_MAX;
+      named_bar_sync(1, kAll);  // c and limit
+      float m[RG], l[RG];
 #pragma unroll
-      for (int r = 0; r < RB; ++r) {
+      for (int r = 0; r < RG; ++r) {
         m[r] = kNoMax;
         l[r] = 0.f;
-        if (r < rows) least = min(least, bar.limit[r]);
       }
+      const int least = bar.limit[0];  // the first token's rows come first
       VRef<10, -3> vref;  // P below 2^4 (stale maximum) * 2^10 * 2; 2^-24 * 2^10 * 2^-3 is below its smallest value
       const uint32_t ring_base = stage_v;
       for (int i = 0; i < s.count; ++i, ++turn) {
@@ -504,19 +510,21 @@ __global__ void __launch_bounds__(kFewThreads, 2)
         const bool partial = id < 0 || key0 + kPage > least;
         wait_warp(&bar.s_full[turn & 1], (turn >> 1) & 1);
         tc_fence_after();
-        float t[RB];
-        if (ok) tmem_rows<RB, kQParts>(tmem + lane_off + (turn & 1) * kSBuf, t);
+        float t[RG];
+        if (ok) tmem_rows<RG, kQParts>(tmem + lane_off + (turn & 1) * kSBuf + g * kQParts * RG, t);
         bool need = o_ratio != 1.f;
 #pragma unroll
-        for (int r = 0; r < RB; ++r) t[r] *= bar.c[r] * ks;
+        for (int r = 0; r < RG; ++r) t[r] *= bar.c[r0 + r] * ks;
         if (partial) {
           // Slots that no token has reached may hold anything, and a product
           // takes every key for every row although 0 * NaN is NaN: those
           // slots become zero in the tile, and so does a NaN, which the rows
           // that see it get back at the end.
 #pragma unroll
-          for (int r = 0; r < RB; ++r)
-            if (id < 0 || key0 + key >= bar.limit[r]) t[r] = -INFINITY;
+          for (int r = 0; r < RG; ++r)
+            if (id < 0 || key0 + key >= bar.limit[r0 + r]) t[r] = -INFINITY;
+        }
+        if (partial && g == 0) {
           const uint32_t at = ring_base + v_tile(i, s.count);
           wait_warp(&bar.full[at % kFewRing], (at / kFewRing) & 1);
           uint4* row = reinterpret_cast<uint4*>(smem + L::kRingOff + (at % kFewRing) * kPageBytes + key * 128);
@@ -533,30 +541,29 @@ __global__ void __launch_bounds__(kFewThreads, 2)
           }
           if (nan) *const_cast<volatile int*>(&bar.nan_seen) = 1;
         }
-        float d[RB];
+        float d[RG];
 #pragma unroll
-        for (int r = 0; r < RB; ++r) {
+        for (int r = 0; r < RG; ++r) {
           d[r] = t[r] - m[r];
           need |= d[r] > kFewStale;
         }
-        if (vote_128(need)) {
+        if (vote_128(2 + g, need)) {
           // new maxima over the page, the same for the four warps; O is
           // rescaled, once its product with the page before is complete (the
           // one before that is: S^T of this page was issued after it)
-          float top[RB];
 #pragma unroll
-          for (int r = 0; r < RB; ++r) {
-            top[r] = t[r];
+          for (int r = 0; r < RG; ++r) {
+            float top = t[r];
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], o));
-            if (lane == 0) bar.top[warp][r] = top[r];
+            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            if (lane == 0) bar.top[quarter][r0 + r] = top;
           }
-          named_bar_sync(1, 128);
-          float by[RB];
+          named_bar_sync(4 + g, 128);
+          float by[RG];
 #pragma unroll
-          for (int r = 0; r < RB; ++r) {
-            const float now =
-                fmaxf(fmaxf(m[r], fmaxf(bar.top[0][r], bar.top[1][r])), fmaxf(bar.top[2][r], bar.top[3][r]));
+          for (int r = 0; r < RG; ++r) {
+            const float now = fmaxf(fmaxf(m[r], fmaxf(bar.top[0][r0 + r], bar.top[1][r0 + r])),
+                                    fmaxf(bar.top[2][r0 + r], bar.top[3][r0 + r]));
             const float alpha = ex2_approx(m[r] - now);
             m[r] = now;
             d[r] = t[r] - now;
@@ -566,26 +573,28 @@ __global__ void __launch_bounds__(kFewThreads, 2)
           if (i > 0 && wait_warp(&bar.pv_done, (turn - 1) & 1)) {
             tc_fence_after();
 #pragma unroll
-            for (int j = 0; j < kPCols; j += 16) {
+            for (int j = 0; j < kPParts * RG; j += 16) {
+              const uint32_t col = tmem + lane_off + kOCol + g * kPParts * RG + j;
               uint32_t o[16];
-              tmem_ld16_wait(tmem + lane_off + kOCol + j, o);
+              tmem_ld16_wait(col, o);
 #pragma unroll
               for (int e = 0; e < 16; ++e)
-                if (j + e < kPParts * RB) o[e] = __float_as_uint(__uint_as_float(o[e]) * by[(j + e) % RB]);
-              tmem_st16(tmem + lane_off + kOCol + j, o);
+                if (j + e < kPParts * RG) o[e] = __float_as_uint(__uint_as_float(o[e]) * by[(j + e) % RG]);
+              tmem_st16(col, o);
             }
             tmem_wait_st();
           }
-          named_bar_sync(1, 128);  // top has been read
+          named_bar_sync(4 + g, 128);  // top has been read
         }
-        // P^T as operand B: row part * RB + r, keys contiguous. An e5m2 value is
+        // P^T as operand B: row part * RG + r of a group, keys contiguous. An e5m2 value is
         // the upper byte of an fp16 value, so the parts are that byte of the
         // fp16 weight, of what remains, and so on, the last one rounded; two
         // rows at a time.
-        uint8_t* pt = smem + L::kPOff + (turn & 1) * L::kPBytes;
+        uint8_t* pt = smem + L::kPOff + (turn & 1) * L::kPBytes + g * kPParts * RG * 128;
+        static_assert(G == 1 || kPParts * RG % 8 == 0, "a group's rows start a swizzle period");
 #pragma unroll
-        for (int r = 0; r < RB; r += 2) {
-          constexpr int kOne = RB == 1;
+        for (int r = 0; r < RG; r += 2) {
+          constexpr int kOne = RG == 1;
           const float w0 = ex2_approx(d[r] + vref.log), w1 = kOne ? 0.f : ex2_approx(d[r + 1 - kOne] + vref.log);
           l[r] = __fmaf_rn(w0, vref.inv, l[r]);
           if (!kOne) l[r + 1 - kOne] = __fmaf_rn(w1, vref.inv, l[r + 1 - kOne]);
@@ -596,7 +605,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
             if (part_i + 1 == kPParts) x += 0x00800080u;
             x &= 0xff00ff00u;
             if (part_i + 1 < kPParts) rest = __hsub2(rest, *reinterpret_cast<const __half2*>(&x));
-            const int row = part_i * RB + r;
+            const int row = part_i * RG + r;
             pt[row * 128 + (key ^ ((row & 7) << 4))] = static_cast<uint8_t>(x >> 8);
             if (!kOne) pt[(row + 1) * 128 + (key ^ (((row + 1) & 7) << 4))] = static_cast<uint8_t>(x >> 24);
           }
@@ -609,40 +618,42 @@ __global__ void __launch_bounds__(kFewThreads, 2)
       // the stretch's result: every lane has its channel of all rows
       wait_warp(&bar.o_full, seg & 1);
       tc_fence_after();
-      float o[RB];
-      if (ok) tmem_rows<RB, kPParts>(tmem + lane_off + kOCol, o);
+      float o[RG];
+      if (ok) tmem_rows<RG, kPParts>(tmem + lane_off + kOCol + g * kPParts * RG, o);
 #pragma unroll
-      for (int r = 0; r < RB; ++r) {
+      for (int r = 0; r < RG; ++r) {
 #pragma unroll
         for (int x = 16; x > 0; x >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], x);
-        if (lane == 0) bar.sum[warp][r] = l[r];
+        if (lane == 0) bar.sum[quarter][r0 + r] = l[r];
       }
-      named_bar_sync(1, 128);
+      named_bar_sync(1, kAll);
       const bool complete = s.count == s.pages;
       const bool patch = *const_cast<volatile int*>(&bar.nan_seen) != 0;
       float* out = part + (2 * static_cast<int64_t>(blockIdx.x) + (seg > 0)) * kFewPartFloats;
       if (ok && *abort_flag == 0) {
 #pragma unroll
-        for (int r = 0; r < RB; ++r) {
+        for (int rr = 0; rr < RG; ++rr) {
+          const int r = r0 + rr;
           if (r >= rows) break;
           const float sum = (bar.sum[0][r] + bar.sum[1][r]) + (bar.sum[2][r] + bar.sum[3][r]);
-          float x = o[r] * vref.unit();
+          float x = o[rr] * vref.unit();
           if (patch && stretch_nan(p, s, bar.limit[r], least, key)) x = NAN;
           if (complete) {
             const int64_t at = static_cast<int64_t>(s.head * p.group + r % p.group) * p.n + s.st.t0 + r / p.group;
             const bool some = sum != 0.f;
             p.o[at * 128 + key] = __float2bfloat16_rn(some ? x / sum : 0.f);
-            if (p.lse && key == 0) p.lse[at] = some ? (m[r] + log2f(sum)) * kLn2 : -INFINITY;
+            if (p.lse && key == 0) p.lse[at] = some ? (m[rr] + log2f(sum)) * kLn2 : -INFINITY;
           } else {
             out[r * 128 + key] = sum != 0.f ? x : 0.f;
-            if (key == 0) *reinterpret_cast<float2*>(out + kFewRows * 128 + 2 * r) =
-                  make_float2(sum != 0.f ? m[r] : -INFINITY, sum);
+            if (key == 0)
+              *reinterpret_cast<float2*>(out + kFewRows * 128 + 2 * r) =
+                  make_float2(sum != 0.f ? m[rr] : -INFINITY, sum);
           }
         }
       }
       tc_fence_before();
-      named_bar_sync(1, 128);  // limit, sum and nan_seen have been read
-      if (key == 0) bar.nan_seen = 0;
+      named_bar_sync(1, kAll);  // limit, sum and nan_seen have been read
+      if (all == 0) bar.nan_seen = 0;
       ++seg;
     }
   }
@@ -650,7 +661,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 5) {
+  if (warp == 1) {
     __syncwarp();
     tmem_dealloc(tmem, kFewCols);
   }
@@ -725,24 +736,24 @@ int make_page_map(CUtensorMap* map, const void* base, int64_t rows) {
   return r == CUDA_SUCCESS ? CALIBATT_OK : CALIBATT_ERR_CUDA;
 }
 
-template <bool SW, int RB>
+template <bool SW, int RG, int G>
 int launch_few(const CUtensorMap& mk, const CUtensorMap& mv, const CacheAttnParams& p, const FewPlan& plan, float* ws,
                cudaStream_t stream) {
   static PerDeviceOnce once;
   const int rc =
-      set_max_smem_once(reinterpret_cast<const void*>(cache_few_kernel<SW, RB>), FewLayout::kDynSmem, once);
+      set_max_smem_once(reinterpret_cast<const void*>(cache_few_kernel<SW, RG, G>), FewLayout::kDynSmem, once);
   if (rc != CALIBATT_OK) return rc;
-  cache_few_kernel<SW, RB><<<plan.ctas, kFewThreads, FewLayout::kDynSmem, stream>>>(mk, mv, p, plan.whole, ws);
+  cache_few_kernel<SW, RG, G><<<plan.ctas, few_threads(G), FewLayout::kDynSmem, stream>>>(mk, mv, p, plan.whole, ws);
   return cudaGetLastError() == cudaSuccess ? CALIBATT_OK : CALIBATT_ERR_CUDA;
 }
 
 template <bool SW>
 int launch_few_rows(const CUtensorMap& mk, const CUtensorMap& mv, const CacheAttnParams& p, const FewPlan& plan,
                     float* ws, cudaStream_t stream) {
-  if (plan.rows <= 1) return launch_few<SW, 1>(mk, mv, p, plan, ws, stream);
-  if (plan.rows <= 4) return launch_few<SW, 4>(mk, mv, p, plan, ws, stream);
-  if (plan.rows <= 8) return launch_few<SW, 8>(mk, mv, p, plan, ws, stream);
-  return launch_few<SW, 16>(mk, mv, p, plan, ws, stream);
+  if (plan.rows <= 1) return launch_few<SW, 1, 1>(mk, mv, p, plan, ws, stream);
+  if (plan.rows <= 4) return launch_few<SW, 4, 1>(mk, mv, p, plan, ws, stream);
+  if (plan.rows <= 8) return launch_few<SW, 8, 1>(mk, mv, p, plan, ws, stream);
+  return launch_few<SW, 8, 2>(mk, mv, p, plan, ws, stream);
 }
 
 }  // namespace
