@@ -95,26 +95,32 @@ __device__ __forceinline__ float score_factor(float row, float key_scale) {
 // (2^15 * 448 * 2^31 keys), stays finite.
 template <int kLog, int kLow>
 struct VRef {
-  float ref = 0.f, top = 0.f;
-  float vs = -1.f, log = 0.f, inv = 0.f;  // the page's: its scale, P's factor as a log2, 1 / that factor
+  float ref = 0.f, top = 0.f, ref_inv = 0.f;
+  float vs = 0.f, log = 0.f, inv = 0.f;  // the page's: its scale, P's factor as a log2, 1 / that factor
 
   static constexpr float kUnit = 1.f / (1 << kLog);
+  // Scales change from page to page, so this is kept to a few instructions:
+  // the approximate logarithm and reciprocal are exact for powers of two, and
+  // within 2^-22 for others.
   __device__ __forceinline__ float page(float scale) {
-    if (scale == vs) return 1.f;
-    vs = scale;
-    if (scale == 0.f) scale = 1.17549435e-38f;
+    vs = scale == 0.f ? 1.17549435e-38f : scale;
     float ratio = 1.f;
     if (ref == 0.f) {
-      ref = top = scale;
-    } else if (scale > 2.f * ref || scale * (1 << -kLow) < ref) {
-      top = fmaxf(top, scale);
-      const float now = fmaxf(scale, top * 8.470329472543003e-22f);
+      ref = top = vs;
+      ref_inv = 1.f / ref;
+    } else if (vs > 2.f * ref || vs * (1 << -kLow) < ref) {
+      top = fmaxf(top, vs);
+      const float now = fmaxf(vs, top * 8.470329472543003e-22f);
       ratio = ref / now;
       ref = now;
+      ref_inv = 1.f / ref;
     }
-    const float f = scale / ref;
-    log = log2f(f) + kLog;
-    inv = kUnit / f;
+    const float f = vs * ref_inv;
+    float l2, r;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(l2) : "f"(f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(f));
+    log = l2 + kLog;
+    inv = kUnit * r;
     return ratio;
   }
   __device__ __forceinline__ float unit() const { return ref * kUnit; }
