@@ -1,6 +1,7 @@
 // Pieces shared by the kernels of the paged 8-bit cache: a stream's share of
 // the packed tokens, and e4m3 conversions.
 #pragma once
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -54,6 +55,15 @@ __device__ __forceinline__ uint32_t take_nan(uint32_t& w) {
 
 // Writes to shared memory become visible to TMA and the tensor core.
 __device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// 2D tiled load of one box into shared memory, completing on `bar`.
+__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y)
+      : "memory");
+}
 
 // Two packed e4m3 values to packed fp16: exact, NaN stays NaN.
 __device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t two) {
@@ -155,11 +165,7 @@ struct CacheAttnParams {
   const float* k_scale;
   const float* v_scale;
   int heads_q, heads_kv, group, n, batch, max_new, table_stride, n_pages, unit;
-  int tiles;               // row tiles of a stream and key head
-  int splits;              // of a row tile's pages
   float scale_log2;
-  float* part_o;           // [splits][heads_q][n][128]
-  float2* part_ml;         // [splits][heads_q][n]: maximum (log2 units), sum
   int* status;
   uint64_t wait_limit_ns;
 };
@@ -212,6 +218,77 @@ struct PageWindow {
   }
 };
 
+// Normalises and stores a row's four channels of a lane; no key seen: 0 and -inf.
+__device__ __forceinline__ void store_row(const CacheAttnParams& p, int64_t at, int lane, float mx, float sum,
+                                          const float4& o) {
+  const bool some = sum != 0.f;
+  const float inv = some ? 1.f / sum : 0.f;
+  uint2 w = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+  if (!some) w = make_uint2(0, 0);
+  *reinterpret_cast<uint2*>(p.o + at * 128 + lane * 4) = w;
+  if (p.lse && lane == 0) p.lse[at] = some ? (mx + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+}
+
+// Joins one row's partial results (a warp): those of CTAs c0 .. c1 - 1 for
+// which `slot` gives an address, each [rows][128] outputs, then maximum (log2
+// units) and sum per row. The lanes fetch 32 CTAs' maxima and sums at a time;
+// the outputs are then loaded independently of each other.
+template <class Slot>
+__device__ __forceinline__ void join_row(const CacheAttnParams& p, int64_t at, int lane, int c0, int c1,
+                                         const Slot& slot, int row, int rows) {
+  float mx = -INFINITY, sum = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int base = c0; base < c1; base += 32) {
+    const float* mine = base + lane < c1 ? slot(base + lane) : nullptr;
+    float2 ml = make_float2(-INFINITY, 0.f);
+    if (mine) ml = *reinterpret_cast<const float2*>(mine + rows * 128 + 2 * row);
+    float top = ml.x;
+#pragma unroll
+    for (int i = 16; i > 0; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
+    const float now = fmaxf(mx, top), use = now == -INFINITY ? 0.f : now;
+    const float keep = ex2_approx(mx - use), w = ex2_approx(ml.x - use);
+    mx = now;
+    float add = ml.y * w;
+#pragma unroll
+    for (int i = 16; i > 0; i >>= 1) add += __shfl_xor_sync(0xffffffffu, add, i);
+    sum = sum * keep + add;
+    o.x *= keep;
+    o.y *= keep;
+    o.z *= keep;
+    o.w *= keep;
+    unsigned have = __ballot_sync(0xffffffffu, mine != nullptr);
+    while (have) {
+      constexpr int kBatch = 4;
+      float4 x[kBatch];
+      float f[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int l = have ? __ffs(have) - 1 : 0;
+        const float* src =
+            reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), l));
+        f[i] = __shfl_sync(0xffffffffu, w, l);
+        x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (have)
+          x[i] = *reinterpret_cast<const float4*>(src + row * 128 + lane * 4);
+        else
+          f[i] = 0.f;
+        have &= have - 1;
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        o.x += x[i].x * f[i];
+        o.y += x[i].y * f[i];
+        o.z += x[i].z * f[i];
+        o.w += x[i].w * f[i];
+      }
+    }
+  }
+  store_row(p, at, lane, mx, sum, o);
+}
+
+// 128-byte rows of a pool's pages, boxes of one page with the 128-byte swizzle.
+int make_page_map(CUtensorMap* map, const void* pool, const CacheAttnParams& p);
+
 // Few query rows (up to 16 that share a key head): the streams' pages, key
 // head by key head, cut into equal shares for `ctas` CTAs; or, with `whole`, a
 // CTA for each key head of each stream.
@@ -225,8 +302,19 @@ FewPlan few_plan(int batch, int heads_kv, int rows, int64_t pages, int sms);
 size_t few_workspace_bytes(const FewPlan& plan);
 int launch_cache_attn_few(const CacheAttnParams& p, const FewPlan& plan, void* ws, cudaStream_t stream);
 
-// Many query rows: tiles of 128 rows (alternate: two slots of a CTA share
-// them and take every other page) or 256 rows on the tensor core.
-int launch_cache_attn_tiles(const CacheAttnParams& p, bool alternate, cudaStream_t stream);
+// Many query rows: tiles of 128 rows (two slots of a CTA share them and take
+// every other page) or 256 rows on the tensor core, one CTA per SM; with
+// `whole` the tiles are not split.
+struct TilePlan {
+  bool alternate, whole;
+  int tiles;  // of a stream and key head, at most
+  int ctas;
+};
+TilePlan tile_plan(int batch, int heads_kv, int64_t rows, int64_t pages, int sms);
+size_t tile_workspace_bytes(const TilePlan& plan);
+int launch_cache_attn_tiles(const CacheAttnParams& p, const TilePlan& plan, void* ws, cudaStream_t stream);
+
+// A partial result of a tile: O, then maximum (log2 units) and sum per row.
+__host__ __device__ constexpr int tile_part_floats(int rows) { return rows * 130; }
 
 }  // namespace calibatt

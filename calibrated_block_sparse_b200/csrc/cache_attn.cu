@@ -8,7 +8,7 @@
 // more by cache_tile.cu, bound by the tensor core. Both split the cache over
 // CTAs along its length; a split leaves its running maximum, sum and
 // unnormalised output in a workspace, and a second kernel joins them.
-// This file holds the entry points, the plan and the tiles' join.
+// This file holds the entry points and the plan.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -25,86 +25,45 @@
 #include "sched.cuh"
 
 namespace calibatt {
-namespace {
 
-// ------------------------------------------------------------------ joining the splits
-// A warp per row: weights 2^(m_s - max m), then the weighted sum of the
-// splits' outputs over the weighted sum of their sums.
-__global__ void __launch_bounds__(128) cache_attn_join_kernel(const __grid_constant__ CacheAttnParams p) {
-  const int lane = threadIdx.x & 31;
-  const int b = blockIdx.z;
-  const Stream st = stream_of(p.tok_start, p.kv_len, b, p.n, p.table_stride);
-  if (st.bad || st.n_new > p.max_new) return;
-  const int tok = blockIdx.x * 4 + (threadIdx.x >> 5);
-  if (tok >= st.n_new) return;
-  const int64_t at = static_cast<int64_t>(blockIdx.y) * p.n + st.t0 + tok;
-  const int64_t step = static_cast<int64_t>(p.heads_q) * p.n;
-  float mx = -INFINITY;
-  for (int s = lane; s < p.splits; s += 32) mx = fmaxf(mx, p.part_ml[s * step + at].x);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  const float use = mx == -INFINITY ? 0.f : mx;
-  float sum = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s = 0; s < p.splits; ++s) {
-    const float2 ml = p.part_ml[s * step + at];
-    if (ml.y == 0.f) continue;  // no key of the split is visible: its output was not written
-    const float f = ex2_approx(ml.x - use);
-    const float4 x = *reinterpret_cast<const float4*>(p.part_o + (s * step + at) * 128 + lane * 4);
-    sum += ml.y * f;
-    o.x += x.x * f;
-    o.y += x.y * f;
-    o.z += x.z * f;
-    o.w += x.w * f;
+int make_page_map(CUtensorMap* map, const void* pool, const CacheAttnParams& p) {
+  EncodeTiledFn enc = get_encode();
+  if (!enc) return CALIBATT_ERR_CUDA;
+  int64_t rows = static_cast<int64_t>(p.n_pages) * p.heads_kv * kPage;
+  if (rows > INT32_MAX) return CALIBATT_ERR_UNSUPPORTED;
+  if (rows == 0) {  // an empty pool is never read: the map needs an address all the same
+    pool = p.q;
+    rows = kPage;
   }
-  const bool some = sum != 0.f;
-  const float inv = some ? 1.f / sum : 0.f;
-  uint2 w = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-  if (!some) w = make_uint2(0, 0);
-  *reinterpret_cast<uint2*>(p.o + at * 128 + lane * 4) = w;
-  if (p.lse && lane == 0) p.lse[at] = some ? (mx + log2f(sum)) * kLn2 : -INFINITY;
+  cuuint64_t dims[2] = {128, static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[1] = {128};
+  cuuint32_t box[2] = {128, kPage};
+  cuuint32_t estr[2] = {1, 1};
+  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(pool), dims, strides, box, estr,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? CALIBATT_OK : CALIBATT_ERR_CUDA;
 }
 
+namespace {
+
 // ------------------------------------------------------------------ plan
+// Which kernel, and how its work is shared out, from the host's bounds alone.
 struct CachePlan {
-  bool few, alternate;  // the kernel for up to 16 rows; tiles of 128 rows instead of 256
-  int tiles, splits;    // of the tile kernel
+  bool few;
   FewPlan fp;
+  TilePlan tp;
 };
 
-// Which kernel, how many row tiles, and into how many splits a tile's pages
-// are cut, from the host's bounds alone.
-// Tiles: one CTA per SM, so the splits that give the shortest schedule: waves
-// of CTAs times the pages of one (plus its start and end, about 3 pages' time),
-// plus the joining's traffic (8 bytes per output value and split; a page takes
-// a tile about 1.1 us).
 CachePlan cache_plan(int batch, int heads_q, int heads_kv, int n, int max_new, int max_kv) {
-  CachePlan c;
+  CachePlan c{};
   const int64_t rows = static_cast<int64_t>(std::min(max_new, n)) * (heads_q / heads_kv);
-  c.few = rows <= kFewRows;
-  c.alternate = rows <= 128;
   const int64_t pages = std::max<int64_t>(1, (static_cast<int64_t>(max_kv) + kPage - 1) / kPage);
-  const int sms = sm_count();
-  if (c.few) {
-    c.tiles = c.splits = 1;
-    c.fp = few_plan(batch, heads_kv, static_cast<int>(rows), pages, sms);
-    return c;
-  }
-  const int tile = c.alternate ? 128 : 256;
-  c.tiles = static_cast<int>((rows + tile - 1) / tile);
-  const int64_t units = static_cast<int64_t>(batch) * heads_kv * c.tiles;
-  const double join = static_cast<double>(heads_q) * std::min<int64_t>(static_cast<int64_t>(batch) * max_new, n) *
-                      1024.0 / 6.5e12 / 1.1e-6;
-  double best = 0.0;
-  c.splits = 1;
-  for (int s = 1; s <= 64 && s <= pages; ++s) {
-    const double waves = static_cast<double>((units * s + sms - 1) / sms);
-    const double time = waves * ((pages + s - 1) / s + 3.0) + (s > 1 ? 4.0 + s * join : 0.0);
-    if (s == 1 || time < best) {
-      best = time;
-      c.splits = s;
-    }
-  }
+  c.few = rows <= kFewRows;
+  if (c.few)
+    c.fp = few_plan(batch, heads_kv, static_cast<int>(rows), pages, sm_count());
+  else
+    c.tp = tile_plan(batch, heads_kv, rows, pages, sm_count());
   return c;
 }
 
@@ -117,10 +76,8 @@ int check_shape(int batch, int heads_q, int heads_kv, int n, int max_new, int ma
   return CALIBATT_OK;
 }
 
-size_t workspace_bytes(const CachePlan& c, int heads_q, int n) {
-  if (c.few) return few_workspace_bytes(c.fp);
-  if (c.splits <= 1) return 0;
-  return static_cast<size_t>(c.splits) * heads_q * n * (128 * sizeof(float) + sizeof(float2));
+size_t workspace_bytes(const CachePlan& c) {
+  return c.few ? few_workspace_bytes(c.fp) : tile_workspace_bytes(c.tp);
 }
 
 }  // namespace
@@ -132,7 +89,7 @@ size_t calibatt_cache_attn_workspace_size(int batch, int heads_q, int heads_kv, 
   using namespace calibatt;
   if (check_shape(batch, heads_q, heads_kv, n, max_new, max_kv) != CALIBATT_OK) return 0;
   if (batch == 0 || n == 0 || max_new == 0) return 0;
-  return workspace_bytes(cache_plan(batch, heads_q, heads_kv, n, max_new, max_kv), heads_q, n);
+  return workspace_bytes(cache_plan(batch, heads_q, heads_kv, n, max_new, max_kv));
 }
 
 int calibatt_cache_attn_fwd(const calibatt_bf16* q, int heads_q, int heads_kv, int n, int d, float scale,
@@ -159,7 +116,7 @@ int calibatt_cache_attn_fwd(const calibatt_bf16* q, int heads_q, int heads_kv, i
                         static_cast<const void*>(v_scale), static_cast<const void*>(lse)})
     if (reinterpret_cast<uintptr_t>(x) & 3u) return CALIBATT_ERR_ALIGN;
   const CachePlan plan = cache_plan(batch, heads_q, heads_kv, n, max_new, max_kv);
-  const size_t need = workspace_bytes(plan, heads_q, n);
+  const size_t need = workspace_bytes(plan);
   if (need > 0 && (!ws || ws_bytes < need)) return CALIBATT_ERR_ARG;
   CacheAttnParams p{};
   p.status = status_word();
@@ -183,23 +140,9 @@ int calibatt_cache_attn_fwd(const calibatt_bf16* q, int heads_q, int heads_kv, i
   p.table_stride = table_stride;
   p.n_pages = n_pages;
   p.unit = causal_unit;
-  p.tiles = plan.tiles;
-  p.splits = plan.splits;
   p.scale_log2 = scale * 1.4426950408889634f;
-  p.part_o = static_cast<float*>(ws);
-  p.part_ml = reinterpret_cast<float2*>(p.part_o + static_cast<int64_t>(plan.splits) * heads_q * n * 128);
-  const int64_t y = static_cast<int64_t>(heads_kv) * plan.tiles;
-  if (y > 65535) return CALIBATT_ERR_UNSUPPORTED;
   p.wait_limit_ns = wait_limit_ns();
-  if (plan.few) return launch_cache_attn_few(p, plan.fp, ws, stream);
-  rc = launch_cache_attn_tiles(p, plan.alternate, stream);
-  if (rc != CALIBATT_OK) return rc;
-  if (plan.splits > 1) {
-    const unsigned gx = (std::min(max_new, n) + 3) / 4;
-    cache_attn_join_kernel<<<dim3(gx, heads_q, batch), 128, 0, stream>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return CALIBATT_ERR_CUDA;
-  }
-  return CALIBATT_OK;
+  return plan.few ? launch_cache_attn_few(p, plan.fp, ws, stream) : launch_cache_attn_tiles(p, plan.tp, ws, stream);
 }
 
 }  // extern "C"

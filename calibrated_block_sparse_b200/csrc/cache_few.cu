@@ -106,15 +106,6 @@ __device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_
       : "memory");
 }
 
-// 2D tiled load of one box into shared memory, completing on `bar`.
-__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y)
-      : "memory");
-}
-
 // Vote of a group's four warps.
 __device__ __forceinline__ bool vote_128(int id, bool x) {
   uint32_t r;
@@ -146,17 +137,6 @@ __device__ __forceinline__ float three_bits(float x) { return __uint_as_float(__
 
 __device__ __forceinline__ uint32_t to_e5m2x2(float lo, float hi) {
   return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E5M2);
-}
-
-// Normalises and stores a row's four channels of a lane; no key seen: 0 and -inf.
-__device__ __forceinline__ void store_row(const CacheAttnParams& p, int64_t at, int lane, float mx, float sum,
-                                          const float4& o) {
-  const bool some = sum != 0.f;
-  const float inv = some ? 1.f / sum : 0.f;
-  uint2 w = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-  if (!some) w = make_uint2(0, 0);
-  *reinterpret_cast<uint2*>(p.o + at * 128 + lane * 4) = w;
-  if (p.lse && lane == 0) p.lse[at] = some ? (mx + log2f(sum)) * kLn2 : -INFINITY;
 }
 
 // Pages of stream b that its last new token sees (at least one, so that rows
@@ -698,42 +678,17 @@ __global__ void __launch_bounds__(128)
   while (c > 0 && share_begin(total, c, ctas) > u0) --c;
   if (share_begin(total, c + 1, ctas) >= u1) return;  // one CTA had all of them and wrote the result
   const int rows = st.n_new * p.group;
-  for (int r = warp; r < rows; r += 4) {
-    float mx = -INFINITY, sum = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    int64_t w0;
-    for (int i = c; i < ctas && (w0 = share_begin(total, i, ctas)) < u1; ++i) {
-      if (w0 == share_begin(total, i + 1, ctas)) continue;  // an empty share
-      // a CTA's first stretch is in its first slot, its last in the second
-      const float* at = part + (2 * static_cast<int64_t>(i) + (w0 < u0)) * kFewPartFloats;
-      const float2 ml = *reinterpret_cast<const float2*>(at + kFewRows * 128 + 2 * r);
-      const float4 x = *reinterpret_cast<const float4*>(at + r * 128 + lane * 4);
-      const float now = fmaxf(mx, ml.x);
-      const float use = now == -INFINITY ? 0.f : now;
-      const float f0 = ex2_approx(mx - use), f1 = ex2_approx(ml.x - use);
-      sum = sum * f0 + ml.y * f1;
-      o.x = o.x * f0 + x.x * f1;
-      o.y = o.y * f0 + x.y * f1;
-      o.z = o.z * f0 + x.z * f1;
-      o.w = o.w * f0 + x.w * f1;
-      mx = now;
-    }
-    store_row(p, static_cast<int64_t>(head * p.group + r % p.group) * p.n + st.t0 + r / p.group, lane, mx, sum, o);
-  }
-}
-
-// 128-byte rows of the cache's pages, boxes of one page with the 128-byte swizzle.
-int make_page_map(CUtensorMap* map, const void* base, int64_t rows) {
-  EncodeTiledFn enc = get_encode();
-  if (!enc) return CALIBATT_ERR_CUDA;
-  cuuint64_t dims[2] = {128, static_cast<cuuint64_t>(rows)};
-  cuuint64_t strides[1] = {128};
-  cuuint32_t box[2] = {128, kPage};
-  cuuint32_t estr[2] = {1, 1};
-  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
-                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? CALIBATT_OK : CALIBATT_ERR_CUDA;
+  const int last = static_cast<int>(std::min<int64_t>(ctas, (u1 * ctas + total - 1) / total + 1));
+  for (int r = warp; r < rows; r += 4)
+    join_row(
+        p, static_cast<int64_t>(head * p.group + r % p.group) * p.n + st.t0 + r / p.group, lane, c, last,
+        [&](int i) -> const float* {
+          const int64_t w0 = share_begin(total, i, ctas);
+          if (w0 >= u1 || w0 == share_begin(total, i + 1, ctas)) return nullptr;  // behind, or an empty share
+          // a CTA's first stretch is in its first slot, its last in the second
+          return part + (2 * static_cast<int64_t>(i) + (w0 < u0)) * kFewPartFloats;
+        },
+        r, kFewRows);
 }
 
 template <bool SW, int RG, int G>
@@ -774,11 +729,8 @@ size_t few_workspace_bytes(const FewPlan& plan) {
 
 int launch_cache_attn_few(const CacheAttnParams& p, const FewPlan& plan, void* ws, cudaStream_t stream) {
   CUtensorMap mk, mv;
-  const int64_t rows = static_cast<int64_t>(p.n_pages) * p.heads_kv * kPage;
-  if (rows > INT32_MAX) return CALIBATT_ERR_UNSUPPORTED;
-  // an empty pool is never read: the maps need an address all the same
-  int rc = make_page_map(&mk, rows ? static_cast<const void*>(p.k8) : p.q, rows ? rows : kPage);
-  if (rc == CALIBATT_OK) rc = make_page_map(&mv, rows ? static_cast<const void*>(p.v8) : p.q, rows ? rows : kPage);
+  int rc = make_page_map(&mk, p.k8, p);
+  if (rc == CALIBATT_OK) rc = make_page_map(&mv, p.v8, p);
   if (rc != CALIBATT_OK) return rc;
   float* part = static_cast<float*>(ws);
   rc = p.wait_limit_ns < kShortWaitNs ? launch_few_rows<true>(mk, mv, p, plan, part, stream)
