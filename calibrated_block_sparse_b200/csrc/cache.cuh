@@ -165,6 +165,7 @@ struct CacheAttnParams {
   const float* k_scale;
   const float* v_scale;
   int heads_q, heads_kv, group, n, batch, max_new, table_stride, n_pages, unit;
+  int max_rows;            // of a stream and key head that the kernel is laid out for
   float scale_log2;
   int* status;
   uint64_t wait_limit_ns;
@@ -229,13 +230,13 @@ __device__ __forceinline__ void store_row(const CacheAttnParams& p, int64_t at, 
   if (p.lse && lane == 0) p.lse[at] = some ? (mx + log2f(sum)) * 0.6931471805599453f : -INFINITY;
 }
 
-// Joins one row's partial results (a warp): those of CTAs c0 .. c1 - 1 for
+// Joins one row's partial results (a warp): those of parts c0 .. c1 - 1 for
 // which `slot` gives an address, each [rows][128] outputs, then maximum (log2
-// units) and sum per row. The lanes fetch 32 CTAs' maxima and sums at a time;
+// units) and sum per row. The lanes fetch 32 parts' maxima and sums at a time;
 // the outputs are then loaded independently of each other.
 template <class Slot>
 __device__ __forceinline__ void join_row(const CacheAttnParams& p, int64_t at, int lane, int c0, int c1,
-                                         const Slot& slot, int row, int rows) {
+                                         const Slot& slot, int64_t row, int64_t rows) {
   float mx = -INFINITY, sum = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int base = c0; base < c1; base += 32) {
@@ -289,32 +290,32 @@ __device__ __forceinline__ void join_row(const CacheAttnParams& p, int64_t at, i
 // 128-byte rows of a pool's pages, boxes of one page with the 128-byte swizzle.
 int make_page_map(CUtensorMap* map, const void* pool, const CacheAttnParams& p);
 
-// Few query rows (up to 16 that share a key head): the streams' pages, key
-// head by key head, cut into equal shares for `ctas` CTAs; or, with `whole`, a
-// CTA for each key head of each stream.
-constexpr int kFewRows = 16;
-struct FewPlan {
+// Up to 16, up to 128 and more query rows that share a key head.
+constexpr int kFewRows = 16, kMidRows = 128, kTileRows = 256;
+
+// Few and mid rows: the streams' pages, key head by key head, cut into equal
+// shares for `ctas` CTAs; or, with `whole`, a CTA for each key head of each
+// stream, and nothing to join.
+struct SharePlan {
   bool whole;
   int ctas;
   int rows;  // the most that a key head has
 };
-FewPlan few_plan(int batch, int heads_kv, int rows, int64_t pages, int sms);
-size_t few_workspace_bytes(const FewPlan& plan);
-int launch_cache_attn_few(const CacheAttnParams& p, const FewPlan& plan, void* ws, cudaStream_t stream);
+int launch_cache_attn_few(const CacheAttnParams& p, const SharePlan& plan, void* ws, cudaStream_t stream);
+int launch_cache_attn_mid(const CacheAttnParams& p, const SharePlan& plan, void* ws, cudaStream_t stream);
+// Joins their partial results, for kernels laid out for `cap` rows.
+int launch_cache_join(const CacheAttnParams& p, const SharePlan& plan, const float* part, int cap,
+                      cudaStream_t stream);
 
-// Many query rows: tiles of 128 rows (two slots of a CTA share them and take
-// every other page) or 256 rows on the tensor core, one CTA per SM; with
-// `whole` the tiles are not split.
+// Many rows: tiles of 256 rows, the pages of each cut into `splits`.
 struct TilePlan {
-  bool alternate, whole;
   int tiles;  // of a stream and key head, at most
-  int ctas;
+  int splits;
 };
-TilePlan tile_plan(int batch, int heads_kv, int64_t rows, int64_t pages, int sms);
-size_t tile_workspace_bytes(const TilePlan& plan);
+// Rows of a split's partial results: an even number, for 16-byte alignment.
+__host__ __device__ constexpr int64_t tile_part_rows(int heads_q, int n) {
+  return (static_cast<int64_t>(heads_q) * n + 1) / 2 * 2;
+}
 int launch_cache_attn_tiles(const CacheAttnParams& p, const TilePlan& plan, void* ws, cudaStream_t stream);
-
-// A partial result of a tile: O, then maximum (log2 units) and sum per row.
-__host__ __device__ constexpr int tile_part_floats(int rows) { return rows * 130; }
 
 }  // namespace calibatt

@@ -5,10 +5,11 @@
 // The query rows that share a key head (its group of query heads, times the
 // new tokens of a stream) are taken together, so a cached byte is read once
 // for all of them: up to 16 rows by cache_few.cu, bound by the cache's bytes,
-// more by cache_tile.cu, bound by the tensor core. Both split the cache over
-// CTAs along its length; a split leaves its running maximum, sum and
-// unnormalised output in a workspace, and a second kernel joins them.
-// This file holds the entry points and the plan.
+// up to 128 by cache_mid.cu, more by cache_tile.cu, bound by the tensor core
+// and the softmax beside it. All split the cache over CTAs along its length; a
+// part leaves its running maximum, sum and unnormalised output in a workspace,
+// and a second kernel joins them. This file holds the entry points, the plan
+// and the join.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -19,12 +20,74 @@
 #include <cstdint>
 
 #include "cache.cuh"
+#include "cache_list.cuh"
 #include "calibatt.h"
 #include "kernels.h"
 #include "ptx.cuh"
 #include "sched.cuh"
 
 namespace calibatt {
+namespace {
+
+// Joins the stretches of one (stream, key head): those of the CTAs whose
+// shares meet its pages. A warp per row, 8 rows per CTA.
+constexpr int kJoinRows = 8;
+__global__ void __launch_bounds__(32 * kJoinRows)
+    cache_join_kernel(const __grid_constant__ CacheAttnParams p, int ctas, const float* part, int cap) {
+  const int lane = threadIdx.x & 31, row = blockIdx.z * kJoinRows + (threadIdx.x >> 5);
+  const int head = blockIdx.x, b = blockIdx.y;
+  const Stream st = stream_of(p.tok_start, p.kv_len, b, p.n, p.table_stride);
+  const int pages = stream_pages(p, st);
+  int64_t before = 0, total = 0;
+  if (pages > 0) {
+    for (int i = lane; i < p.batch; i += 32) {
+      const int64_t x = stream_pages(p, stream_of(p.tok_start, p.kv_len, i, p.n, p.table_stride));
+      total += x;
+      if (i < b) before += x;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      total += __shfl_xor_sync(0xffffffffu, total, o);
+      before += __shfl_xor_sync(0xffffffffu, before, o);
+    }
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (pages == 0 || row >= st.n_new * p.group) return;
+  total *= p.heads_kv;
+  const int64_t u0 = before * p.heads_kv + static_cast<int64_t>(head) * pages, u1 = u0 + pages;
+  // the last CTA whose share begins at or before u0
+  int c = static_cast<int>(u0 * ctas / total);
+  while (c + 1 < ctas && share_begin(total, c + 1, ctas) <= u0) ++c;
+  while (c > 0 && share_begin(total, c, ctas) > u0) --c;
+  if (share_begin(total, c + 1, ctas) >= u1) return;  // one CTA had all of them and wrote the result
+  const int last = static_cast<int>(min(static_cast<int64_t>(ctas), (u1 * ctas + total - 1) / total + 1));
+  join_row(
+      p, static_cast<int64_t>(head * p.group + row % p.group) * p.n + st.t0 + row / p.group, lane, c, last,
+      [&](int i) -> const float* {
+        const int64_t w0 = share_begin(total, i, ctas);
+        if (w0 >= u1 || w0 == share_begin(total, i + 1, ctas)) return nullptr;  // behind, or an empty share
+        return part_of(const_cast<float*>(part), i, w0 > u0, cap);
+      },
+      row, cap);
+}
+
+}  // namespace
+
+int launch_cache_join(const CacheAttnParams& p, const SharePlan& plan, const float* part, int cap,
+                      cudaStream_t stream) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(p.heads_kv, p.batch, (plan.rows + kJoinRows - 1) / kJoinRows);
+  cfg.blockDim = dim3(32 * kJoinRows);
+  cfg.stream = stream;
+  // it may be resident while the pages are still read: it waits in the kernel
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, cache_join_kernel, p, plan.ctas, part, cap) == cudaSuccess ? CALIBATT_OK
+                                                                                             : CALIBATT_ERR_CUDA;
+}
 
 int make_page_map(CUtensorMap* map, const void* pool, const CacheAttnParams& p) {
   EncodeTiledFn enc = get_encode();
@@ -50,20 +113,67 @@ namespace {
 // ------------------------------------------------------------------ plan
 // Which kernel, and how its work is shared out, from the host's bounds alone.
 struct CachePlan {
-  bool few;
-  FewPlan fp;
-  TilePlan tp;
+  int rows;  // the most that share a key head, in one stream
+  SharePlan share;
+  TilePlan tile;
 };
+
+// Shares for `slots` CTAs that run at the same time. Up to 4 pages the join
+// costs more than the split saves. Where the streams' key heads fit a whole
+// number of times, their pages are cut alike and no share crosses from one to
+// the next, which costs about 4 pages' time (its start and end once more);
+// ragged streams cross anyway. A share has at least two pages.
+SharePlan share_plan(int batch, int heads_kv, int rows, int64_t pages, int slots) {
+  SharePlan f;
+  const int64_t units = static_cast<int64_t>(batch) * heads_kv;
+  f.rows = rows;
+  f.whole = pages <= 4;
+  int64_t ctas = units;
+  if (!f.whole) {
+    ctas = slots;
+    if (units <= slots) {
+      const int64_t each = slots / units;
+      if ((pages + each - 1) / each <= (pages * units + slots - 1) / slots + 4) ctas = units * each;
+    }
+    ctas = std::min<int64_t>(ctas, units * ((pages + 1) / 2));
+  }
+  f.ctas = static_cast<int>(ctas);
+  return f;
+}
+
+// One CTA per SM, so the splits that give the shortest schedule: waves of CTAs
+// times the pages of one (plus its start and end, about 3 pages' time), plus
+// the joining's traffic (8 bytes per output value and split; a page takes a
+// tile about 1.1 us).
+TilePlan tile_plan(int batch, int heads_q, int heads_kv, int n, int max_new, int64_t rows, int64_t pages, int sms) {
+  TilePlan t;
+  t.tiles = static_cast<int>((rows + kTileRows - 1) / kTileRows);
+  const int64_t units = static_cast<int64_t>(batch) * heads_kv * t.tiles;
+  const double join = static_cast<double>(heads_q) * std::min<int64_t>(static_cast<int64_t>(batch) * max_new, n) *
+                      1024.0 / 6.5e12 / 1.1e-6;
+  double best = 0.0;
+  t.splits = 1;
+  for (int s = 1; s <= 64 && s <= pages; ++s) {
+    const double waves = static_cast<double>((units * s + sms - 1) / sms);
+    const double time = waves * ((pages + s - 1) / s + 3.0) + (s > 1 ? 4.0 + s * join : 0.0);
+    if (s == 1 || time < best) {
+      best = time;
+      t.splits = s;
+    }
+  }
+  return t;
+}
 
 CachePlan cache_plan(int batch, int heads_q, int heads_kv, int n, int max_new, int max_kv) {
   CachePlan c{};
   const int64_t rows = static_cast<int64_t>(std::min(max_new, n)) * (heads_q / heads_kv);
   const int64_t pages = std::max<int64_t>(1, (static_cast<int64_t>(max_kv) + kPage - 1) / kPage);
-  c.few = rows <= kFewRows;
-  if (c.few)
-    c.fp = few_plan(batch, heads_kv, static_cast<int>(rows), pages, sm_count());
+  const int sms = sm_count();
+  c.rows = static_cast<int>(rows);
+  if (rows <= kMidRows)
+    c.share = share_plan(batch, heads_kv, c.rows, pages, rows <= kFewRows ? 2 * sms : sms);
   else
-    c.tp = tile_plan(batch, heads_kv, rows, pages, sm_count());
+    c.tile = tile_plan(batch, heads_q, heads_kv, n, max_new, rows, pages, sms);
   return c;
 }
 
@@ -76,8 +186,14 @@ int check_shape(int batch, int heads_q, int heads_kv, int n, int max_new, int ma
   return CALIBATT_OK;
 }
 
-size_t workspace_bytes(const CachePlan& c) {
-  return c.few ? few_workspace_bytes(c.fp) : tile_workspace_bytes(c.tp);
+size_t workspace_bytes(const CachePlan& c, int heads_q, int n) {
+  if (c.rows <= kMidRows) {
+    if (c.share.whole) return 0;
+    const int cap = c.rows <= kFewRows ? kFewRows : kMidRows;
+    return 2 * static_cast<size_t>(c.share.ctas) * part_floats(cap) * sizeof(float);
+  }
+  if (c.tile.splits <= 1) return 0;
+  return c.tile.splits * static_cast<size_t>(tile_part_rows(heads_q, n)) * part_floats(1) * sizeof(float);
 }
 
 }  // namespace
@@ -89,7 +205,7 @@ size_t calibatt_cache_attn_workspace_size(int batch, int heads_q, int heads_kv, 
   using namespace calibatt;
   if (check_shape(batch, heads_q, heads_kv, n, max_new, max_kv) != CALIBATT_OK) return 0;
   if (batch == 0 || n == 0 || max_new == 0) return 0;
-  return workspace_bytes(cache_plan(batch, heads_q, heads_kv, n, max_new, max_kv));
+  return workspace_bytes(cache_plan(batch, heads_q, heads_kv, n, max_new, max_kv), heads_q, n);
 }
 
 int calibatt_cache_attn_fwd(const calibatt_bf16* q, int heads_q, int heads_kv, int n, int d, float scale,
@@ -116,7 +232,7 @@ int calibatt_cache_attn_fwd(const calibatt_bf16* q, int heads_q, int heads_kv, i
                         static_cast<const void*>(v_scale), static_cast<const void*>(lse)})
     if (reinterpret_cast<uintptr_t>(x) & 3u) return CALIBATT_ERR_ALIGN;
   const CachePlan plan = cache_plan(batch, heads_q, heads_kv, n, max_new, max_kv);
-  const size_t need = workspace_bytes(plan);
+  const size_t need = workspace_bytes(plan, heads_q, n);
   if (need > 0 && (!ws || ws_bytes < need)) return CALIBATT_ERR_ARG;
   CacheAttnParams p{};
   p.status = status_word();
@@ -142,7 +258,10 @@ int calibatt_cache_attn_fwd(const calibatt_bf16* q, int heads_q, int heads_kv, i
   p.unit = causal_unit;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.wait_limit_ns = wait_limit_ns();
-  return plan.few ? launch_cache_attn_few(p, plan.fp, ws, stream) : launch_cache_attn_tiles(p, plan.tp, ws, stream);
+  p.max_rows = plan.rows <= kFewRows ? kFewRows : plan.rows <= kMidRows ? kMidRows : INT_MAX;
+  if (plan.rows <= kFewRows) return launch_cache_attn_few(p, plan.share, ws, stream);
+  if (plan.rows <= kMidRows) return launch_cache_attn_mid(p, plan.share, ws, stream);
+  return launch_cache_attn_tiles(p, plan.tile, ws, stream);
 }
 
 }  // extern "C"

@@ -6,7 +6,7 @@
 // streams' lengths are (they are read on the device), so no SM waits for a
 // long stream. A stretch of a share that is not all of its stream's pages
 // leaves maximum, sum and unnormalised output in the workspace, and
-// cache_few_join_kernel joins them.
+// cache_join_kernel joins them.
 //
 // The tensor core multiplies the cache's bytes as they are: a page is the
 // 128-row operand A, K as it lies in memory and V transposed, and the few rows
@@ -41,6 +41,7 @@
 #include <cstdint>
 
 #include "cache.cuh"
+#include "cache_list.cuh"
 #include "calibatt.h"
 #include "kernels.h"
 #include "ptx.cuh"
@@ -52,7 +53,6 @@ namespace {
 constexpr int few_threads(int groups) { return 64 + 128 * groups; }
 constexpr int kFewRing = 5;
 constexpr int kPageBytes = kPage * 128;
-constexpr int kFewPartFloats = kFewRows * 128 + 2 * kFewRows;  // a partial result: O, then maximum and sum per row
 constexpr float kFewStale = 4.0f;                              // log2 units
 constexpr float kNoMax = -3e38f;                               // of a row that has seen no key
 constexpr int kQParts = 3, kPParts = 4;
@@ -139,111 +139,6 @@ __device__ __forceinline__ uint32_t to_e5m2x2(float lo, float hi) {
   return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E5M2);
 }
 
-// Pages of stream b that its last new token sees (at least one, so that rows
-// which see nothing are written), 0 for a stream without new tokens.
-__device__ __forceinline__ int stream_pages(const CacheAttnParams& p, const Stream& st) {
-  if (st.bad || st.n_new == 0 || st.n_new > p.max_new || st.n_new * p.group > kFewRows) return 0;
-  return max(1, (visible(st.len - 1, st.len, p.unit) + kPage - 1) / kPage);
-}
-
-// The list of all (stream, key head, page) triples.
-struct PageList {
-  // its length; every lane of the warp gets it
-  static __device__ int64_t total(const CacheAttnParams& p, int lane) {
-    int64_t sum = 0;
-    for (int b = lane; b < p.batch; b += 32)
-      sum += stream_pages(p, stream_of(p.tok_start, p.kv_len, b, p.n, p.table_stride));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    return sum * p.heads_kv;
-  }
-  // the stream of entry w, and the entry that its pages begin at
-  static __device__ int find(const CacheAttnParams& p, int64_t w, int lane, int64_t& begin) {
-    begin = 0;
-    for (int b0 = 0; b0 < p.batch; b0 += 32) {
-      int64_t mine = 0;
-      if (b0 + lane < p.batch)
-        mine = static_cast<int64_t>(p.heads_kv) *
-               stream_pages(p, stream_of(p.tok_start, p.kv_len, b0 + lane, p.n, p.table_stride));
-      int64_t end = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, end, o);
-        if (lane >= o) end += y;
-      }
-      const unsigned behind = __ballot_sync(0xffffffffu, begin + end > w);
-      if (behind) {
-        const int at = __ffs(behind) - 1;
-        begin += __shfl_sync(0xffffffffu, end - mine, at);
-        return b0 + at;
-      }
-      begin += __shfl_sync(0xffffffffu, end, 31);
-    }
-    return p.batch;
-  }
-};
-
-// First entry of CTA c's share of `total` entries.
-__device__ __forceinline__ int64_t share_begin(int64_t total, int c, int ctas) { return total * c / ctas; }
-
-// A CTA's walk: consecutive pages pg .. pg + count - 1 of one stream and head.
-struct Stretch {
-  int b, head, pg, count, pages;
-  Stream st;
-};
-
-struct Walk {
-  int64_t w, end;
-  int b, head, pg, pages;
-  Stream st;
-
-  __device__ __forceinline__ void load_stream(const CacheAttnParams& p) {
-    st = stream_of(p.tok_start, p.kv_len, b, p.n, p.table_stride);
-    pages = stream_pages(p, st);
-  }
-  __device__ void start(const CacheAttnParams& p, bool whole, int lane) {
-    if (whole) {
-      b = blockIdx.x / p.heads_kv;
-      head = blockIdx.x % p.heads_kv;
-      pg = 0;
-      load_stream(p);
-      w = 0;
-      end = pages;
-      return;
-    }
-    const int64_t total = PageList::total(p, lane);
-    w = share_begin(total, blockIdx.x, gridDim.x);
-    end = share_begin(total, blockIdx.x + 1, gridDim.x);
-    if (w >= end) return;
-    int64_t begin;
-    b = PageList::find(p, w, lane, begin);
-    load_stream(p);
-    head = static_cast<int>((w - begin) / pages);
-    pg = static_cast<int>((w - begin) % pages);
-  }
-  __device__ bool next(const CacheAttnParams& p, Stretch& s) {
-    if (w >= end) return false;
-    s.b = b;
-    s.head = head;
-    s.pg = pg;
-    s.pages = pages;
-    s.st = st;
-    s.count = static_cast<int>(min(static_cast<int64_t>(pages - pg), end - w));
-    w += s.count;
-    if (w < end) {
-      pg = 0;
-      if (++head == p.heads_kv) {
-        head = 0;
-        do {
-          ++b;
-          load_stream(p);
-        } while (pages == 0);
-      }
-    }
-    return true;
-  }
-};
-
 // Where V of page i of a stretch of `count` is in the ring's order.
 __device__ __forceinline__ uint32_t v_tile(int i, int count) { return i + 1 < count ? 2 * i + 2 : 2 * i + 1; }
 
@@ -304,8 +199,7 @@ __global__ void __launch_bounds__(few_threads(G), 2)
   if (blockIdx.x == 0 && warp == 0)
     for (int b = lane; b < p.batch; b += 32) {
       const Stream st = stream_of(p.tok_start, p.kv_len, b, p.n, p.table_stride);
-      if (st.bad || st.n_new > p.max_new || st.n_new * static_cast<int64_t>(p.group) > kFewRows)
-        record_error(p.status, CALIBATT_ERR_CSR);
+      if (!stream_fits(p, st)) record_error(p.status, CALIBATT_ERR_CSR);
     }
 
   Walk walk;
@@ -609,7 +503,7 @@ __global__ void __launch_bounds__(few_threads(G), 2)
       named_bar_sync(1, kAll);
       const bool complete = s.count == s.pages;
       const bool patch = *const_cast<volatile int*>(&bar.nan_seen) != 0;
-      float* out = part + (2 * static_cast<int64_t>(blockIdx.x) + (seg > 0)) * kFewPartFloats;
+      float* out = part_of(part, blockIdx.x, s.pg > 0, kFewRows);
       if (ok && *abort_flag == 0) {
 #pragma unroll
         for (int rr = 0; rr < RG; ++rr) {
@@ -647,52 +541,8 @@ __global__ void __launch_bounds__(few_threads(G), 2)
   }
 }
 
-// Joins the stretches of one (stream, key head): the CTAs whose shares meet
-// its pages, in order. A warp per row.
-__global__ void __launch_bounds__(128)
-    cache_few_join_kernel(const __grid_constant__ CacheAttnParams p, int ctas, const float* part) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int head = blockIdx.x, b = blockIdx.y;
-  const Stream st = stream_of(p.tok_start, p.kv_len, b, p.n, p.table_stride);
-  const int pages = stream_pages(p, st);
-  int64_t before = 0, total = 0;
-  if (pages > 0) {
-    for (int i = lane; i < p.batch; i += 32) {
-      const int64_t x = stream_pages(p, stream_of(p.tok_start, p.kv_len, i, p.n, p.table_stride));
-      total += x;
-      if (i < b) before += x;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      total += __shfl_xor_sync(0xffffffffu, total, o);
-      before += __shfl_xor_sync(0xffffffffu, before, o);
-    }
-  }
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (pages == 0) return;
-  total *= p.heads_kv;
-  const int64_t u0 = before * p.heads_kv + static_cast<int64_t>(head) * pages, u1 = u0 + pages;
-  // the last CTA whose share begins at or before u0
-  int c = static_cast<int>(u0 * ctas / total);
-  while (c + 1 < ctas && share_begin(total, c + 1, ctas) <= u0) ++c;
-  while (c > 0 && share_begin(total, c, ctas) > u0) --c;
-  if (share_begin(total, c + 1, ctas) >= u1) return;  // one CTA had all of them and wrote the result
-  const int rows = st.n_new * p.group;
-  const int last = static_cast<int>(std::min<int64_t>(ctas, (u1 * ctas + total - 1) / total + 1));
-  for (int r = warp; r < rows; r += 4)
-    join_row(
-        p, static_cast<int64_t>(head * p.group + r % p.group) * p.n + st.t0 + r / p.group, lane, c, last,
-        [&](int i) -> const float* {
-          const int64_t w0 = share_begin(total, i, ctas);
-          if (w0 >= u1 || w0 == share_begin(total, i + 1, ctas)) return nullptr;  // behind, or an empty share
-          // a CTA's first stretch is in its first slot, its last in the second
-          return part + (2 * static_cast<int64_t>(i) + (w0 < u0)) * kFewPartFloats;
-        },
-        r, kFewRows);
-}
-
 template <bool SW, int RG, int G>
-int launch_few(const CUtensorMap& mk, const CUtensorMap& mv, const CacheAttnParams& p, const FewPlan& plan, float* ws,
+int launch_few(const CUtensorMap& mk, const CUtensorMap& mv, const CacheAttnParams& p, const SharePlan& plan, float* ws,
                cudaStream_t stream) {
   static PerDeviceOnce once;
   const int rc =
@@ -703,7 +553,7 @@ int launch_few(const CUtensorMap& mk, const CUtensorMap& mv, const CacheAttnPara
 }
 
 template <bool SW>
-int launch_few_rows(const CUtensorMap& mk, const CUtensorMap& mv, const CacheAttnParams& p, const FewPlan& plan,
+int launch_few_rows(const CUtensorMap& mk, const CUtensorMap& mv, const CacheAttnParams& p, const SharePlan& plan,
                     float* ws, cudaStream_t stream) {
   if (plan.rows <= 1) return launch_few<SW, 1, 1>(mk, mv, p, plan, ws, stream);
   if (plan.rows <= 4) return launch_few<SW, 4, 1>(mk, mv, p, plan, ws, stream);
@@ -713,21 +563,7 @@ int launch_few_rows(const CUtensorMap& mk, const CUtensorMap& mv, const CacheAtt
 
 }  // namespace
 
-FewPlan few_plan(int batch, int heads_kv, int rows, int64_t pages, int sms) {
-  const int64_t units = static_cast<int64_t>(batch) * heads_kv;
-  FewPlan f;
-  // up to 4 pages the join costs more than the split saves
-  f.rows = rows;
-  f.whole = pages <= 4;
-  f.ctas = static_cast<int>(f.whole ? units : std::min<int64_t>(2ll * sms, units * ((pages + 1) / 2)));
-  return f;
-}
-
-size_t few_workspace_bytes(const FewPlan& plan) {
-  return plan.whole ? 0 : 2 * static_cast<size_t>(plan.ctas) * kFewPartFloats * sizeof(float);
-}
-
-int launch_cache_attn_few(const CacheAttnParams& p, const FewPlan& plan, void* ws, cudaStream_t stream) {
+int launch_cache_attn_few(const CacheAttnParams& p, const SharePlan& plan, void* ws, cudaStream_t stream) {
   CUtensorMap mk, mv;
   int rc = make_page_map(&mk, p.k8, p);
   if (rc == CALIBATT_OK) rc = make_page_map(&mv, p.v8, p);
@@ -735,20 +571,7 @@ int launch_cache_attn_few(const CacheAttnParams& p, const FewPlan& plan, void* w
   float* part = static_cast<float*>(ws);
   rc = p.wait_limit_ns < kShortWaitNs ? launch_few_rows<true>(mk, mv, p, plan, part, stream)
                                       : launch_few_rows<false>(mk, mv, p, plan, part, stream);
-  if (rc != CALIBATT_OK || plan.whole) return rc;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(p.heads_kv, p.batch);
-  cfg.blockDim = dim3(128);
-  cfg.stream = stream;
-  // resident while the pages are still read: it waits in the kernel
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, cache_few_join_kernel, p, plan.ctas, static_cast<const float*>(part)) == cudaSuccess
-             ? CALIBATT_OK
-             : CALIBATT_ERR_CUDA;
+  return rc != CALIBATT_OK || plan.whole ? rc : launch_cache_join(p, plan, part, kFewRows, stream);
 }
 
 }  // namespace calibatt
