@@ -416,7 +416,7 @@ __global__ void __launch_bounds__(kMidThreads, 1)
     // ---------------------------------------------------------- softmax
     warpgroup_regs_inc<kMidSoftmaxRegs>();
     const int s = warp >> 2;
-    const int row = (warp & 3) * 32 + lane;
+    const int tm_row = (warp & 3) * 32 + lane;  // of Q's tile = TMEM lane
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t sc = tmem + lane_off + s * 128, oc = tmem + lane_off + 256 + s * 128;
     uint32_t n_s = 0, n_o[2] = {0, 0};
@@ -439,10 +439,19 @@ __global__ void __launch_bounds__(kMidThreads, 1)
       const int np = seg.np;
       const bool second = np > 1;  // slot 1 has work
       const bool active = s == 0 || second;
-      const bool row_valid = row < seg.rows;
-      const int tok = row_valid ? row / p.group : 0;
+      // With up to 64 rows Q's tile holds them twice, and slot 1 takes the
+      // second copy: the slots' rows then lie in different warps of the SM's
+      // partitions. A warp without rows leaves its part of S and P as it is:
+      // only its own rows of O depend on it.
+      const int copy = seg.rows <= 32 ? 32 : seg.rows <= 64 ? 64 : 0;
+      const int row = s == 1 ? tm_row - copy : tm_row;  // the stream's
+      const bool row_valid = row >= 0 && row < seg.rows;
+      const bool idle = !__any_sync(0xffffffffu, row_valid);
+      const int q_row = copy > 0 && tm_row >= copy ? tm_row - copy : tm_row;
+      const bool q_valid = q_row < seg.rows;
+      const int tok = q_valid ? q_row / p.group : 0;
       const int64_t at =
-          static_cast<int64_t>(seg.head * p.group + (row_valid ? row % p.group : 0)) * p.n + seg.t0 + tok;
+          static_cast<int64_t>(seg.head * p.group + (q_valid ? q_row % p.group : 0)) * p.n + seg.t0 + tok;
       // a padded row sees all keys: it is computed and not stored
       const int limit = row_valid ? visible(seg.len - seg.n_new + tok, seg.len, p.unit) : seg.len;
       float m_run = -INFINITY, l_run = 0.f;
@@ -455,7 +464,7 @@ __global__ void __launch_bounds__(kMidThreads, 1)
         uint4 w[16];
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
-          w[j] = row_valid ? __ldg(src + j) : make_uint4(0, 0, 0, 0);
+          w[j] = q_valid ? __ldg(src + j) : make_uint4(0, 0, 0, 0);
           const uint32_t x[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
 #pragma unroll
           for (int e = 0; e < 4; ++e)
@@ -464,7 +473,7 @@ __global__ void __launch_bounds__(kMidThreads, 1)
         const float shrink = row_shrink(amax, 0);
         const float c_row = p.scale_log2 / shrink;
         if (s == 0) {
-          const uint32_t dst = sbase + L::kQOff + row * 128;
+          const uint32_t dst = sbase + L::kQOff + tm_row * 128;
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
             const uint32_t x[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
@@ -472,7 +481,7 @@ __global__ void __launch_bounds__(kMidThreads, 1)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
               h[e] = pack_half2(__uint_as_float(x[e] << 16) * shrink, __uint_as_float(x[e] & 0xffff0000u) * shrink);
-            st_shared16(dst + (j >> 3) * kHalf + (((j & 7) ^ (row & 7)) << 4), h[0], h[1], h[2], h[3]);
+            st_shared16(dst + (j >> 3) * kHalf + (((j & 7) ^ (tm_row & 7)) << 4), h[0], h[1], h[2], h[3]);
           }
           fence_proxy_async();
           mbar_arrive(&bar.q_full);
@@ -487,6 +496,11 @@ __global__ void __launch_bounds__(kMidThreads, 1)
           const float o_ratio = vref.page(__shfl_sync(0xffffffffu, win.vs, i & 31));
           if (!wait_warp(&bar.s_full[s], n_s & 1)) break;
           ++n_s;
+          if (idle) {
+            mbar_arrive(&bar.p_full[s][0]);
+            mbar_arrive(&bar.p_full[s][1]);
+            continue;
+          }
           tc_fence_after();
           const int key0 = (seg.pg0 + i) * kPage;
           const int cut = id < 0 ? 0 : min(limit - key0, kPage);  // keys of the page that the row sees
@@ -570,9 +584,9 @@ __global__ void __launch_bounds__(kMidThreads, 1)
       // [channel][row], 64 channels at a time
       float* joined = reinterpret_cast<float*>(smem + L::kQOff);
       if (second) {
-        if (s == 1) bar.slot_ml[row] = make_float2(m_run, l_run);
+        if (s == 1 && row_valid) bar.slot_ml[row] = make_float2(m_run, l_run);
         named_bar_sync(1, 256);
-        if (s == 0) {
+        if (s == 0 && row_valid) {
           const float2 o = bar.slot_ml[row];
           const float mx = fmaxf(m_run, o.x);
           const float use = mx == -INFINITY ? 0.f : mx;
@@ -601,23 +615,24 @@ __global__ void __launch_bounds__(kMidThreads, 1)
         uint32_t o[32];
         if (second && (cc & 1) == 0) {
           if (cc > 0) named_bar_sync(1, 256);  // slot 0 has read the first half
-          if (s == 1 && done) {
+          if (s == 1 && done && !idle) {
             const float unit = vref.unit();
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh) {
               tmem_ld32_wait(oc + (cc + hh) * 32, o);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) joined[(hh * 32 + e) * 128 + row] = __uint_as_float(o[e]) * unit;
+              for (int e = 0; e < 32; ++e)
+                if (row_valid) joined[(hh * 32 + e) * 128 + row] = __uint_as_float(o[e]) * unit;
             }
           }
           named_bar_sync(1, 256);
         }
-        if (!done || s == 1) continue;
+        if (!done || s == 1 || idle) continue;
         tmem_ld32_wait(oc + cc * 32, o);
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
           float x = __uint_as_float(o[e]) * f0;
-          if (second) x += joined[((cc & 1) * 32 + e) * 128 + row] * f1;
+          if (second) x += joined[((cc & 1) * 32 + e) * 128 + tm_row] * f1;
           o[e] = __float_as_uint(x);
         }
         if (patch && row_valid) {

@@ -330,6 +330,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const int r = r0 + s * 128 + row;
     const bool row_valid = r < r1;
+    // a warp without rows leaves its part of S and P as it is: only its own
+    // rows of O depend on it
+    const bool idle = !__any_sync(0xffffffffu, row_valid);
     const int tok = row_valid ? r / p.group : 0;
     const int64_t at = static_cast<int64_t>(head * p.group + (row_valid ? r % p.group : 0)) * p.n + st.t0 + tok;
     // a padded row sees all keys: it is computed and not stored
@@ -377,6 +380,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const float ck = score_factor(c_row, __shfl_sync(0xffffffffu, win.ks, i & 31));
         const float o_ratio = vref.page(__shfl_sync(0xffffffffu, win.vs, i & 31));
         if (!wait_warp(&bar.s_full[s], i & 1)) break;
+        if (idle) {
+          mbar_arrive(&bar.p_full[s][0]);
+          mbar_arrive(&bar.p_full[s][1]);
+          continue;
+        }
         tc_fence_after();
         const int key0 = (pg0 + i) * kPage;
         const int cut = id < 0 ? 0 : min(limit - key0, kPage);  // keys of the page that the row sees
