@@ -94,8 +94,9 @@ def cache_write(x, c, scale, tok_start, kv_len, table):
                 c[page, h, lo:hi] = round_e4m3(new / s)
 
 
-def cache_attention(q, c_k, c_v, s_k, s_v, tok_start, kv_len, table, scale, unit=0):
-    """(o, lse, sum p |v|) [heads_q][n].. of every packed token; NaN where a token belongs to no stream."""
+def cache_attention(q, c_k, c_v, s_k, s_v, tok_start, kv_len, table, scale, unit=0, shift=0):
+    """(o, lse, sum p |v|) [heads_q][n].. of every packed token; NaN where a token belongs to no stream. shift: tokens
+    before the cached ones that count for positions and are not attended to."""
     hq, n, d = q.shape
     group = hq // c_k.shape[1]
     o, av = np.full((hq, n, d), np.nan), np.full((hq, n, d), np.nan)
@@ -108,8 +109,8 @@ def cache_attention(q, c_k, c_v, s_k, s_v, tok_start, kv_len, table, scale, unit
             k = (_VALUES[c_k[pages, g]] * s_k[pages, g].astype(np.float64)[:, None, None]).reshape(-1, d)[:length]
             v = (_VALUES[c_v[pages, g]] * s_v[pages, g].astype(np.float64)[:, None, None]).reshape(-1, d)[:length]
             for i in range(t0, t1):
-                pos = length - (t1 - t0) + i - t0
-                end = length if unit == 0 else min(length, max(0, (pos // unit + 1) * unit))
+                pos = shift + length - (t1 - t0) + i - t0
+                end = length if unit == 0 else min(length, max(0, (pos // unit + 1) * unit - shift))
                 if end == 0:
                     o[h, i], av[h, i], lse[h, i] = 0.0, 0.0, -np.inf
                     continue

@@ -323,6 +323,15 @@ SHAPES = [
     (4, 4, [2, 0, 5], [2, 77, 900], 1), (40, 8, [1], [2500], 0), (3, 3, [17], [1000], 1), (2, 1, [40], [333], 7),
     (2, 2, [129], [140], 1), (1, 1, [300], [300], 64), (4, 2, [70, 33], [513, 64], 0), (6, 2, [100], [1300], 25),
     (1, 1, [260, 1], [770, 128], 0), (2, 2, [513], [600], 128), (8, 1, [31], [4000], 0), (2, 2, [128], [4096], 1),
+    # the borders of the kernels' row counts, 1 to 16 rows in every layout
+    (1, 1, [16], [1500], 1), (4, 2, [8, 3, 1], [1500, 40, 700], 3), (8, 2, [1, 2], [2000, 128], 0),
+    (3, 1, [2, 1, 0, 2], [900, 6, 50, 129], 1), (7, 1, [1], [1300], 0), (10, 2, [1, 1, 1], [130, 2600, 384], 1),
+    # 17 to 128, one copy or two of the rows
+    (1, 1, [17], [1400], 1), (5, 1, [7, 1], [640, 2300], 2), (2, 1, [32], [900], 0), (3, 1, [11, 21, 4], [700, 90, 5], 9),
+    (1, 1, [64, 65, 1, 0, 128], [64, 3000, 1, 7, 400], 1), (16, 2, [12], [1025], 4),
+    # more: tiles of 256, of which one or both halves are used, split or not
+    (1, 1, [129, 5], [129, 1000], 1), (3, 3, [256], [2000], 0), (1, 1, [257], [5000], 16), (4, 1, [65, 70], [900, 71], 1),
+    (2, 2, [700, 300, 40], [2500, 300, 700], 100), (8, 8, [384], [1100], 128),
 ]
 
 
@@ -420,6 +429,32 @@ def test_extreme_queries_and_scales(binding, so, rows, lens):
     big = so.cache_attention(bf16_to_f64(q[:, m:m + 1]), *args, [0, 1], [lens], c.table_h, 0.05)
     np.testing.assert_allclose(bf16_to_f64(o[:, m:m + 1]), big[0], rtol=2.0 ** -7)
     assert torch.isnan(o[0, m + 1]).all()
+
+
+@pytest.mark.parametrize("hq,hk,new,lens,unit", [(4, 2, [1, 1], [3000, 9000], 1), (4, 2, [20, 30], [3000, 9000], 1),
+                                                 (2, 1, [90, 200], [3000, 9000], 50)])
+def test_wild_pages_are_left_out(binding, so, hq, hk, new, lens, unit):
+    """A table entry outside the pool in the middle of a stream: reported, and its keys are not seen."""
+    g = _gen(77)
+    c = Cache(2, hk, -(-max(lens) // 128), seed=31)
+    q = _randn(g, hq, sum(new), 128) * 0.5
+    table = c.table.clone()
+    table[0, 5], table[1, 40] = -7, 1 << 30
+    o, lse = binding.cache_attn_fwd(q.cuda(), *c.dev, _i32(_starts(new)), _i32(lens), table, max_new=max(new),
+                                    max_kv=max(lens), causal_unit=unit, scale=0.05)
+    assert binding.get_status() == -2 and binding.get_status() == 0
+    # the oracle on streams without that page: the order of keys does not matter where all are seen
+    for b, (wild, m) in enumerate(zip((5, 40), new)):
+        tab = np.delete(c.table_h[b], wild)[None]
+        ln = lens[b] - 128
+        rows = slice(_starts(new)[b], _starts(new)[b] + m)
+        ref = so.cache_attention(bf16_to_f64(q[:, rows]), c.k_h, c.v_h, c.ks_h, c.vs_h, [0, m], [ln], tab, 0.05, unit)
+        if unit > 1:  # positions moved with the page: take the same visible ends
+            ref = so.cache_attention(bf16_to_f64(q[:, rows]), c.k_h, c.v_h, c.ks_h, c.vs_h, [0, m], [ln], tab, 0.05, unit,
+                                     shift=128)
+        part = Cache.__new__(Cache)
+        part.k_h, part.v_h, part.ks_h, part.vs_h, part.table_h = c.k_h, c.v_h, c.ks_h, c.vs_h, tab
+        _attn_close(o[:, rows], lse[:, rows], ref, q[:, rows], part, [ln], 0.05, _p_err(new, hq, hk))
 
 
 def test_a_long_stream_past_32_bit_offsets(binding):
@@ -528,6 +563,43 @@ def test_a_captured_step_replays_with_new_lengths(binding, so):
             assert torch.equal(a, b)
         assert torch.equal(c.k.view(torch.uint8), ref.k.view(torch.uint8)) and torch.equal(c.vs, ref.vs)
     assert binding.get_status() == 0
+
+
+def test_frame_streams_match_the_calls_and_the_oracle(binding, so):
+    """The package's own path: two ragged streams, frames begun in one step and ended in the next."""
+    from calibrated_block_sparse_b200.stream import FrameStreams
+    g = _gen(91)
+    H, W, hq, hk = 4, 9, 4, 2
+    st = FrameStreams(batch=2, heads=hq, kv_heads=hk, H=H, W=W, pages=12, max_tokens=600)
+    c = Cache(2, hk, 5, seed=3, spare=2)
+    for x in (c.k_h, c.v_h):
+        x[:] = 0
+    scale, done = 1 / math.sqrt(128), [0, 0]
+    for new in ([36, 20], [1, 300], [0, 16], [130, 1]):
+        n = sum(new)
+        x = _randn(g, n, hq + 2 * hk, 128).cuda()
+        o, lse = st.step(x[:, :hq], x[:, hq:hq + hk], x[:, hq + hk:], new=new, causal_unit=H * W)
+        t = np.concatenate([np.arange(a, a + m) for a, m in zip(done, new)])
+        pos = torch.from_numpy(np.stack([t // 36, t % 36 // W, t % W], 1).astype(np.int32)).cuda()
+        done = [a + m for a, m in zip(done, new)]
+        assert st.lengths == done
+        qr, kr = binding.rope_fwd(x[:, :hq], x[:, hq:hq + hk], st.plan, pos=pos)
+        start = _starts(new)
+        so.cache_write(bf16_to_f64(kr.transpose(0, 1)), c.k_h, c.ks_h, start, done, c.table_h)
+        so.cache_write(bf16_to_f64(x[:, hq + hk:]), c.v_h, c.vs_h, start, done, c.table_h)
+        ref = so.cache_attention(bf16_to_f64(qr), c.k_h, c.v_h, c.ks_h, c.vs_h, start, done, c.table_h, scale, H * W)
+        _attn_close(o, lse, ref, qr, c, done, scale, _p_err(new, hq, hk))
+    assert binding.get_status() == 0
+    # refusals change nothing
+    free = st.free_pages
+    big = torch.zeros((2000, hq + 2 * hk, 128), dtype=torch.bfloat16, device="cuda")
+    for new in ([2000, 0], [400, 600]):
+        y = big[:sum(new)]
+        with pytest.raises((ValueError, RuntimeError)):
+            st.step(y[:, :hq], y[:, hq:hq + hk], y[:, hq + hk:], new=new)
+    assert st.lengths == done and st.free_pages == free
+    st.drop(0)
+    assert st.lengths == [0, done[1]] and st.free_pages > free
 
 
 def test_two_streams_at_once_and_a_repeat_give_the_same(binding):

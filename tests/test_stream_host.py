@@ -135,3 +135,10 @@ def test_binding_wants_cuda_tensors(binding):
         binding.cache_write(x, x, None, None, None, None, None, None, None)
     with pytest.raises(TypeError):
         binding.cache_attn_fwd(x, None, None, None, None, None, None, None)
+
+
+def test_frame_streams_refuse_bad_shapes():
+    from calibrated_block_sparse_b200.stream import FrameStreams
+    for bad in (dict(batch=0), dict(heads=3), dict(kv_heads=0), dict(H=0), dict(pages=0)):
+        with pytest.raises(ValueError):
+            FrameStreams(**{**dict(batch=1, heads=4, kv_heads=2, H=2, W=3, pages=4), **bad})
