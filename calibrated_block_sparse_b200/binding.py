@@ -9,9 +9,11 @@ import of a compute function fails loudly.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import math
 import os
 import threading
+from operator import index as index_of
 
 import numpy as np
 import torch
@@ -802,7 +804,40 @@ def _new(like, shape, dtype, stream):
         return like.new_empty(shape, dtype=dtype)
 
 
-_Int3 = ctypes.c_int32 * 3
+class _CtypesCalls:
+    """The streaming calls through ctypes, with the arguments of the compiled module (_pycalls): the function first."""
+
+    @staticmethod
+    def rope(fn, plan, q, qt, qh, hq, k, kt, kh, hk, n, pos, H, W, s0, s1, s2, qo, qot, qoh, ko, kot, koh, stream):
+        return fn(plan, q, qt, qh, hq, k, kt, kh, hk, n, HEAD_DIM, pos, H, W, (ctypes.c_int32 * 3)(s0, s1, s2), qo, qot,
+                  qoh, ko, kot, koh, stream)
+
+    @staticmethod
+    def cache_write(fn, k, kt, kh, v, vt, vh, heads, n, *rest):
+        return fn(k, kt, kh, v, vt, vh, heads, n, HEAD_DIM, *rest)
+
+    @staticmethod
+    def cache_attn(fn, q, hq, hk, n, *rest):
+        return fn(q, hq, hk, n, HEAD_DIM, *rest)
+
+
+_calls = None
+_fns = ()
+
+
+def _load_calls():
+    """The compiled calls, or those of ctypes, and the four functions as they take them."""
+    global _calls, _fns
+    lib = load()
+    fns = [getattr(lib, f"calibatt_{x}") for x in ("rope_fwd", "rope_bwd", "cache_write", "cache_attn_fwd")]
+    if os.path.exists(_build.PYCALLS):
+        spec = importlib.util.spec_from_file_location("_pycalls", _build.PYCALLS)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        _fns, _calls = tuple(ctypes.cast(f, ctypes.c_void_p).value for f in fns), module
+    else:
+        _fns, _calls = tuple(fns), _CtypesCalls
+    return _calls
 
 
 def _rope(forward, q, k, plan, grid, start, pos, q_out, k_out, stream):
@@ -819,9 +854,11 @@ def _rope(forward, q, k, plan, grid, start, pos, q_out, k_out, stream):
     out_shape = (heads, n, HEAD_DIM) if forward else (n, heads, HEAD_DIM)
     if q_out is None:
         q_out = _new(q, out_shape, torch.bfloat16, stream)
-    shape, ost = _want_rows(q_out, "q_out", index)
-    if shape != out_shape:
-        raise ValueError(f"q_out must be {list(out_shape)}")
+        ost = (out_shape[1] * HEAD_DIM, HEAD_DIM)
+    else:
+        shape, ost = _want_rows(q_out, "q_out", index)
+        if shape != out_shape:
+            raise ValueError(f"q_out must be {list(out_shape)}")
     if k is not None:
         shape, kst = _want_rows(k, "k", index)
         if shape[tok] != n:
@@ -830,9 +867,11 @@ def _rope(forward, q, k, plan, grid, start, pos, q_out, k_out, stream):
         out_shape = (heads_k, n, HEAD_DIM) if forward else (n, heads_k, HEAD_DIM)
         if k_out is None:
             k_out = _new(k, out_shape, torch.bfloat16, stream)
-        shape, kost = _want_rows(k_out, "k_out", index)
-        if shape != out_shape:
-            raise ValueError(f"k_out must be {list(out_shape)}")
+            kost = (out_shape[1] * HEAD_DIM, HEAD_DIM)
+        else:
+            shape, kost = _want_rows(k_out, "k_out", index)
+            if shape != out_shape:
+                raise ValueError(f"k_out must be {list(out_shape)}")
         k_out_ptr = k_out.data_ptr()
     elif k_out is not None:
         raise ValueError("k_out without k")
@@ -842,19 +881,20 @@ def _rope(forward, q, k, plan, grid, start, pos, q_out, k_out, stream):
         if grid is None:
             raise ValueError("give the positions as a grid (H, W) or as a tensor pos [n][3]")
         H, W = grid
-        pos_ptr, at = None, _Int3(*start)
+        pos_ptr = None
     else:
         if grid is not None:
             raise ValueError("give the positions as a grid (H, W) or as a tensor pos [n][3], not as both")
         _want(pos, torch.int32, "pos", index)
         if pos.shape != (n, 3):
             raise ValueError(f"pos must be [{n}][3]")
-        H, W, pos_ptr, at = 0, 0, pos.data_ptr(), None
-    lib = _lib or load()
-    rc = (lib.calibatt_rope_fwd if forward else lib.calibatt_rope_bwd)(
-        ctypes.byref(plan), q.data_ptr(), st[tok], st[hd], heads, k_ptr, kst[tok], kst[hd], heads_k, n, HEAD_DIM,
-        pos_ptr, H, W, at, q_out.data_ptr(), ost[hd], ost[tok], k_out_ptr, kost[hd], kost[tok],
-        _current_raw_stream(index) if stream is None else stream.cuda_stream)
+        H, W, pos_ptr = 0, 0, pos.data_ptr()
+    s0, s1, s2 = start
+    calls = _calls or _load_calls()
+    rc = calls.rope(_fns[0 if forward else 1], ctypes.addressof(plan), q.data_ptr(), st[tok], st[hd], heads, k_ptr,
+                    kst[tok], kst[hd], heads_k, n, pos_ptr, H, W, s0, s1, s2, q_out.data_ptr(), ost[hd], ost[tok],
+                    k_out_ptr, kost[hd], kost[tok],
+                    _current_raw_stream(index) if stream is None else stream.cuda_stream)
     if rc:
         _check(rc, "calibatt_rope_fwd" if forward else "calibatt_rope_bwd")
     return q_out, k_out
@@ -918,11 +958,11 @@ def cache_write(k, v, k8, v8, k_scale, v_scale, tok_start, kv_len, table, max_ne
     pages, cache_heads, batch, width = _cache_args(k8, v8, k_scale, v_scale, tok_start, kv_len, table, index)
     if cache_heads != heads:
         raise ValueError(f"the cache has {cache_heads} heads, k has {heads}")
-    rc = (_lib or load()).calibatt_cache_write(
-        k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], heads, n, HEAD_DIM, tok_start.data_ptr(),
-        kv_len.data_ptr(), batch, n if max_new is None else max_new, table.data_ptr(), width, pages, k8.data_ptr(),
-        v8.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-        _current_raw_stream(index) if stream is None else stream.cuda_stream)
+    calls = _calls or _load_calls()
+    rc = calls.cache_write(_fns[2], k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], heads, n,
+                           tok_start.data_ptr(), kv_len.data_ptr(), batch, n if max_new is None else index_of(max_new),
+                           table.data_ptr(), width, pages, k8.data_ptr(), v8.data_ptr(), k_scale.data_ptr(),
+                           v_scale.data_ptr(), _current_raw_stream(index) if stream is None else stream.cuda_stream)
     if rc:
         _check(rc, "calibatt_cache_write")
 
@@ -970,24 +1010,22 @@ def cache_attn_fwd(q, k8, v8, k_scale, v_scale, tok_start, kv_len, table, max_ne
             raise ValueError(f"lse must be [{heads_q}][{n}]")
     elif want_lse:
         lse = _new(q, (heads_q, n), torch.float32, stream)
-    if max_new is None:
-        max_new = n
-    if max_kv is None:
-        max_kv = width * BLOCK
-    lib = _lib or load()
+    max_new = n if max_new is None else index_of(max_new)
+    max_kv = width * BLOCK if max_kv is None else index_of(max_kv)
+    calls = _calls or _load_calls()
     if ws is not None:
         _want(ws, torch.uint8, "ws", index)
         ws_bytes = ws.numel()
     else:
-        ws_bytes = lib.calibatt_cache_attn_workspace_size(batch, heads_q, heads_kv, n, max_new, max_kv)
+        ws_bytes = _lib.calibatt_cache_attn_workspace_size(batch, heads_q, heads_kv, n, max_new, max_kv)
         if ws_bytes:
             ws = _new(q, (ws_bytes,), torch.uint8, stream)
-    rc = lib.calibatt_cache_attn_fwd(
-        q.data_ptr(), heads_q, heads_kv, n, HEAD_DIM, _SCALE if scale is None else scale, causal_unit,
-        tok_start.data_ptr(), kv_len.data_ptr(), batch, max_new, max_kv, table.data_ptr(), width, pages, k8.data_ptr(),
-        v8.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), o.data_ptr(), None if lse is None else lse.data_ptr(),
-        None if ws is None else ws.data_ptr(), ws_bytes,
-        _current_raw_stream(index) if stream is None else stream.cuda_stream)
+    rc = calls.cache_attn(_fns[3], q.data_ptr(), heads_q, heads_kv, n, _SCALE if scale is None else float(scale),
+                          index_of(causal_unit), tok_start.data_ptr(), kv_len.data_ptr(), batch, max_new, max_kv,
+                          table.data_ptr(), width, pages, k8.data_ptr(), v8.data_ptr(), k_scale.data_ptr(),
+                          v_scale.data_ptr(), o.data_ptr(), None if lse is None else lse.data_ptr(),
+                          None if ws is None else ws.data_ptr(), ws_bytes,
+                          _current_raw_stream(index) if stream is None else stream.cuda_stream)
     if rc:
         _check(rc, "calibatt_cache_attn_fwd")
     return o, lse

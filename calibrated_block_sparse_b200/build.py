@@ -1,4 +1,5 @@
-"""Build libcalibatt.so (the C-ABI CUDA library) in-tree with nvcc for sm_100a.
+"""Build libcalibatt.so (the C-ABI CUDA library) in-tree with nvcc for sm_100a,
+and _pycalls.so (its streaming calls without ctypes) where Python's headers are.
 
     python -m calibrated_block_sparse_b200.build [--verbose-ptxas]
 """
@@ -9,6 +10,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 import tempfile
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -16,6 +18,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libcalibatt.so")
+PYCALLS = os.path.join(HERE, "_pycalls.so")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -34,8 +37,8 @@ def needs_build() -> bool:
     if not os.path.exists(LIB):
         return True
     t = os.path.getmtime(LIB)
-    deps = sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + \
-        glob.glob(os.path.join(INCLUDE, "*.h"))
+    deps = sources() + [os.path.join(CSRC, "pycalls.c")] + glob.glob(os.path.join(CSRC, "*.cuh")) + \
+        glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(INCLUDE, "*.h"))
     return any(os.path.getmtime(p) > t for p in deps)
 
 
@@ -68,7 +71,21 @@ def build(force: bool = False, ptxas_verbose: bool = False, jobs: int = 4, out_p
         subprocess.check_call([cc, *ARCH, "-shared", "-o", out, *objs, "-lcudart_static", "-ldl", "-lpthread",
                                "-lrt"])
         os.replace(out, target)
+    if out_path is None:
+        build_pycalls()
     return target
+
+
+def build_pycalls():
+    """Compile csrc/pycalls.c; returns its path, or None without a C compiler or Python's headers."""
+    gcc, include = shutil.which("gcc") or shutil.which("cc"), sysconfig.get_paths()["include"]
+    if gcc is None or not os.path.exists(os.path.join(include, "Python.h")):
+        return None
+    out = PYCALLS + f".tmp{os.getpid()}"
+    subprocess.check_call([gcc, "-O2", "-std=c11", "-Wall", "-Wextra", "-fPIC", "-shared", "-I", include, "-I", INCLUDE,
+                           os.path.join(CSRC, "pycalls.c"), "-o", out])
+    os.replace(out, PYCALLS)
+    return PYCALLS
 
 
 if __name__ == "__main__":

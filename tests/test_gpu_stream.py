@@ -327,10 +327,12 @@ SHAPES = [
     (1, 1, [16], [1500], 1), (4, 2, [8, 3, 1], [1500, 40, 700], 3), (8, 2, [1, 2], [2000, 128], 0),
     (3, 1, [2, 1, 0, 2], [900, 6, 50, 129], 1), (7, 1, [1], [1300], 0), (10, 2, [1, 1, 1], [130, 2600, 384], 1),
     # 17 to 128, one copy or two of the rows
-    (1, 1, [17], [1400], 1), (5, 1, [7, 1], [640, 2300], 2), (2, 1, [32], [900], 0), (3, 1, [11, 21, 4], [700, 90, 5], 9),
+    (1, 1, [17], [1400], 1), (5, 1, [7, 1], [640, 2300], 2), (2, 1, [32], [900], 0),
+    (3, 1, [11, 21, 4], [700, 90, 5], 9),
     (1, 1, [64, 65, 1, 0, 128], [64, 3000, 1, 7, 400], 1), (16, 2, [12], [1025], 4),
     # more: tiles of 256, of which one or both halves are used, split or not
-    (1, 1, [129, 5], [129, 1000], 1), (3, 3, [256], [2000], 0), (1, 1, [257], [5000], 16), (4, 1, [65, 70], [900, 71], 1),
+    (1, 1, [129, 5], [129, 1000], 1), (3, 3, [256], [2000], 0), (1, 1, [257], [5000], 16),
+    (4, 1, [65, 70], [900, 71], 1),
     (2, 2, [700, 300, 40], [2500, 300, 700], 100), (8, 8, [384], [1100], 128),
 ]
 
@@ -450,8 +452,8 @@ def test_wild_pages_are_left_out(binding, so, hq, hk, new, lens, unit):
         rows = slice(_starts(new)[b], _starts(new)[b] + m)
         ref = so.cache_attention(bf16_to_f64(q[:, rows]), c.k_h, c.v_h, c.ks_h, c.vs_h, [0, m], [ln], tab, 0.05, unit)
         if unit > 1:  # positions moved with the page: take the same visible ends
-            ref = so.cache_attention(bf16_to_f64(q[:, rows]), c.k_h, c.v_h, c.ks_h, c.vs_h, [0, m], [ln], tab, 0.05, unit,
-                                     shift=128)
+            ref = so.cache_attention(bf16_to_f64(q[:, rows]), c.k_h, c.v_h, c.ks_h, c.vs_h, [0, m], [ln], tab, 0.05,
+                                     unit, shift=128)
         part = Cache.__new__(Cache)
         part.k_h, part.v_h, part.ks_h, part.vs_h, part.table_h = c.k_h, c.v_h, c.ks_h, c.vs_h, tab
         _attn_close(o[:, rows], lse[:, rows], ref, q[:, rows], part, [ln], 0.05, _p_err(new, hq, hk))
@@ -600,6 +602,28 @@ def test_frame_streams_match_the_calls_and_the_oracle(binding, so):
     assert st.lengths == done and st.free_pages == free
     st.drop(0)
     assert st.lengths == [0, done[1]] and st.free_pages > free
+
+
+def test_the_compiled_calls_and_ctypes_give_the_same(binding, monkeypatch):
+    g = _gen(61)
+    x = _randn(g, 40, 6, 128).cuda()
+    plan = binding.rope_plan()
+    out = []
+    for calls in (None, binding._CtypesCalls):
+        if calls is not None:
+            monkeypatch.setattr(binding, "_calls", calls)
+            names = ("rope_fwd", "rope_bwd", "cache_write", "cache_attn_fwd")
+            monkeypatch.setattr(binding, "_fns", tuple(getattr(binding.load(), f"calibatt_{f}") for f in names))
+        c = Cache(1, 2, 2, seed=5)
+        q, k = binding.rope_fwd(x[:, :2], x[:, 2:4], plan, grid=(4, 5), start=(3, 1, 2))
+        back, _ = binding.rope_bwd(q, None, plan, grid=(4, 5), start=(3, 1, 2))
+        binding.cache_write(k.transpose(0, 1), x[:, 4:], *c.dev, _i32([0, 40]), _i32([100]), c.table)
+        o, lse = binding.cache_attn_fwd(q, *c.dev, _i32([0, 40]), _i32([100]), c.table, causal_unit=7, scale=0.1)
+        out.append([q, k, back, c.k.view(torch.uint8), c.ks, o, lse])
+        with pytest.raises(TypeError):
+            binding.cache_attn_fwd(q, *c.dev, _i32([0, 40]), _i32([100]), c.table, max_new=2.5)
+    assert all(torch.equal(a, b) for a, b in zip(*out))
+    assert binding.get_status() == 0
 
 
 def test_two_streams_at_once_and_a_repeat_give_the_same(binding):
