@@ -15,8 +15,10 @@
 // so nothing of the cache passes through registers (converting it to fp16
 // there, for mma.sync, took ~500 ALU instructions per warp and 8 KB and held
 // the kernel at 52 % of the DRAM rate). Q and P are written as sums of e5m2
-// values, in columns of their own that are added up in fp32: three parts of 3
-// significant bits hold a bf16 value's 8 exactly, four parts hold P to 2^-12.
+// values: three parts of 3 significant bits hold a bf16 value's 8 exactly, four
+// parts hold P to 2^-12. The products of Q's parts are accumulated into the
+// same columns of S^T; those of P's parts have columns of their own (one
+// product instead of four), which are added up at the end of a stretch.
 // e5m2 spans 2^-16 .. 2^15, so a row of Q, scaled by a power of two to a
 // largest value in [2^13, 2^14), is exact down to 2^-22 of it and within 2^-31
 // of it below, and weights keep a bit down to 2^-24 of the largest.
@@ -78,8 +80,8 @@ struct FewBarriers {
 
 struct FewLayout {
   static constexpr int kRingOff = 0;
-  static constexpr int kQOff = kFewRing * kPageBytes;                  // Q^T's operand: few_cols rows of 128 channels
-  static constexpr int kPOff = kQOff + few_cols(kFewRows, kQParts) * 128;  // P^T's: few_cols rows of 128 keys, two buffers
+  static constexpr int kQOff = kFewRing * kPageBytes;                  // Q^T's operand: rows of 128 channels, part by part
+  static constexpr int kPOff = kQOff + kQParts * few_cols(kFewRows, 1) * 128;  // P^T's: rows of 128 keys, two buffers
   static constexpr int kPBytes = few_cols(kFewRows, kPParts) * 128;
   static constexpr int kBarOff = kPOff + 2 * kPBytes;
   static constexpr int kDynSmem = kBarOff + static_cast<int>(sizeof(FewBarriers)) + 1024;
@@ -87,8 +89,8 @@ struct FewLayout {
 // two CTAs on an SM (228 KB, of which each takes 1 KB more)
 static_assert(2 * (FewLayout::kDynSmem + 1024) <= 233472, "shared memory budget");
 
-// Tensor memory: S^T in two buffers of up to 48 columns, O^T in up to 64.
-constexpr uint32_t kFewCols = 256, kSBuf = 64, kOCol = 128;
+// Tensor memory: S^T in two buffers of 16 columns, O^T in up to 64.
+constexpr uint32_t kFewCols = 128, kSBuf = 32, kOCol = 64;
 
 // kind::f8f6f4, A e4m3, B e5m2, fp32 accumulation, M = 128; V is A with its
 // channels (M) contiguous.
@@ -162,7 +164,7 @@ __global__ void __launch_bounds__(few_threads(G), 2)
                      const __grid_constant__ CacheAttnParams p, bool whole, float* part) {
   using L = FewLayout;
   constexpr int RB = RG * G, kAll = 128 * G;
-  constexpr int kQCols = few_cols(RG * G, kQParts), kPCols = few_cols(RG * G, kPParts);
+  constexpr int kQCols = few_cols(RG * G, 1), kPCols = few_cols(RG * G, kPParts);
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
@@ -276,8 +278,11 @@ __global__ void __launch_bounds__(few_threads(G), 2)
         if (!wait(&bar.full[stage], phase)) return false;
         tc_fence_after();
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          mma_f8(tmem + (t & 1) * kSBuf, ring0 + stage * (kPageBytes >> 4) + k * 2, q0 + k * 2, kIdescS, k > 0);
+        for (int i = 0; i < kQParts; ++i)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_f8(tmem + (t & 1) * kSBuf, ring0 + stage * (kPageBytes >> 4) + k * 2,
+                   q0 + i * (kQCols * 128 >> 4) + k * 2, kIdescS, (i > 0 || k > 0) ? 1u : 0u);
         mma_commit(&bar.s_full[t & 1]);
         ring_next();
         return true;
@@ -333,7 +338,7 @@ __global__ void __launch_bounds__(few_threads(G), 2)
         bar.c[all] = 0.f;
         bar.limit[all] = 0;
       }
-      // the rows of Q as operand B: row part * RG + r of a group, channels contiguous
+      // the rows of Q as operand B of each part, channels contiguous
       for (int r = warp - 2; r < rows; r += 4 * G) {
         const int tok = r / p.group, h = s.head * p.group + r % p.group;
         const uint2 w = *reinterpret_cast<const uint2*>(
@@ -358,7 +363,7 @@ __global__ void __launch_bounds__(few_threads(G), 2)
             y[e] = part_i + 1 < kQParts ? three_bits(x[e]) : x[e];
             x[e] -= y[e];
           }
-          const int row = (r / RG * kQParts + part_i) * RG + r % RG;
+          const int row = part_i * kQCols + r;
           *reinterpret_cast<uint32_t*>(smem + L::kQOff + row * 128 + ((lane * 4) ^ ((row & 7) << 4))) =
               to_e5m2x2(y[0], y[1]) | to_e5m2x2(y[2], y[3]) << 16;
         }
@@ -385,7 +390,7 @@ __global__ void __launch_bounds__(few_threads(G), 2)
         wait_warp(&bar.s_full[turn & 1], (turn >> 1) & 1);
         tc_fence_after();
         float t[RG];
-        if (ok) tmem_rows<RG, kQParts>(tmem + lane_off + (turn & 1) * kSBuf + g * kQParts * RG, t);
+        if (ok) tmem_rows<RG, 1>(tmem + lane_off + (turn & 1) * kSBuf + r0, t);
         bool need = o_ratio != 1.f;
 #pragma unroll
         for (int r = 0; r < RG; ++r) t[r] *= bar.c[r0 + r] * ks;
