@@ -74,6 +74,7 @@ struct FewBarriers {
   int nan_seen;
   int limit[kFewRows];            // keys that a row sees
   float c[kFewRows];              // a raw score's factor, without the key scale
+  Walk walk[10];                  // per warp: it would hold 14 registers from one stretch to the next
   float top[4][kFewRows];         // per warp of a group, of a page
   float sum[4][kFewRows];         // per warp of a group, at a stretch's end
 };
@@ -204,15 +205,28 @@ __global__ void __launch_bounds__(few_threads(G), 2)
       if (!stream_fits(p, st)) record_error(p.status, CALIBATT_ERR_CSR);
     }
 
-  Walk walk;
-  walk.start(p, whole, lane);
+  {
+    Walk walk;
+    walk.start(p, whole, lane);
+    if (lane == 0) bar.walk[warp] = walk;
+    __syncwarp();
+  }
+  // for all lanes of a warp, or its lane 0 alone
+  auto next_stretch = [&](Stretch& s, unsigned lanes) -> bool {
+    Walk walk = bar.walk[warp];
+    const bool more = walk.next(p, s);
+    __syncwarp(lanes);
+    if (lane == 0) bar.walk[warp] = walk;
+    __syncwarp(lanes);
+    return more;
+  };
   Stretch s;
   if (warp == 0) {
     // ---------------------------------------------------------- TMA producer
     uint32_t stage = 0, phase = 0;
     int used = 0;
     bool ok = true;
-    while (ok && walk.next(p, s)) {
+    while (ok && next_stretch(s, 0xffffffffu)) {
       PageWindow<false> win(p, s.b, s.head, s.pg, s.count, s.st.len);
       win.fetch(lane, p.status);
       int id_now = -1, id_before = -1, k_at = 0;
@@ -287,7 +301,7 @@ __global__ void __launch_bounds__(few_threads(G), 2)
         ring_next();
         return true;
       };
-      while (ok && walk.next(p, s)) {
+      while (ok && next_stretch(s, 1u)) {
         if (!(ok = wait(&bar.q_full, stretch & 1))) break;
         ++stretch;
         if (!(ok = issue_s(turn))) break;
@@ -329,7 +343,7 @@ __global__ void __launch_bounds__(few_threads(G), 2)
       return ok;
     };
     uint32_t stage_v = 0;  // ring stages passed: V of this page, for the pages that are cleaned
-    while (walk.next(p, s)) {
+    while (next_stretch(s, 0xffffffffu)) {
       const int rows = s.st.n_new * p.group;
       PageWindow<true> win(p, s.b, s.head, s.pg, s.count, s.st.len);
       win.fetch(lane, p.status);
