@@ -258,7 +258,11 @@ int calibatt_cache_attn_fwd(const calibatt_bf16* q, int heads_q, int heads_kv, i
   p.unit = causal_unit;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.wait_limit_ns = wait_limit_ns();
-  p.max_rows = plan.rows <= kFewRows ? kFewRows : plan.rows <= kMidRows ? kMidRows : INT_MAX;
+  p.max_rows = plan.rows <= kFewRows   ? kFewRows
+               : plan.rows <= 32       ? 32
+               : plan.rows <= 64       ? 64
+               : plan.rows <= kMidRows ? kMidRows
+                                       : INT_MAX;
   if (plan.rows <= kFewRows) return launch_cache_attn_few(p, plan.share, ws, stream);
   if (plan.rows <= kMidRows) return launch_cache_attn_mid(p, plan.share, ws, stream);
   return launch_cache_attn_tiles(p, plan.tile, ws, stream);

@@ -7,8 +7,9 @@
 // leaves maximum, sum and unnormalised output in the workspace, and
 // cache_join_kernel joins them.
 //
-// CTA (512 threads, persistent), one tile of 128 query rows:
-//   warps 0-3, 4-7   softmax of slot 0 and slot 1 (thread = query row = TMEM lane)
+// CTA (512 threads, persistent), one tile of 128 / KS query rows, KS times over:
+//   warps 0-3, 4-7   softmax of slot 0 and slot 1 (thread = TMEM lane = query
+//                    row and its KS-th of a page's keys)
 //   warps 8-11       converters: e4m3 tiles to fp16 operand tiles in a
 //                    4-stage ring (128-byte swizzle on both sides)
 //   warp  12         MMA issuer (one thread): S = Q K^T and O += P V
@@ -17,8 +18,18 @@
 //   warp  15         idle
 // The two slots hold the same rows and take every other page, and are joined
 // at a stretch's end: the chain S -> softmax -> P V of one slot runs beside the
-// other's. Numbers are held as in cache_tile.cu: fp16 operands without scales,
+// other's. The tensor core multiplies 128 rows whatever is in them, so up to 64
+// (32) rows stand in the tile 2 (4) times, and each copy takes the softmax of a
+// half (quarter) of the keys, with zeros for the others in P: all warps work on
+// a chain that is 2 (4) times as short. Numbers are held as in cache_tile.cu: fp16 operands without scales,
 // O in units of a reference value scale.
+// Bound by shared memory: a page's 32 KB land there, are read and written as
+// 64 KB by the converters, and 96 KB are read as operands (Q's tile anew for
+// each page): 224 KB at 128 bytes a cycle are 1790 cycles, of the ~1850 that a
+// page takes with 25 rows. Measured: 16 streams of 20000 tokens, 40 query heads
+// on 8, 5 new tokens each in 132 us, half of the DRAM rate (150 us without the
+// copies; 148 us with K as an 8-bit operand and Q in three parts, which are 12
+// products instead of 8; 132 us with a second warpgroup of converters).
 // The register split leaves the issuer without spills; a spill there is read
 // back through an L1 that the tiles have flushed (measured at 40 registers:
 // ~350 cycles per MMA).
@@ -89,7 +100,6 @@ struct MidBarriers {
   int go[2];                // whether the softmax warps got stretch k (k even, odd)
   int raw_bad[kRaw];        // the tile's page is outside the pool: nothing was loaded
   int nan_seen[kNanSlots];  // 1 + number of the stretch in which a NaN value was taken out of a page
-  float2 slot_ml[128];      // slot 1's maximum and sum
   Segment seg[kSegs];
 };
 
@@ -118,11 +128,22 @@ __device__ __forceinline__ void store_half(uint32_t row_addr, int r, int j, cons
   st_shared16(row_addr + (((j + 1) ^ (r & 7)) << 4), h[4], h[5], h[6], h[7]);
 }
 
-template <bool SW>
+__device__ __forceinline__ void tmem_ld_scores(uint32_t at, float (&s)[32]) {
+  tmem_ld32_wait(at, reinterpret_cast<uint32_t(&)[32]>(s));
+}
+__device__ __forceinline__ void tmem_ld_scores(uint32_t at, float (&s)[64]) { tmem_ld64_wait(at, s); }
+__device__ __forceinline__ void tmem_ld_scores(uint32_t at, float (&s)[128]) {
+  tmem_ld64_wait(at, reinterpret_cast<float(&)[64]>(s[0]));
+  tmem_ld64_wait(at + 64, reinterpret_cast<float(&)[64]>(s[64]));
+}
+
+template <bool SW, int KS>
 __global__ void __launch_bounds__(kMidThreads, 1)
     cache_mid_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                      const __grid_constant__ CacheAttnParams p, bool whole, float* part) {
   using L = MidLayout;
+  constexpr int kRows = 128 / KS;   // rows of Q's tile, which holds them KS times
+  constexpr int kKeys = kPage / KS;  // of a page, for the rows of one copy
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
@@ -417,6 +438,7 @@ __global__ void __launch_bounds__(kMidThreads, 1)
     warpgroup_regs_inc<kMidSoftmaxRegs>();
     const int s = warp >> 2;
     const int tm_row = (warp & 3) * 32 + lane;  // of Q's tile = TMEM lane
+    const int row = tm_row % kRows, copy = tm_row / kRows;
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t sc = tmem + lane_off + s * 128, oc = tmem + lane_off + 256 + s * 128;
     uint32_t n_s = 0, n_o[2] = {0, 0};
@@ -439,19 +461,13 @@ __global__ void __launch_bounds__(kMidThreads, 1)
       const int np = seg.np;
       const bool second = np > 1;  // slot 1 has work
       const bool active = s == 0 || second;
-      // With up to 64 rows Q's tile holds them twice, and slot 1 takes the
-      // second copy: the slots' rows then lie in different warps of the SM's
-      // partitions. A warp without rows leaves its part of S and P as it is:
-      // only its own rows of O depend on it.
-      const int copy = seg.rows <= 32 ? 32 : seg.rows <= 64 ? 64 : 0;
-      const int row = s == 1 ? tm_row - copy : tm_row;  // the stream's
-      const bool row_valid = row >= 0 && row < seg.rows;
+      // A warp without rows leaves its part of S and P as it is: only its own
+      // rows of O depend on it.
+      const bool row_valid = row < seg.rows;
       const bool idle = !__any_sync(0xffffffffu, row_valid);
-      const int q_row = copy > 0 && tm_row >= copy ? tm_row - copy : tm_row;
-      const bool q_valid = q_row < seg.rows;
-      const int tok = q_valid ? q_row / p.group : 0;
+      const int tok = row_valid ? row / p.group : 0;
       const int64_t at =
-          static_cast<int64_t>(seg.head * p.group + (q_valid ? q_row % p.group : 0)) * p.n + seg.t0 + tok;
+          static_cast<int64_t>(seg.head * p.group + (row_valid ? row % p.group : 0)) * p.n + seg.t0 + tok;
       // a padded row sees all keys: it is computed and not stored
       const int limit = row_valid ? visible(seg.len - seg.n_new + tok, seg.len, p.unit) : seg.len;
       float m_run = -INFINITY, l_run = 0.f;
@@ -464,7 +480,7 @@ __global__ void __launch_bounds__(kMidThreads, 1)
         uint4 w[16];
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
-          w[j] = q_valid ? __ldg(src + j) : make_uint4(0, 0, 0, 0);
+          w[j] = row_valid ? __ldg(src + j) : make_uint4(0, 0, 0, 0);
           const uint32_t x[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
 #pragma unroll
           for (int e = 0; e < 4; ++e)
@@ -503,16 +519,16 @@ __global__ void __launch_bounds__(kMidThreads, 1)
           }
           tc_fence_after();
           const int key0 = (seg.pg0 + i) * kPage;
-          const int cut = id < 0 ? 0 : min(limit - key0, kPage);  // keys of the page that the row sees
-          float sv[2][64];
-          tmem_ld64_wait(sc, sv[0]);
-          tmem_ld64_wait(sc + 64, sv[1]);
-          if (__any_sync(0xffffffffu, cut < kPage)) {
+          // keys that the row sees, of the page's that are its copy's
+          const int cut = id < 0 ? 0 : min(limit - key0 - copy * kKeys, kKeys);
+          float sv[kKeys];
+          tmem_ld_scores(sc + copy * kKeys, sv);
+          if (__any_sync(0xffffffffu, cut < kKeys)) {
 #pragma unroll
-            for (int e = 0; e < 128; ++e)
-              if (e >= cut) sv[e >> 6][e & 63] = -INFINITY;
+            for (int e = 0; e < kKeys; ++e)
+              if (e >= cut) sv[e] = -INFINITY;
           }
-          const float mx = fmaxf(row_max64(sv[0]), row_max64(sv[1]));
+          const float mx = row_max_of(sv);
           const float page_max = mx * ck;
           const float m_new = fmaxf(m_run, page_max);
           // keep a stale running max unless it grew by more than the threshold
@@ -527,7 +543,7 @@ __global__ void __launch_bounds__(kMidThreads, 1)
           if (__any_sync(0xffffffffu, fabsf(m_use) > kBigScore)) {
             const float mx0 = mx == -INFINITY ? 0.f : mx;
 #pragma unroll
-            for (int e = 0; e < 128; ++e) sv[e >> 6][e & 63] = (sv[e >> 6][e & 63] - mx0) * ck;
+            for (int e = 0; e < kKeys; ++e) sv[e] = (sv[e] - mx0) * ck;
             mul = 1.f;
             add = page_max - m_use + vref.log;
           }
@@ -548,20 +564,36 @@ __global__ void __launch_bounds__(kMidThreads, 1)
           started = true;
           const float2 c2 = make_float2(mul, mul), n2 = make_float2(add, add);
           float2 a4[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          // P (fp16, two keys per column) over the first 64 columns of S: in
+          // two halves, or with zeros for the other copies' keys
+          if constexpr (KS > 1) {
+            const uint32_t zero[16] = {};
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t pk[32];
+            for (int c = 0; c < 4; ++c)
+              if (c / (4 / KS) != copy) tmem_st16(sc + c * 16, zero);
+          }
+          constexpr int kPart = kKeys < 64 ? kKeys : 64;
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const float2 x = exp2_mufu2(ffma2(make_float2(sv[h][2 * e], sv[h][2 * e + 1]), c2, n2));
+          for (int h = 0; h < kKeys / kPart; ++h) {
+            uint32_t pk[kPart / 2];
+#pragma unroll
+            for (int e = 0; e < kPart / 2; ++e) {
+              const float2 x = exp2_mufu2(ffma2(make_float2(sv[h * kPart + 2 * e], sv[h * kPart + 2 * e + 1]), c2, n2));
               a4[e & 3] = fadd2(a4[e & 3], x);
               pk[e] = pack_half2(x.x, x.y);
             }
-            // P (fp16, two keys per column) over the first 64 columns of S
-            tmem_st32(sc + h * 32, pk);
+            if constexpr (KS == 4)
+              tmem_st16(sc + copy * 16, pk);
+            else
+              tmem_st32(sc + (copy + h) * 32, pk);
             tmem_wait_st();
             tc_fence_before();
-            mbar_arrive(&bar.p_full[s][h]);
+            if constexpr (KS == 1) {
+              mbar_arrive(&bar.p_full[s][h]);
+            } else {
+              mbar_arrive(&bar.p_full[s][0]);
+              mbar_arrive(&bar.p_full[s][1]);
+            }
           }
           const float2 s01 = fadd2(a4[0], a4[1]), s23 = fadd2(a4[2], a4[3]);
           l_run = l_run * alpha + ((s01.x + s01.y) + (s23.x + s23.y)) * vref.inv;
@@ -579,63 +611,57 @@ __global__ void __launch_bounds__(kMidThreads, 1)
       }
       tc_fence_after();
       const bool done = ok && *abort_flag == 0;
-      float f0 = vref.unit(), f1 = 0.f;
-      // slot 1 hands its rows to slot 0 through Q's tile,
-      // [channel][row], 64 channels at a time
+      // A row's shares of the stretch, two slots by KS copies, are added up
+      // through Q's tile, 32 channels at a time and 16 / KS of them by each of
+      // the threads that hold a share: [share][channel][row].
       float* joined = reinterpret_cast<float*>(smem + L::kQOff);
-      if (second) {
-        if (s == 1 && row_valid) bar.slot_ml[row] = make_float2(m_run, l_run);
-        named_bar_sync(1, 256);
-        if (s == 0 && row_valid) {
-          const float2 o = bar.slot_ml[row];
-          const float mx = fmaxf(m_run, o.x);
-          const float use = mx == -INFINITY ? 0.f : mx;
-          const float g0 = ex2_approx(m_run - use);
-          f1 = ex2_approx(o.x - use);
-          l_run = l_run * g0 + o.y * f1;
-          f0 *= g0;
-          m_run = mx;
-        }
+      const int share = s * KS + copy, n_shares = second ? 2 * KS : KS;
+      float2* ml = reinterpret_cast<float2*>(joined);  // maxima and sums first
+      ml[share * kRows + row] = make_float2(m_run, l_run);
+      named_bar_sync(1, 256);
+      float mx = -INFINITY, l = 0.f;
+      for (int i = 0; i < n_shares; ++i) mx = fmaxf(mx, ml[i * kRows + row].x);
+      const float use = mx == -INFINITY ? 0.f : mx;
+      for (int i = 0; i < n_shares; ++i) {
+        const float2 x = ml[i * kRows + row];
+        l += x.y * ex2_approx(x.x - use);
       }
-      const bool some = l_run != 0.f;
-      const float inv = some ? 1.f / l_run : 0.f;
+      const float factor = ex2_approx(m_run - use) * vref.unit();
+      const bool some = l != 0.f;
+      const float inv = some ? 1.f / l : 0.f;
       const bool complete = np == seg.pages;
       float* out = part_of(part, blockIdx.x, seg.pg0 > 0, kMidRows);
-      const bool write = done && row_valid && s == 0;
-      if (write) {
+      if (done && row_valid && share == 0) {
         if (!complete)
-          *reinterpret_cast<float2*>(out + kMidRows * 128 + 2 * row) = make_float2(m_run, some ? l_run : 0.f);
+          *reinterpret_cast<float2*>(out + kMidRows * 128 + 2 * row) = make_float2(mx, some ? l : 0.f);
         else if (p.lse)
-          p.lse[at] = some ? (m_run + log2f(l_run)) * kLn2 : -INFINITY;
+          p.lse[at] = some ? (mx + log2f(l)) * kLn2 : -INFINITY;
       }
       const bool patch =
           *const_cast<volatile int*>(&bar.nan_seen[seg.number % kNanSlots]) == seg.number + 1;
+      constexpr int kCh = 16 / KS;
 #pragma unroll 1
       for (int cc = 0; cc < 4; ++cc) {
-        uint32_t o[32];
-        if (second && (cc & 1) == 0) {
-          if (cc > 0) named_bar_sync(1, 256);  // slot 0 has read the first half
-          if (s == 1 && done && !idle) {
-            const float unit = vref.unit();
+        named_bar_sync(1, 256);  // what was there has been read
+        if (done && active && !idle) {
+          uint32_t o[32];
+          tmem_ld32_wait(oc + cc * 32, o);
 #pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-              tmem_ld32_wait(oc + (cc + hh) * 32, o);
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (row_valid) joined[(hh * 32 + e) * 128 + row] = __uint_as_float(o[e]) * unit;
-            }
-          }
-          named_bar_sync(1, 256);
+          for (int e = 0; e < 32; ++e) joined[(share * 32 + e) * kRows + row] = __uint_as_float(o[e]) * factor;
         }
-        if (!done || s == 1 || idle) continue;
-        tmem_ld32_wait(oc + cc * 32, o);
+        named_bar_sync(1, 256);
+        if (!done || !row_valid) continue;
+        const int ch = cc * 32 + share * kCh;  // the thread's channels
+        float x[kCh];
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          float x = __uint_as_float(o[e]) * f0;
-          if (second) x += joined[((cc & 1) * 32 + e) * 128 + tm_row] * f1;
-          o[e] = __float_as_uint(x);
+        for (int e = 0; e < kCh; ++e) x[e] = 0.f;
+#pragma unroll
+        for (int i = 0; i < 2 * KS; ++i) {
+          if (i >= n_shares) break;
+#pragma unroll
+          for (int e = 0; e < kCh; ++e) x[e] += joined[(i * 32 + share * kCh + e) * kRows + row];
         }
-        if (patch && row_valid) {
+        if (patch) {
           // NaN values that were taken out of pages that not every row sees whole
           const int32_t* table = p.table + static_cast<int64_t>(seg.b) * p.table_stride;
           uint32_t bad = 0;
@@ -643,31 +669,32 @@ __global__ void __launch_bounds__(kMidThreads, 1)
             const int id = __ldg(table + key / kPage);
             if (id < 0 || id >= p.n_pages) continue;
             const uint8_t* v = p.v8 + ((static_cast<int64_t>(id) * p.heads_kv + seg.head) * kPage + key % kPage) * 128;
-            for (int e = 0; e < 32; ++e)
-              if ((v[cc * 32 + e] & 0x7f) == 0x7f) bad |= 1u << e;
+            for (int e = 0; e < kCh; ++e)
+              if ((v[ch + e] & 0x7f) == 0x7f) bad |= 1u << e;
           }
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (bad >> e & 1) o[e] = 0x7fffffffu;
+          for (int e = 0; e < kCh; ++e)
+            if (bad >> e & 1) x[e] = __int_as_float(0x7fffffff);
         }
-        if (!row_valid) continue;
         if (!complete) {
-          uint4* dst = reinterpret_cast<uint4*>(out + row * 128 + cc * 32);
+          float4* dst = reinterpret_cast<float4*>(out + row * 128 + ch);
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            dst[e] = some ? make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]) : make_uint4(0, 0, 0, 0);
+          for (int e = 0; e < kCh / 4; ++e)
+            dst[e] = some ? make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3])
+                          : make_float4(0.f, 0.f, 0.f, 0.f);
         } else {
-          uint32_t pk[16];
+          uint2* dst = reinterpret_cast<uint2*>(p.o + at * 128 + ch);
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            pk[e] = some ? pack_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv) : 0u;
-          store_row_chunk(p.o + at * 128 + cc * 32, pk);
+          for (int e = 0; e < kCh / 4; ++e)
+            dst[e] = some ? make_uint2(pack_bf16x2(x[4 * e] * inv, x[4 * e + 1] * inv),
+                                       pack_bf16x2(x[4 * e + 2] * inv, x[4 * e + 3] * inv))
+                          : make_uint2(0, 0);
         }
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.seg_empty[k % kSegs]);
-      if (second) named_bar_sync(1, 256);  // Q's tile may be written again
+      named_bar_sync(1, 256);  // Q's tile may be written again
     }
   }
 
@@ -681,21 +708,21 @@ __global__ void __launch_bounds__(kMidThreads, 1)
   }
 }
 
-template <bool SW>
+template <bool SW, int KS>
 int launch(const CUtensorMap& mk, const CUtensorMap& mv, const CacheAttnParams& p, const SharePlan& plan, float* part,
            cudaStream_t stream) {
   static PerDeviceOnce once;
-  const int rc = set_max_smem_once(reinterpret_cast<const void*>(cache_mid_kernel<SW>), kMidSmem, once);
+  const int rc = set_max_smem_once(reinterpret_cast<const void*>(cache_mid_kernel<SW, KS>), kMidSmem, once);
   if (rc != CALIBATT_OK) return rc;
   // the register split needs the allotment it was sized for
   static std::once_flag regs_once;
   static int launch_regs = 0;
   std::call_once(regs_once, [] {
     cudaFuncAttributes fa;
-    if (cudaFuncGetAttributes(&fa, cache_mid_kernel<SW>) == cudaSuccess) launch_regs = fa.numRegs;
+    if (cudaFuncGetAttributes(&fa, cache_mid_kernel<SW, KS>) == cudaSuccess) launch_regs = fa.numRegs;
   });
   if (launch_regs * kMidThreads < kMidRegs) return CALIBATT_ERR_CUDA;
-  cache_mid_kernel<SW><<<plan.ctas, kMidThreads, kMidSmem, stream>>>(mk, mv, p, plan.whole, part);
+  cache_mid_kernel<SW, KS><<<plan.ctas, kMidThreads, kMidSmem, stream>>>(mk, mv, p, plan.whole, part);
   return cudaGetLastError() == cudaSuccess ? CALIBATT_OK : CALIBATT_ERR_CUDA;
 }
 
@@ -707,8 +734,13 @@ int launch_cache_attn_mid(const CacheAttnParams& p, const SharePlan& plan, void*
   if (rc == CALIBATT_OK) rc = make_page_map(&mv, p.v8, p);
   if (rc != CALIBATT_OK) return rc;
   float* part = static_cast<float*>(ws);
-  rc = p.wait_limit_ns < kShortWaitNs ? launch<true>(mk, mv, p, plan, part, stream)
-                                      : launch<false>(mk, mv, p, plan, part, stream);
+  const bool sw = p.wait_limit_ns < kShortWaitNs;
+  if (p.max_rows <= 32)
+    rc = sw ? launch<true, 4>(mk, mv, p, plan, part, stream) : launch<false, 4>(mk, mv, p, plan, part, stream);
+  else if (p.max_rows <= 64)
+    rc = sw ? launch<true, 2>(mk, mv, p, plan, part, stream) : launch<false, 2>(mk, mv, p, plan, part, stream);
+  else
+    rc = sw ? launch<true, 1>(mk, mv, p, plan, part, stream) : launch<false, 1>(mk, mv, p, plan, part, stream);
   return rc != CALIBATT_OK || plan.whole ? rc : launch_cache_join(p, plan, part, kMidRows, stream);
 }
 

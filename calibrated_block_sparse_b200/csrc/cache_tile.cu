@@ -397,7 +397,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           for (int e = 0; e < 128; ++e)
             if (e >= cut) sv[e >> 6][e & 63] = -INFINITY;
         }
-        const float mx = fmaxf(row_max64(sv[0]), row_max64(sv[1]));
+        const float mx = fmaxf(row_max_of(sv[0]), row_max_of(sv[1]));
         const float page_max = mx * ck;
         const float m_new = fmaxf(m_run, page_max);
         // keep a stale running max unless it grew by more than the threshold

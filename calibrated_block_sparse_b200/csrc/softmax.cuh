@@ -48,18 +48,19 @@ __device__ __forceinline__ float row_max128(const float (&s)[128]) {
   return fmaxf(max3f(a[0], a[1], a[2]), fmaxf(max3f(a[3], a[4], a[5]), max3f(a[6], a[7], a[7])));
 }
 
-// max over 64 values, likewise.
-__device__ __forceinline__ float row_max64(const float (&s)[64]) {
+// max over N values (a multiple of 16), likewise.
+template <int N>
+__device__ __forceinline__ float row_max_of(const float (&s)[N]) {
   float a[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) a[i] = s[i];
 #pragma unroll
-  for (int k = 8; k + 16 <= 64; k += 16) {
+  for (int k = 8; k + 16 <= N; k += 16) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) a[i] = max3f(a[i], s[k + i], s[k + 8 + i]);
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) a[i] = fmaxf(a[i], s[56 + i]);
+  for (int i = 0; i < 8; ++i) a[i] = fmaxf(a[i], s[N - 8 + i]);
   return fmaxf(max3f(a[0], a[1], a[2]), fmaxf(max3f(a[3], a[4], a[5]), fmaxf(a[6], a[7])));
 }
 
