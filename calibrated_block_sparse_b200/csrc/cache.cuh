@@ -308,14 +308,15 @@ int launch_cache_join(const CacheAttnParams& p, const SharePlan& plan, const flo
                       cudaStream_t stream);
 
 // Many rows: tiles of 256 rows, the pages of each cut into `splits`.
+// More rows: tiles of them; those behind the first `whole` are split over the
+// keys and joined.
 struct TilePlan {
   int tiles;  // of a stream and key head, at most
+  int chunk;  // (stream, key head) pairs whose tiles are taken together
+  int units;  // tiles of all pairs
+  int whole;
   int splits;
 };
-// Rows of a split's partial results: an even number, for 16-byte alignment.
-__host__ __device__ constexpr int64_t tile_part_rows(int heads_q, int n) {
-  return (static_cast<int64_t>(heads_q) * n + 1) / 2 * 2;
-}
 int launch_cache_attn_tiles(const CacheAttnParams& p, const TilePlan& plan, void* ws, cudaStream_t stream);
 
 }  // namespace calibatt

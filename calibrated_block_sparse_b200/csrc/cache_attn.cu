@@ -116,6 +116,7 @@ struct CachePlan {
   int rows;  // the most that share a key head, in one stream
   SharePlan share;
   TilePlan tile;
+  bool fits = true;  // the grid's limits
 };
 
 // Shares for `slots` CTAs that run at the same time. Up to 4 pages the join
@@ -141,27 +142,55 @@ SharePlan share_plan(int batch, int heads_kv, int rows, int64_t pages, int slots
   return f;
 }
 
-// One CTA per SM, so the splits that give the shortest schedule: waves of CTAs
-// times the pages of one (plus its start and end, about 3 pages' time), plus
-// the joining's traffic (8 bytes per output value and split; a page takes a
-// tile about 1.1 us).
-TilePlan tile_plan(int batch, int heads_q, int heads_kv, int n, int max_new, int64_t rows, int64_t pages, int sms) {
-  TilePlan t;
-  t.tiles = static_cast<int>((rows + kTileRows - 1) / kTileRows);
-  const int64_t units = static_cast<int64_t>(batch) * heads_kv * t.tiles;
-  const double join = static_cast<double>(heads_q) * std::min<int64_t>(static_cast<int64_t>(batch) * max_new, n) *
-                      1024.0 / 6.5e12 / 1.1e-6;
-  double best = 0.0;
+// One CTA per SM. Full waves of tiles are taken whole; the tiles behind them
+// are split so that the schedule is shortest, in a tile's time for a page
+// (about 2 us): rounds of CTAs times the pages of one (plus its start and end,
+// about 3), the joining's launch and its traffic. A pair's last tile, if it has
+// up to 128 rows, takes about 0.75 of a tile's time and fills gaps. All SMs at
+// work at the same time run into the power limit, so a schedule without gaps is
+// no shorter than 1 / 0.88 of the work: splitting 92 of the 240 full tiles of a
+// 480p frame to fill its second wave was slower (1095 -> 1140 us), splitting the
+// 12 behind a wave faster (40 heads, 1024 rows, 20000 keys: 639 -> 427 us).
+bool tile_plan(TilePlan& t, int batch, int heads_kv, int64_t rows, int64_t pages, int sms) {
+  const int64_t tiles = (rows + kTileRows - 1) / kTileRows, pairs = static_cast<int64_t>(batch) * heads_kv;
+  if (pairs > INT_MAX / 2 / tiles) return false;
+  t.tiles = static_cast<int>(tiles);
+  // two waves of tiles: the pages of a pair are read from memory about twice
+  t.chunk = static_cast<int>(std::min(pairs, (2 * sms + tiles - 1) / tiles));
+  const int64_t units = pairs * tiles, whole = units / sms * sms;
+  t.units = static_cast<int>(units);
+  t.whole = t.units;
   t.splits = 1;
+  const int64_t rest = units - whole;
+  if (rest == 0) return true;
+  const bool odd = rows % kTileRows > 0 && rows % kTileRows <= kTileRows / 2;
+  const int64_t small = odd ? std::min(rest, pairs) : 0;
+  const double page = 2e-6;
+  const double join = 2.0 * kTileRows * 520 / 6.5e12 / page * static_cast<double>(rest);
+  const double waves = static_cast<double>(whole / sms);
+  const double least = (static_cast<double>(units) - (odd ? 0.5 * static_cast<double>(pairs) : 0.0)) / sms / 0.88 *
+                       static_cast<double>(pages);
+  double best = 0.0;
   for (int s = 1; s <= 64 && s <= pages; ++s) {
-    const double waves = static_cast<double>((units * s + sms - 1) / sms);
-    const double time = waves * ((pages + s - 1) / s + 3.0) + (s > 1 ? 4.0 + s * join : 0.0);
+    // whole tiles' parts, then the last tiles' into the gaps
+    const int64_t full = (rest - small) * s, over = full % sms, gaps = sms - over, m = small * s;
+    double last = over > 0 ? 1.0 : 0.0;
+    if (m > 0)
+      last = std::max(last, m <= gaps              ? 0.75
+                            : m <= 2 * gaps        ? 1.5
+                            : m <= 2 * gaps + over ? 1.75
+                                                   : 2.5);
+    const double rounds = static_cast<double>(full / sms) + last;
+    const double each = static_cast<double>((pages + s - 1) / s) + 3.0;
+    const double time = std::max(least, waves * static_cast<double>(pages + 3) + rounds * each) +
+                        (s > 1 ? 2.5 + s * join : 0.0);
     if (s == 1 || time < best) {
-      best = time;
+      best = s == 1 ? 0.95 * time : time;  // a split is worth its join if it saves 5 %
       t.splits = s;
     }
   }
-  return t;
+  if (t.splits > 1) t.whole = static_cast<int>(whole);
+  return true;
 }
 
 CachePlan cache_plan(int batch, int heads_q, int heads_kv, int n, int max_new, int max_kv) {
@@ -173,7 +202,7 @@ CachePlan cache_plan(int batch, int heads_q, int heads_kv, int n, int max_new, i
   if (rows <= kMidRows)
     c.share = share_plan(batch, heads_kv, c.rows, pages, rows <= kFewRows ? 2 * sms : sms);
   else
-    c.tile = tile_plan(batch, heads_q, heads_kv, n, max_new, rows, pages, sms);
+    c.fits = tile_plan(c.tile, batch, heads_kv, rows, pages, sms);
   return c;
 }
 
@@ -186,14 +215,13 @@ int check_shape(int batch, int heads_q, int heads_kv, int n, int max_new, int ma
   return CALIBATT_OK;
 }
 
-size_t workspace_bytes(const CachePlan& c, int heads_q, int n) {
+size_t workspace_bytes(const CachePlan& c) {
   if (c.rows <= kMidRows) {
     if (c.share.whole) return 0;
     const int cap = c.rows <= kFewRows ? kFewRows : kMidRows;
     return 2 * static_cast<size_t>(c.share.ctas) * part_floats(cap) * sizeof(float);
   }
-  if (c.tile.splits <= 1) return 0;
-  return c.tile.splits * static_cast<size_t>(tile_part_rows(heads_q, n)) * part_floats(1) * sizeof(float);
+  return static_cast<size_t>(c.tile.units - c.tile.whole) * c.tile.splits * part_floats(kTileRows) * sizeof(float);
 }
 
 }  // namespace
@@ -205,7 +233,7 @@ size_t calibatt_cache_attn_workspace_size(int batch, int heads_q, int heads_kv, 
   using namespace calibatt;
   if (check_shape(batch, heads_q, heads_kv, n, max_new, max_kv) != CALIBATT_OK) return 0;
   if (batch == 0 || n == 0 || max_new == 0) return 0;
-  return workspace_bytes(cache_plan(batch, heads_q, heads_kv, n, max_new, max_kv), heads_q, n);
+  return workspace_bytes(cache_plan(batch, heads_q, heads_kv, n, max_new, max_kv));
 }
 
 int calibatt_cache_attn_fwd(const calibatt_bf16* q, int heads_q, int heads_kv, int n, int d, float scale,
@@ -231,8 +259,9 @@ int calibatt_cache_attn_fwd(const calibatt_bf16* q, int heads_q, int heads_kv, i
                         static_cast<const void*>(table), static_cast<const void*>(k_scale),
                         static_cast<const void*>(v_scale), static_cast<const void*>(lse)})
     if (reinterpret_cast<uintptr_t>(x) & 3u) return CALIBATT_ERR_ALIGN;
-  const CachePlan plan = cache_plan(batch, heads_q, heads_kv, n, max_new, max_kv);
-  const size_t need = workspace_bytes(plan, heads_q, n);
+  CachePlan plan = cache_plan(batch, heads_q, heads_kv, n, max_new, max_kv);
+  if (!plan.fits) return CALIBATT_ERR_UNSUPPORTED;
+  const size_t need = workspace_bytes(plan);
   if (need > 0 && (!ws || ws_bytes < need)) return CALIBATT_ERR_ARG;
   CacheAttnParams p{};
   p.status = status_word();
@@ -265,6 +294,8 @@ int calibatt_cache_attn_fwd(const calibatt_bf16* q, int heads_q, int heads_kv, i
                                        : INT_MAX;
   if (plan.rows <= kFewRows) return launch_cache_attn_few(p, plan.share, ws, stream);
   if (plan.rows <= kMidRows) return launch_cache_attn_mid(p, plan.share, ws, stream);
+  // under a causal mask over mostly new tokens the last tiles are short as they are
+  if (causal_unit > 0 && plan.tile.whole > 0 && max_new > max_kv / 2) plan.tile.whole = plan.tile.units;
   return launch_cache_attn_tiles(p, plan.tile, ws, stream);
 }
 

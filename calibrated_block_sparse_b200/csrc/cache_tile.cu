@@ -96,9 +96,26 @@ __device__ __forceinline__ void store_half(uint32_t row_addr, int r, int j, cons
   st_shared16(row_addr + (((j + 1) ^ (r & 7)) << 4), h[4], h[5], h[6], h[7]);
 }
 
+// Tiles are taken rank by rank for a chunk of (stream, key head) pairs. Under a
+// causal mask the tiles with most keys have the lowest ranks, so the last ones
+// to start are short (3 x 16 heads, 6240 tokens by frames of 1560: 491 -> 455
+// us against head by head).
+struct TileUnit {
+  int b, head, rank;
+};
+__device__ __forceinline__ TileUnit tile_unit(const CacheAttnParams& p, const TilePlan& plan, int unit) {
+  const int per_chunk = plan.chunk * plan.tiles;
+  const int pair0 = unit / per_chunk * plan.chunk, pairs = min(plan.chunk, p.batch * p.heads_kv - pair0);
+  const int pair = pair0 + unit % per_chunk % pairs;
+  return {pair / p.heads_kv, pair % p.heads_kv, unit % per_chunk / pairs};
+}
+__device__ __forceinline__ int tile_first_row(const CacheAttnParams& p, const TileUnit& u, int tiles) {
+  return (p.unit > 0 ? tiles - 1 - u.rank : u.rank) * kTileRows;
+}
+
 template <bool SW>
 __global__ void __launch_bounds__(kTileThreads, 1)
-    cache_tile_kernel(const __grid_constant__ CacheAttnParams p, int tiles, int splits, float* part) {
+    cache_tile_kernel(const __grid_constant__ CacheAttnParams p, const TilePlan plan, float* part) {
   using L = TileLayout;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -109,18 +126,19 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   // ------------------------------------------------------------ the CTA's work
-  const int split = blockIdx.x;
-  const int head = blockIdx.y / tiles;
-  const int tile = tiles - 1 - static_cast<int>(blockIdx.y) % tiles;  // causal: most keys first
-  const int b = blockIdx.z;
+  const int behind = static_cast<int>(blockIdx.x) - plan.whole;
+  const int splits = behind < 0 ? 1 : plan.splits, split = behind < 0 ? 0 : behind % splits;
+  const TileUnit u = tile_unit(p, plan, plan.whole + (behind < 0 ? behind : behind / splits));
+  const int b = u.b, head = u.head;
   const Stream st = stream_of(p.tok_start, p.kv_len, b, p.n, p.table_stride);
   if (st.bad || st.n_new > p.max_new) {
     if (threadIdx.x == 0) record_error(p.status, CALIBATT_ERR_CSR);
     return;
   }
   const int rows = st.n_new * p.group;
-  const int r0 = tile * kTileRows;
-  if (r0 >= rows) return;
+  const int tiles = (rows + kTileRows - 1) / kTileRows;
+  if (u.rank >= tiles) return;
+  const int r0 = tile_first_row(p, u, tiles);
   const int r1 = min(rows, r0 + kTileRows);
   const int first_pos = st.len - st.n_new;  // position of the first new token
   const int least = visible(first_pos + r0 / p.group, st.len, p.unit);        // keys that every row sees
@@ -460,11 +478,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     if (done && active) {
       const bool some = np > 0 && l_run != 0.f;
       const float inv = some ? 1.f / l_run : 0.f;
-      const int64_t part_rows = tile_part_rows(p.heads_q, p.n);
-      float* out = part + split * part_rows * part_floats(1);
+      float* out = part + static_cast<int64_t>(behind) * part_floats(kTileRows);  // with splits
       if (row_valid) {
         if (splits > 1)
-          *reinterpret_cast<float2*>(out + part_rows * 128 + 2 * at) = make_float2(m_run, some ? l_run : 0.f);
+          *reinterpret_cast<float2*>(out + kTileRows * 128 + 2 * (s * 128 + row)) = make_float2(m_run, some ? l_run : 0.f);
         else if (p.lse)
           p.lse[at] = some ? (m_run + log2f(l_run)) * kLn2 : -INFINITY;
       }
@@ -496,7 +513,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
         if (!row_valid) continue;
         if (splits > 1) {
-          uint4* dst = reinterpret_cast<uint4*>(out + at * 128 + cc * 32);
+          uint4* dst = reinterpret_cast<uint4*>(out + (s * 128 + row) * 128 + cc * 32);
 #pragma unroll
           for (int e = 0; e < 8; ++e)
             dst[e] = some ? make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]) : make_uint4(0, 0, 0, 0);
@@ -524,17 +541,22 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 // Joins the splits of the rows: a warp per row.
 constexpr int kJoinRows = 8;
 __global__ void __launch_bounds__(32 * kJoinRows)
-    cache_tile_join_kernel(const __grid_constant__ CacheAttnParams p, int splits, const float* part) {
+    cache_tile_join_kernel(const __grid_constant__ CacheAttnParams p, const TilePlan plan, const float* part) {
   const int lane = threadIdx.x & 31;
-  const int b = blockIdx.z;
-  const Stream st = stream_of(p.tok_start, p.kv_len, b, p.n, p.table_stride);
-  const int tok = blockIdx.x * kJoinRows + (threadIdx.x >> 5);
+  const int nth = blockIdx.x / (kTileRows / kJoinRows);  // of the split tiles
+  const int row = blockIdx.x % (kTileRows / kJoinRows) * kJoinRows + (threadIdx.x >> 5);
+  const TileUnit u = tile_unit(p, plan, plan.whole + nth);
+  const Stream st = stream_of(p.tok_start, p.kv_len, u.b, p.n, p.table_stride);
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (st.bad || st.n_new > p.max_new || tok >= st.n_new) return;
-  const int64_t at = static_cast<int64_t>(blockIdx.y) * p.n + st.t0 + tok;
-  const int64_t part_rows = tile_part_rows(p.heads_q, p.n);
+  if (st.bad || st.n_new > p.max_new) return;
+  const int rows = st.n_new * p.group, tiles = (rows + kTileRows - 1) / kTileRows;
+  if (u.rank >= tiles) return;
+  const int r = tile_first_row(p, u, tiles) + row;
+  if (r >= rows) return;
   join_row(
-      p, at, lane, 0, splits, [&](int i) { return part + i * part_rows * part_floats(1); }, at, part_rows);
+      p, static_cast<int64_t>(u.head * p.group + r % p.group) * p.n + st.t0 + r / p.group, lane, 0, plan.splits,
+      [&](int i) { return part + (static_cast<int64_t>(nth) * plan.splits + i) * part_floats(kTileRows); }, row,
+      kTileRows);
 }
 
 template <bool SW>
@@ -550,10 +572,8 @@ int launch(const CacheAttnParams& p, const TilePlan& plan, float* part, cudaStre
     if (cudaFuncGetAttributes(&fa, cache_tile_kernel<SW>) == cudaSuccess) launch_regs = fa.numRegs;
   });
   if (launch_regs * kTileThreads < kTileRegs) return CALIBATT_ERR_CUDA;
-  const int64_t y = static_cast<int64_t>(p.heads_kv) * plan.tiles;
-  if (y > 65535) return CALIBATT_ERR_UNSUPPORTED;
-  cache_tile_kernel<SW><<<dim3(plan.splits, static_cast<unsigned>(y), p.batch), kTileThreads, TileLayout::kDynSmem,
-                          stream>>>(p, plan.tiles, plan.splits, part);
+  const int64_t ctas = plan.whole + static_cast<int64_t>(plan.units - plan.whole) * plan.splits;
+  cache_tile_kernel<SW><<<static_cast<unsigned>(ctas), kTileThreads, TileLayout::kDynSmem, stream>>>(p, plan, part);
   return cudaGetLastError() == cudaSuccess ? CALIBATT_OK : CALIBATT_ERR_CUDA;
 }
 
@@ -563,9 +583,9 @@ int launch_cache_attn_tiles(const CacheAttnParams& p, const TilePlan& plan, void
   float* part = static_cast<float*>(ws);
   const int rc = p.wait_limit_ns < kShortWaitNs ? launch<true>(p, plan, part, stream)
                                                 : launch<false>(p, plan, part, stream);
-  if (rc != CALIBATT_OK || plan.splits <= 1) return rc;
+  if (rc != CALIBATT_OK || plan.whole == plan.units) return rc;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((std::min(p.max_new, p.n) + kJoinRows - 1) / kJoinRows, p.heads_q, p.batch);
+  cfg.gridDim = dim3(static_cast<unsigned>(plan.units - plan.whole) * (kTileRows / kJoinRows));
   cfg.blockDim = dim3(32 * kJoinRows);
   cfg.stream = stream;
   cudaLaunchAttribute attr{};
@@ -573,7 +593,7 @@ int launch_cache_attn_tiles(const CacheAttnParams& p, const TilePlan& plan, void
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, cache_tile_join_kernel, p, plan.splits, static_cast<const float*>(part)) ==
+  return cudaLaunchKernelEx(&cfg, cache_tile_join_kernel, p, plan, static_cast<const float*>(part)) ==
                  cudaSuccess
              ? CALIBATT_OK
              : CALIBATT_ERR_CUDA;

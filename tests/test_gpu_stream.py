@@ -334,6 +334,9 @@ SHAPES = [
     (1, 1, [129, 5], [129, 1000], 1), (3, 3, [256], [2000], 0), (1, 1, [257], [5000], 16),
     (4, 1, [65, 70], [900, 71], 1),
     (2, 2, [700, 300, 40], [2500, 300, 700], 100), (8, 8, [384], [1100], 128),
+    # more tiles than the SMs of any GPU take at once: the ones behind are split, or under the causal mask not
+    (80, 80, [300], [1280], 0), (160, 40, [70], [1300], 30), (20, 20, [300, 257, 40, 290], [1000, 1280, 640, 1290], 1),
+    (80, 80, [300], [420], 1), (40, 40, [1024], [2000], 1),
 ]
 
 
@@ -355,7 +358,8 @@ def test_cache_attention_matches_oracle(binding, so, hq, hk, new, lens, unit):
     _attn_close(o[:, cut], lse[:, cut], [r[:, cut] for r in ref], q, c, lens, scale, _p_err(new, hq, hk))
 
 
-@pytest.mark.parametrize("new,lens", [([4, 3], [2, 0]), ([200], [150]), ([150, 1], [0, 0])])
+@pytest.mark.parametrize("new,lens", [([4, 3], [2, 0]), ([200], [150]), ([150, 1], [0, 0]), ([16, 9], [7, 0]),
+                                      ([30], [11]), ([60, 50], [0, 45])])
 @pytest.mark.parametrize("unit", [0, 1, 5])
 def test_rows_that_see_nothing(binding, so, new, lens, unit):
     c = Cache(len(new), 2, 2, seed=3)
@@ -371,7 +375,7 @@ def test_rows_that_see_nothing(binding, so, new, lens, unit):
     assert binding.get_status() == 0
 
 
-@pytest.mark.parametrize("hq,new,unit", [(2, 3, 1), (2, 40, 1), (1, 300, 128), (1, 200, 1)])
+@pytest.mark.parametrize("hq,new,unit", [(2, 3, 1), (2, 20, 1), (2, 40, 1), (2, 100, 9), (1, 300, 128), (1, 200, 1)])
 def test_nan_in_later_tokens_does_not_reach_earlier_rows(binding, so, hq, new, unit):
     lens = 300 + new
     c = Cache(1, hq, -(-lens // 128), seed=5)
@@ -394,7 +398,7 @@ def test_nan_in_later_tokens_does_not_reach_earlier_rows(binding, so, hq, new, u
                         _p_err([new], 1, 1))
 
 
-@pytest.mark.parametrize("hq,new,unit", [(2, 3, 1), (1, 200, 1), (1, 260, 7)])
+@pytest.mark.parametrize("hq,new,unit", [(2, 3, 1), (2, 30, 1), (1, 60, 4), (2, 100, 1), (1, 200, 1), (1, 260, 7)])
 def test_nan_in_a_value_alone_reaches_its_channel_of_the_rows_that_see_it(binding, so, hq, new, unit):
     lens = 200 + new
     c = Cache(1, hq, -(-lens // 128), seed=15)
@@ -409,7 +413,7 @@ def test_nan_in_a_value_alone_reaches_its_channel_of_the_rows_that_see_it(bindin
     _attn_close(o, lse, ref, q, c, [lens], 0.05, _p_err([new], 1, 1))
 
 
-@pytest.mark.parametrize("rows", [6, 140])
+@pytest.mark.parametrize("rows", [6, 20, 50, 100, 140])
 @pytest.mark.parametrize("lens", [128, 256, 384])
 def test_extreme_queries_and_scales(binding, so, rows, lens):
     """Rows of very large and very small queries, pages whose scales lie far apart, infinities in one row."""

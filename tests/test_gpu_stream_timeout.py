@@ -30,8 +30,15 @@ def test_cache_attention_wait_runs_out_then_context_is_usable(heads, kv_heads, n
     assert binding.get_status() == 0
     try:
         binding.set_wait_limit(1e-9)
-        call()
-        assert binding.get_status() == -6
+        # a wait that begins and ends within one tick of the GPU's timer is not
+        # seen to take time, so a call may get through
+        status = 0
+        for _ in range(200):
+            call()
+            status = binding.get_status()
+            if status != 0:
+                break
+        assert status == -6
     finally:
         binding.set_wait_limit(0.0)
     o, lse = call()
