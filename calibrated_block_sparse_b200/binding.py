@@ -809,8 +809,11 @@ class _CtypesCalls:
 
     @staticmethod
     def rope(fn, plan, q, qt, qh, hq, k, kt, kh, hk, n, pos, H, W, s0, s1, s2, qo, qot, qoh, ko, kot, koh, stream):
-        return fn(plan, q, qt, qh, hq, k, kt, kh, hk, n, HEAD_DIM, pos, H, W, (ctypes.c_int32 * 3)(s0, s1, s2), qo, qot,
-                  qoh, ko, kot, koh, stream)
+        start = (s0, s1, s2)
+        if any(not -1 << 31 <= index_of(s) < 1 << 31 for s in start):
+            raise OverflowError("a start that does not fit 32 bits")
+        return fn(plan, q, qt, qh, hq, k, kt, kh, hk, n, HEAD_DIM, pos, H, W, (ctypes.c_int32 * 3)(*start), qo, qot, qoh,
+                  ko, kot, koh, stream)
 
     @staticmethod
     def cache_write(fn, k, kt, kh, v, vt, vh, heads, n, *rest):

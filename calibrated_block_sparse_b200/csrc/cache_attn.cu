@@ -124,8 +124,7 @@ struct CachePlan {
 // number of times, their pages are cut alike and no share crosses from one to
 // the next, which costs about 4 pages' time (its start and end once more);
 // ragged streams cross anyway. A share has at least two pages.
-SharePlan share_plan(int batch, int heads_kv, int rows, int64_t pages, int slots) {
-  SharePlan f;
+bool share_plan(SharePlan& f, int batch, int heads_kv, int rows, int64_t pages, int slots) {
   const int64_t units = static_cast<int64_t>(batch) * heads_kv;
   f.rows = rows;
   f.whole = pages <= 4;
@@ -138,8 +137,8 @@ SharePlan share_plan(int batch, int heads_kv, int rows, int64_t pages, int slots
     }
     ctas = std::min<int64_t>(ctas, units * ((pages + 1) / 2));
   }
-  f.ctas = static_cast<int>(ctas);
-  return f;
+  f.ctas = static_cast<int>(std::min<int64_t>(ctas, INT_MAX));
+  return ctas <= INT_MAX;
 }
 
 // One CTA per SM. Full waves of tiles are taken whole; the tiles behind them
@@ -200,7 +199,7 @@ CachePlan cache_plan(int batch, int heads_q, int heads_kv, int n, int max_new, i
   const int sms = sm_count();
   c.rows = static_cast<int>(rows);
   if (rows <= kMidRows)
-    c.share = share_plan(batch, heads_kv, c.rows, pages, rows <= kFewRows ? 2 * sms : sms);
+    c.fits = share_plan(c.share, batch, heads_kv, c.rows, pages, rows <= kFewRows ? 2 * sms : sms);
   else
     c.fits = tile_plan(c.tile, batch, heads_kv, rows, pages, sms);
   return c;

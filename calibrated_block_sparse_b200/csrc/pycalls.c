@@ -41,6 +41,11 @@ static PyObject* rope(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   long long v[24];
   (void)self;
   if (!take(a, n, 24, v, -1)) return NULL;
+  for (int i = 14; i < 17; ++i)
+    if (v[i] != small(v[i])) {
+      PyErr_SetString(PyExc_OverflowError, "a start that does not fit 32 bits");
+      return NULL;
+    }
   const int32_t start[3] = {small(v[14]), small(v[15]), small(v[16])};
   int rc;
   Py_BEGIN_ALLOW_THREADS;

@@ -28,7 +28,8 @@ class FrameStreams:
     pages: pages of 128 tokens shared by the streams; max_tokens: the most
     tokens of one stream (default: all pages). A step that needs more pages
     than are free, or makes a stream longer than max_tokens, is refused before
-    anything is changed.
+    anything is changed. A step copies its lists from the host; a captured graph
+    calls the binding's functions with lists of its own on the device.
     """
 
     def __init__(self, batch, heads, kv_heads, H, W, pages, max_tokens=None, plan=None, device=None):
@@ -75,11 +76,17 @@ class FrameStreams:
         binding.cache_attn_fwd (H * W: a token sees its own frame and earlier
         ones; 0: all tokens of its stream, those of this step too)."""
         n = q.shape[0]
-        new = [n] if new is None and self.batch == 1 else new
-        if new is None or len(new) != self.batch or sum(new) != n or min(new) < 0:
+        if new is None and self.batch == 1:
+            new = [n]
+        new = [] if new is None else [int(m) for m in new]
+        if len(new) != self.batch or sum(new) != n or min(new) < 0:
             raise ValueError(f"new must give each of the {self.batch} streams its share of the {n} tokens")
-        if q.shape[1] != self.heads or k.shape[1] != self.kv_heads:
-            raise ValueError(f"q must have {self.heads} heads, k and v {self.kv_heads}")
+        rest = binding.HEAD_DIM,
+        if q.shape != (n, self.heads) + rest or k.shape != (n, self.kv_heads) + rest or v.shape != k.shape:
+            raise ValueError(f"q must be [{n}][{self.heads}][{rest[0]}], k and v [{n}][{self.kv_heads}][{rest[0]}]")
+        for t, name in ((q, "q"), (k, "k"), (v, "v")):
+            if t.dtype != torch.bfloat16 or t.device != self.k8.device or t.stride(2) != 1:
+                raise ValueError(f"{name} must be bfloat16 on {self.k8.device} with contiguous channels")
         self._extend(new)
         dev = self.k8.device
         hw = self.H * self.W
@@ -89,13 +96,15 @@ class FrameStreams:
             t = torch.cat([torch.arange(a, a + m) for a, m in zip(self.lengths, new)])
             where = dict(pos=torch.stack([t // hw, t % hw // self.W, t % self.W], 1).to(torch.int32).to(dev))
         q, k = binding.rope_fwd(q, k, self.plan, **where)
-        self.lengths = [a + m for a, m in zip(self.lengths, new)]
+        lengths = [a + m for a, m in zip(self.lengths, new)]
         start = torch.tensor([0] + new, dtype=torch.int32).cumsum(0, dtype=torch.int32).to(dev)
-        length = torch.tensor(self.lengths, dtype=torch.int32).to(dev)
+        length = torch.tensor(lengths, dtype=torch.int32).to(dev)
         binding.cache_write(k.transpose(0, 1), v, self.k8, self.v8, self.k_scale, self.v_scale, start, length,
                             self.table, max_new=max(new))
-        return binding.cache_attn_fwd(q, self.k8, self.v8, self.k_scale, self.v_scale, start, length, self.table,
-                                      max_new=max(new), max_kv=max(self.lengths), causal_unit=causal_unit)
+        out = binding.cache_attn_fwd(q, self.k8, self.v8, self.k_scale, self.v_scale, start, length, self.table,
+                                     max_new=max(new), max_kv=max(lengths), causal_unit=causal_unit)
+        self.lengths = lengths
+        return out
 
     def drop(self, b):
         """Ends stream b: its pages are free again and it starts anew."""

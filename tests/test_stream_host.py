@@ -77,6 +77,20 @@ def test_rope_refusals(binding, fn):
     assert call(plan=plan) == UNSUPPORTED
 
 
+@pytest.mark.parametrize("compiled", [True, False])
+def test_starts_beyond_32_bits_are_refused(binding, compiled):
+    calls = binding._load_calls() if compiled else binding._CtypesCalls
+    assert (calls is not binding._CtypesCalls) == compiled  # build() made the compiled calls
+    fn = binding._fns[0] if compiled else binding.load().calibatt_rope_fwd
+    plan = binding.rope_plan()
+    a = [ctypes.addressof(plan), FAKE, 512, 128, 4, None, 0, 0, 0, 0, None, 2, 5]
+    out = [FAKE + (1 << 24), 128, 1280, None, 0, 0, None]
+    assert calls.rope(fn, *a, 1 << 30, 0, -1 << 31, *out) == OK  # no tokens
+    for bad in (1 << 31, -(1 << 31) - 1, 1 << 40):
+        with pytest.raises(OverflowError):
+            calls.rope(fn, *a, 0, bad, 0, *out)
+
+
 def _write(binding, **kw):
     a = dict(k=FAKE, kts=512, khs=128, v=FAKE, vts=512, vhs=128, heads=4, n=10, d=128, start=FAKE, kv=FAKE, batch=2,
              max_new=5, table=FAKE, ts=3, pages=9, k8=FAKE, v8=FAKE + 4096, ks=FAKE, vs=FAKE + 64)
@@ -107,7 +121,9 @@ def _attn(binding, **kw):
 def test_cache_attn_refusals(binding):
     for fine in (dict(n=0), dict(batch=0), dict(max_new=0)):
         assert _attn(binding, **fine) == OK, fine
-    for bad in (dict(d=64), dict(batch=70000), dict(hq=70000, hk=1)):
+    for bad in (dict(d=64), dict(batch=70000), dict(hq=70000, hk=1),
+                dict(batch=65535, hq=65535, hk=65535),  # more CTAs than a grid takes: few rows, and many
+                dict(batch=65535, hq=60000, hk=60000, n=400, max_new=400)):
         assert _attn(binding, **bad) == UNSUPPORTED, bad
     for bad in (dict(q=0), dict(o=0), dict(hq=7), dict(hk=0), dict(n=-1), dict(scale=0.0), dict(scale=float("inf")),
                 dict(scale=float("nan")), dict(unit=-1), dict(start=0), dict(kv=0), dict(table=0), dict(k8=0),
