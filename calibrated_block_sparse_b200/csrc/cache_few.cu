@@ -32,6 +32,12 @@
 // the softmax of 16 rows in one thread is a chain of ~4000 cycles a page.
 // The running maximum of a row moves only if it grew by more than 2^4, which a
 // page finds out with one vote of a group's warps.
+//
+// Measured on B200: one token of 40 heads over 32760 cached (335 MB) in 60 us,
+// 86 % of the rate of a plain copy; 16 streams of 20000 tokens, 40 query heads
+// on 8, 3 tokens each (15 rows a key head, 437 MB) in 105 us, 64 %: there half of
+// the issue slots are taken, by chains of 8 warps per CTA that split every
+// weight into its parts.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
