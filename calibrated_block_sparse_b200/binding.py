@@ -766,8 +766,9 @@ def rope_plan(dims=(44, 42, 42), theta=10000.0, pairing="interleaved", ladder="a
     return plan
 
 
-# The streaming calls are made per layer and frame, or per token, so their
-# checks are kept to a few attribute reads per tensor.
+# The streaming calls are made per layer and frame, or per token: a call whose
+# arguments are in order is made by compiled code (_load_fast). What follows
+# checks and makes the others.
 
 def _refuse(t, name, dtype, index, contiguous=True):
     if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype and (not contiguous or t.is_contiguous()):
@@ -804,43 +805,28 @@ def _new(like, shape, dtype, stream):
         return like.new_empty(shape, dtype=dtype)
 
 
-class _CtypesCalls:
-    """The streaming calls through ctypes, with the arguments of the compiled module (_pycalls): the function first."""
-
-    @staticmethod
-    def rope(fn, plan, q, qt, qh, hq, k, kt, kh, hk, n, pos, H, W, s0, s1, s2, qo, qot, qoh, ko, kot, koh, stream):
-        start = (s0, s1, s2)
-        if any(not -1 << 31 <= index_of(s) < 1 << 31 for s in start):
-            raise OverflowError("a start that does not fit 32 bits")
-        return fn(plan, q, qt, qh, hq, k, kt, kh, hk, n, HEAD_DIM, pos, H, W, (ctypes.c_int32 * 3)(*start), qo, qot, qoh,
-                  ko, kot, koh, stream)
-
-    @staticmethod
-    def cache_write(fn, k, kt, kh, v, vt, vh, heads, n, *rest):
-        return fn(k, kt, kh, v, vt, vh, heads, n, HEAD_DIM, *rest)
-
-    @staticmethod
-    def cache_attn(fn, q, hq, hk, n, *rest):
-        return fn(q, hq, hk, n, HEAD_DIM, *rest)
+class _NoFast:
+    """In the place of the compiled calls where they were not built."""
+    rope = cache_write = cache_attn = staticmethod(lambda *args: None)
 
 
-_calls = None
-_fns = ()
+_fast = None
 
 
-def _load_calls():
-    """The compiled calls, or those of ctypes, and the four functions as they take them."""
-    global _calls, _fns
-    lib = load()
-    fns = [getattr(lib, f"calibatt_{x}") for x in ("rope_fwd", "rope_bwd", "cache_write", "cache_attn_fwd")]
+def _load_fast():
+    """The compiled calls (csrc/pycalls.cpp): they make a call whose arguments
+    are in order and return None for any other, which the functions below then
+    make or refuse."""
+    global _fast
+    lib, fast = load(), _NoFast
     if os.path.exists(_build.PYCALLS):
         spec = importlib.util.spec_from_file_location("_pycalls", _build.PYCALLS)
-        module = importlib.util.module_from_spec(spec)
-        spec.loader.exec_module(module)
-        _fns, _calls = tuple(ctypes.cast(f, ctypes.c_void_p).value for f in fns), module
-    else:
-        _fns, _calls = tuple(fns), _CtypesCalls
-    return _calls
+        fast = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(fast)
+        fast.bind(*(ctypes.cast(getattr(lib, f"calibatt_{x}"), ctypes.c_void_p).value
+                    for x in ("rope_fwd", "rope_bwd", "cache_write", "cache_attn_fwd", "cache_attn_workspace_size")))
+    _fast = fast
+    return fast
 
 
 def _rope(forward, q, k, plan, grid, start, pos, q_out, k_out, stream):
@@ -892,12 +878,12 @@ def _rope(forward, q, k, plan, grid, start, pos, q_out, k_out, stream):
         if pos.shape != (n, 3):
             raise ValueError(f"pos must be [{n}][3]")
         H, W, pos_ptr = 0, 0, pos.data_ptr()
-    s0, s1, s2 = start
-    calls = _calls or _load_calls()
-    rc = calls.rope(_fns[0 if forward else 1], ctypes.addressof(plan), q.data_ptr(), st[tok], st[hd], heads, k_ptr,
-                    kst[tok], kst[hd], heads_k, n, pos_ptr, H, W, s0, s1, s2, q_out.data_ptr(), ost[hd], ost[tok],
-                    k_out_ptr, kost[hd], kost[tok],
-                    _current_raw_stream(index) if stream is None else stream.cuda_stream)
+    if len(start) != 3 or any(not -1 << 31 <= index_of(x) < 1 << 31 for x in start):
+        raise ValueError("start must be three numbers of 32 bits")
+    fn = load().calibatt_rope_fwd if forward else load().calibatt_rope_bwd
+    rc = fn(ctypes.byref(plan), q.data_ptr(), st[tok], st[hd], heads, k_ptr, kst[tok], kst[hd], heads_k, n, HEAD_DIM,
+            pos_ptr, H, W, (ctypes.c_int32 * 3)(*start), q_out.data_ptr(), ost[hd], ost[tok], k_out_ptr, kost[hd],
+            kost[tok], _current_raw_stream(index) if stream is None else stream.cuda_stream)
     if rc:
         _check(rc, "calibatt_rope_fwd" if forward else "calibatt_rope_bwd")
     return q_out, k_out
@@ -908,12 +894,20 @@ def rope_fwd(q, k, plan, grid=None, start=(0, 0, 0), pos=None, q_out=None, k_out
     any strides by their positions: a grid (H, W) whose first token is at
     `start` (time, height, width), or pos, int32 [n][3]. Returns them as
     [heads][n][128], the layout of the attention calls."""
+    if stream is None:
+        out = (_fast or _load_fast()).rope(True, q, k, ctypes.addressof(plan), grid, start, pos, q_out, k_out)
+        if out is not None:
+            return out
     return _rope(True, q, k, plan, grid, start, pos, q_out, k_out, stream)
 
 
 def rope_bwd(dq_out, dk_out, plan, grid=None, start=(0, 0, 0), pos=None, dq=None, dk=None, stream=None):
     """Gradients of rope_fwd's inputs, [n][heads][128], from those of its
     outputs, [heads][n][128] of any strides (expanded ones too)."""
+    if stream is None:
+        out = (_fast or _load_fast()).rope(False, dq_out, dk_out, ctypes.addressof(plan), grid, start, pos, dq, dk)
+        if out is not None:
+            return out
     return _rope(False, dq_out, dk_out, plan, grid, start, pos, dq, dk, stream)
 
 
@@ -949,6 +943,9 @@ def cache_write(k, v, k8, v8, k_scale, v_scale, tok_start, kv_len, table, max_ne
     """Appends keys and values [n][heads][128] (any strides) of the batch's new
     tokens to the paged 8-bit cache (calibatt_cache_write). max_new: the most
     new tokens of one stream (default: n)."""
+    if stream is None and (_fast or _load_fast()).cache_write(k, v, k8, v8, k_scale, v_scale, tok_start, kv_len, table,
+                                                              max_new):
+        return
     shape, ks = _want_rows(k, "k")
     index = k.get_device()
     if torch.cuda.current_device() != index:
@@ -961,11 +958,11 @@ def cache_write(k, v, k8, v8, k_scale, v_scale, tok_start, kv_len, table, max_ne
     pages, cache_heads, batch, width = _cache_args(k8, v8, k_scale, v_scale, tok_start, kv_len, table, index)
     if cache_heads != heads:
         raise ValueError(f"the cache has {cache_heads} heads, k has {heads}")
-    calls = _calls or _load_calls()
-    rc = calls.cache_write(_fns[2], k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], heads, n,
-                           tok_start.data_ptr(), kv_len.data_ptr(), batch, n if max_new is None else index_of(max_new),
-                           table.data_ptr(), width, pages, k8.data_ptr(), v8.data_ptr(), k_scale.data_ptr(),
-                           v_scale.data_ptr(), _current_raw_stream(index) if stream is None else stream.cuda_stream)
+    rc = load().calibatt_cache_write(
+        k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], heads, n, HEAD_DIM, tok_start.data_ptr(),
+        kv_len.data_ptr(), batch, n if max_new is None else index_of(max_new), table.data_ptr(), width, pages,
+        k8.data_ptr(), v8.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+        _current_raw_stream(index) if stream is None else stream.cuda_stream)
     if rc:
         _check(rc, "calibatt_cache_write")
 
@@ -990,6 +987,11 @@ def cache_attn_fwd(q, k8, v8, k_scale, v_scale, tok_start, kv_len, table, max_ne
     8-bit cache (calibatt_cache_attn_fwd); returns (o, lse). Rows of tokens
     that belong to no stream keep what o and lse hold. max_new, max_kv: the
     most new and cached tokens of one stream (default: n, the table's width)."""
+    if stream is None:
+        out = (_fast or _load_fast()).cache_attn(q, k8, v8, k_scale, v_scale, tok_start, kv_len, table, max_new, max_kv,
+                                                 causal_unit, o, lse, ws, scale, want_lse)
+        if out is not None:
+            return out
     if not isinstance(q, torch.Tensor):
         _refuse(q, "q", torch.bfloat16, None)
     index = q.get_device()
@@ -1015,20 +1017,19 @@ def cache_attn_fwd(q, k8, v8, k_scale, v_scale, tok_start, kv_len, table, max_ne
         lse = _new(q, (heads_q, n), torch.float32, stream)
     max_new = n if max_new is None else index_of(max_new)
     max_kv = width * BLOCK if max_kv is None else index_of(max_kv)
-    calls = _calls or _load_calls()
     if ws is not None:
         _want(ws, torch.uint8, "ws", index)
         ws_bytes = ws.numel()
     else:
-        ws_bytes = _lib.calibatt_cache_attn_workspace_size(batch, heads_q, heads_kv, n, max_new, max_kv)
+        ws_bytes = load().calibatt_cache_attn_workspace_size(batch, heads_q, heads_kv, n, max_new, max_kv)
         if ws_bytes:
             ws = _new(q, (ws_bytes,), torch.uint8, stream)
-    rc = calls.cache_attn(_fns[3], q.data_ptr(), heads_q, heads_kv, n, _SCALE if scale is None else float(scale),
-                          index_of(causal_unit), tok_start.data_ptr(), kv_len.data_ptr(), batch, max_new, max_kv,
-                          table.data_ptr(), width, pages, k8.data_ptr(), v8.data_ptr(), k_scale.data_ptr(),
-                          v_scale.data_ptr(), o.data_ptr(), None if lse is None else lse.data_ptr(),
-                          None if ws is None else ws.data_ptr(), ws_bytes,
-                          _current_raw_stream(index) if stream is None else stream.cuda_stream)
+    rc = load().calibatt_cache_attn_fwd(
+        q.data_ptr(), heads_q, heads_kv, n, HEAD_DIM, _SCALE if scale is None else float(scale), index_of(causal_unit),
+        tok_start.data_ptr(), kv_len.data_ptr(), batch, max_new, max_kv, table.data_ptr(), width, pages, k8.data_ptr(),
+        v8.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), o.data_ptr(), None if lse is None else lse.data_ptr(),
+        None if ws is None else ws.data_ptr(), ws_bytes,
+        _current_raw_stream(index) if stream is None else stream.cuda_stream)
     if rc:
         _check(rc, "calibatt_cache_attn_fwd")
     return o, lse

@@ -1,11 +1,12 @@
 """Build libcalibatt.so (the C-ABI CUDA library) in-tree with nvcc for sm_100a,
-and _pycalls.so (its streaming calls without ctypes) where Python's headers are.
+and _pycalls.so (its streaming calls without ctypes) against the installed torch.
 
     python -m calibrated_block_sparse_b200.build [--verbose-ptxas]
 """
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -37,7 +38,7 @@ def needs_build() -> bool:
     if not os.path.exists(LIB):
         return True
     t = os.path.getmtime(LIB)
-    deps = sources() + [os.path.join(CSRC, "pycalls.c")] + glob.glob(os.path.join(CSRC, "*.cuh")) + \
+    deps = sources() + [os.path.join(CSRC, "pycalls.cpp")] + glob.glob(os.path.join(CSRC, "*.cuh")) + \
         glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(INCLUDE, "*.h"))
     return any(os.path.getmtime(p) > t for p in deps)
 
@@ -54,6 +55,7 @@ def build(force: bool = False, ptxas_verbose: bool = False, jobs: int = 4, out_p
     if ptxas_verbose:
         flags += ["-Xptxas", "-v"]
     flags += [f"-D{d}" for d in defines]
+    pycalls = start_pycalls(cc) if out_path is None else None
     with tempfile.TemporaryDirectory(prefix="calibatt_build_") as tmp:
         objs = []
         procs = []
@@ -71,21 +73,31 @@ def build(force: bool = False, ptxas_verbose: bool = False, jobs: int = 4, out_p
         subprocess.check_call([cc, *ARCH, "-shared", "-o", out, *objs, "-lcudart_static", "-ldl", "-lpthread",
                                "-lrt"])
         os.replace(out, target)
-    if out_path is None:
-        build_pycalls()
+    if pycalls is not None:
+        process, made = pycalls
+        if process.wait() != 0:
+            raise RuntimeError("compiling pycalls.cpp failed")
+        os.replace(made, PYCALLS)
     return target
 
 
-def build_pycalls():
-    """Compile csrc/pycalls.c; returns its path, or None without a C compiler or Python's headers."""
-    gcc, include = shutil.which("gcc") or shutil.which("cc"), sysconfig.get_paths()["include"]
-    if gcc is None or not os.path.exists(os.path.join(include, "Python.h")):
+def start_pycalls(cc):
+    """Starts compiling csrc/pycalls.cpp: the process and the file it makes, or
+    None without a C++ compiler or the headers of Python or torch."""
+    gxx, include = shutil.which("g++") or shutil.which("c++"), sysconfig.get_paths()["include"]
+    spec = importlib.util.find_spec("torch")
+    if gxx is None or spec is None or not os.path.exists(os.path.join(include, "Python.h")):
+        return None
+    torch = spec.submodule_search_locations[0]
+    if not os.path.exists(os.path.join(torch, "include", "torch", "csrc", "autograd", "python_variable.h")):
         return None
     out = PYCALLS + f".tmp{os.getpid()}"
-    subprocess.check_call([gcc, "-O2", "-std=c11", "-Wall", "-Wextra", "-fPIC", "-shared", "-I", include, "-I", INCLUDE,
-                           os.path.join(CSRC, "pycalls.c"), "-o", out])
-    os.replace(out, PYCALLS)
-    return PYCALLS
+    headers = [include, INCLUDE, os.path.join(torch, "include"),
+               os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+               os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(cc))), "include")]
+    return subprocess.Popen([gxx, "-O2", "-std=c++17", "-Wall", "-fPIC", "-shared", *(f"-I{x}" for x in headers),
+                             os.path.join(CSRC, "pycalls.cpp"), "-o", out, "-L" + os.path.join(torch, "lib"), "-lc10",
+                             "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]), out
 
 
 if __name__ == "__main__":

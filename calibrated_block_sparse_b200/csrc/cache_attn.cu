@@ -119,15 +119,20 @@ struct CachePlan {
   bool fits = true;  // the grid's limits
 };
 
-// Shares for `slots` CTAs that run at the same time. Up to 4 pages the join
-// costs more than the split saves. Where the streams' key heads fit a whole
+// Shares for `slots` CTAs that run at the same time. Up to 5 pages the join
+// costs more than the split saves, and up to 8 if there are several streams,
+// whose shares begin and end inside others' (measured whole and split: 40 heads
+// of one stream, a row each, 5 pages 10.0 and 11.5 us, 8 pages 13.1 and 12.0;
+// 16 streams of 8 heads, 5 pages 10.0 and 15.3 us, 8 pages 13.7 and 16.4; 4
+// streams of 8 heads with 5 rows each, 8 pages 15.6 and 17.5, 12 pages 19.7 and
+// 17.8). Where the streams' key heads fit a whole
 // number of times, their pages are cut alike and no share crosses from one to
 // the next, which costs about 4 pages' time (its start and end once more);
 // ragged streams cross anyway. A share has at least two pages.
 bool share_plan(SharePlan& f, int batch, int heads_kv, int rows, int64_t pages, int slots) {
   const int64_t units = static_cast<int64_t>(batch) * heads_kv;
   f.rows = rows;
-  f.whole = pages <= 4;
+  f.whole = pages <= (batch > 1 ? 8 : 5);
   int64_t ctas = units;
   if (!f.whole) {
     ctas = slots;

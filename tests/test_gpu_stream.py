@@ -621,11 +621,19 @@ def test_the_compiled_calls_and_ctypes_give_the_same(binding, monkeypatch):
     x = _randn(g, 40, 6, 128).cuda()
     plan = binding.rope_plan()
     out = []
-    for calls in (None, binding._CtypesCalls):
-        if calls is not None:
-            monkeypatch.setattr(binding, "_calls", calls)
-            names = ("rope_fwd", "rope_bwd", "cache_write", "cache_attn_fwd")
-            monkeypatch.setattr(binding, "_fns", tuple(getattr(binding.load(), f"calibatt_{f}") for f in names))
+    fast, made = binding._load_fast(), []
+    assert fast is not binding._NoFast  # build() made them
+
+    class Fast:  # the compiled calls, counted
+        def __getattr__(self, name):
+            def call(*args):
+                done = getattr(fast, name)(*args)
+                made.append(done is not None)
+                return done
+            return call
+
+    for calls in (Fast(), binding._NoFast):
+        monkeypatch.setattr(binding, "_fast", calls)
         c = Cache(1, 2, 2, seed=5)
         q, k = binding.rope_fwd(x[:, :2], x[:, 2:4], plan, grid=(4, 5), start=(3, 1, 2))
         back, _ = binding.rope_bwd(q, None, plan, grid=(4, 5), start=(3, 1, 2))
@@ -634,6 +642,7 @@ def test_the_compiled_calls_and_ctypes_give_the_same(binding, monkeypatch):
         out.append([q, k, back, c.k.view(torch.uint8), c.ks, o, lse])
         with pytest.raises(TypeError):
             binding.cache_attn_fwd(q, *c.dev, _i32([0, 40]), _i32([100]), c.table, max_new=2.5)
+    assert made == [True] * 4 + [False]
     assert all(torch.equal(a, b) for a, b in zip(*out))
     assert binding.get_status() == 0
 

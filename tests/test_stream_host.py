@@ -77,18 +77,17 @@ def test_rope_refusals(binding, fn):
     assert call(plan=plan) == UNSUPPORTED
 
 
-@pytest.mark.parametrize("compiled", [True, False])
-def test_starts_beyond_32_bits_are_refused(binding, compiled):
-    calls = binding._load_calls() if compiled else binding._CtypesCalls
-    assert (calls is not binding._CtypesCalls) == compiled  # build() made the compiled calls
-    fn = binding._fns[0] if compiled else binding.load().calibatt_rope_fwd
-    plan = binding.rope_plan()
-    a = [ctypes.addressof(plan), FAKE, 512, 128, 4, None, 0, 0, 0, 0, None, 2, 5]
-    out = [FAKE + (1 << 24), 128, 1280, None, 0, 0, None]
-    assert calls.rope(fn, *a, 1 << 30, 0, -1 << 31, *out) == OK  # no tokens
-    for bad in (1 << 31, -(1 << 31) - 1, 1 << 40):
-        with pytest.raises(OverflowError):
-            calls.rope(fn, *a, 0, bad, 0, *out)
+def test_compiled_calls_leave_what_is_not_plain_to_the_binding(binding):
+    """Nothing is enqueued for tensors that are not CUDA tensors, or no tensors at all."""
+    fast = binding._load_fast()
+    assert fast is not binding._NoFast  # build() made them
+    x, plan = torch.zeros((3, 2, 128), dtype=torch.bfloat16), ctypes.addressof(binding.rope_plan())
+    for q in (x, None, 3, "q", [1.0], torch.nn.Parameter(x)):
+        assert fast.rope(True, q, None, plan, (1, 3), (0, 0, 0), None, None, None) is None
+        assert fast.cache_write(q, q, *[q] * 7, None) is None
+        assert fast.cache_attn(q, *[q] * 7, None, None, 0, None, None, None, None, True) is None
+    for wrong in ((), (True,), (x,) * 40):
+        assert fast.rope(*wrong) is None and fast.cache_write(*wrong) is None and fast.cache_attn(*wrong) is None
 
 
 def _write(binding, **kw):
