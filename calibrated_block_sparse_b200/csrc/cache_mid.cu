@@ -23,7 +23,7 @@
 // half (quarter) of the keys, with zeros for the others in P: all warps work on
 // a chain that is 2 (4) times as short. Numbers are held as in cache_tile.cu: fp16 operands without scales,
 // O in units of a reference value scale.
-// Bound by shared memory: a page's 32 KB land there, are read and written as
+// Bound, by this count, by shared memory: a page's 32 KB land there, are read and written as
 // 64 KB by the converters, and 96 KB are read as operands (Q's tile anew for
 // each page): 224 KB at 128 bytes a cycle are 1790 cycles, of the ~1850 that a
 // page takes with 25 rows. Measured: 16 streams of 20000 tokens, 40 query heads
