@@ -14,7 +14,7 @@
 // (queries, then keys) with them, so their cost is shared by all heads; reads
 // and writes are whole 256-byte rows, which makes the change between the
 // projections' token-major layout and the attention's head-major one free.
-// Measured on B200: 32760 tokens x 80 heads (1.34 GB) in 215 us, 96 % of the
+// Measured on B200: 32760 tokens x 80 heads (1.34 GB) in 211 us, 98 % of the
 // rate of a plain copy.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -32,7 +32,7 @@
 namespace calibatt {
 namespace {
 
-constexpr int kRopeThreads = 128;
+constexpr int kRopeThreads = 64;
 
 struct RopeView {
   const __nv_bfloat16* in;
@@ -116,8 +116,10 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
   const int h_end = min(heads, (static_cast<int>(blockIdx.y) + 1) * p.heads_per_cta);
   // kBatch heads are loaded at a time, and the next ones before these are
   // stored: the output may be the input's own memory, so the compiler cannot
-  // move a load over a store. The first loads run beside the sines.
-  constexpr int kBatch = kHalves ? 2 : 4;
+  // move a load over a store. The first loads run beside the sines. With half
+  // as many heads at a time 24.4 and 34.4 us instead of 21.6 and 32.6 (the
+  // sizes named at the launch), with more of them 24 and 32.
+  constexpr int kBatch = kHalves ? 4 : 8;
   constexpr int kChunks = kHalves ? 2 : 1;
   uint4 v[kBatch][kChunks], next[kBatch][kChunks];
   auto load = [&](int h0, uint4 (&w)[kBatch][kChunks]) {
@@ -272,11 +274,11 @@ int rope(const calibatt_rope_plan* plan, const void* q, int64_t q_ts, int64_t q_
   p.head_lanes = 1;
   while (p.head_lanes < slots && static_cast<int64_t>(slots / p.head_lanes) > n) p.head_lanes *= 2;
   const int64_t gx = (n * p.head_lanes + slots - 1) / slots;
-  // and the heads are spread over CTAs until there are 8 per SM: fewer leave
-  // SMs idle, more repeat the sines. Measured at 4680 tokens x 80 heads (192
-  // MB): 34.6 us with 8, 33.7 with 16, 36.7 with 32; at 7421 x 32 with halves
-  // paired: 24.5, 25.1, 31.0 (CTAs of 256 threads: 36.7 and 26.2 with 8).
-  const int64_t want = 8ll * sm_count();
+  // and the heads are spread over CTAs until there are 12 per SM: fewer leave
+  // SMs idle, more repeat the sines. Measured at 7421 tokens x 32 heads with
+  // halves paired: 21.6 us with 12, 22.7 with 16, 25.1 with 32; at 4680 x 80
+  // (192 MB): 32.6, 32.9, 33.5 (CTAs of 128 threads, 8 per SM: 23.0 and 33.1).
+  const int64_t want = 12ll * sm_count();
   int64_t gy = (want + gx - 1) / gx;
   const int64_t most = (all + p.head_lanes - 1) / p.head_lanes;
   if (gy > most) gy = most;
