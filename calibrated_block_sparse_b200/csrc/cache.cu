@@ -13,10 +13,11 @@
 // Bound by memory: 2 bytes read and 1 written per value. One CTA takes the
 // new tokens of one page and head (of K or of V): every value is held in
 // registers between the maximum and the rounding, so it is read once.
-// Measured on B200: 4 x 10800 tokens of 40 heads (1.03 GB) in 168 us, 94 % of
-// the rate of a plain copy; one 480p frame (1560 tokens, 48 MB) in 11 us, of
-// which 7.4 are its bytes and the rest the launch and one CTA's chain of load,
-// maximum, rounding and store.
+// Measured on B200: 4 x 10800 tokens of 40 heads (1.03 GB) in 159 us, the rate
+// of a plain copy (161 with four CTAs per SM instead of five, 179 with 512
+// threads per CTA); one 480p frame (1560 tokens, 48 MB) in 9.7 us, of which 7.4
+// are its bytes and the rest the launch and one CTA's chain of load, maximum,
+// rounding and store.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -83,7 +84,7 @@ __device__ __forceinline__ int page_exponent(float a) {
 
 __device__ __forceinline__ float exp2_int(int e) { return __int_as_float((e + 127) << 23); }
 
-__global__ void __launch_bounds__(kWriteThreads, 4) cache_write_kernel(const __grid_constant__ WriteParams p) {
+__global__ void __launch_bounds__(kWriteThreads, 5) cache_write_kernel(const __grid_constant__ WriteParams p) {
   const int which = blockIdx.x & 1, head = blockIdx.x >> 1;
   const int b = blockIdx.z;
   const Stream st = stream_of(p.tok_start, p.kv_len, b, p.n, p.table_stride);
