@@ -35,9 +35,9 @@
 //
 // Measured on B200: one token of 40 heads over 32760 cached (335 MB) in 60 us,
 // 86 % of the rate of a plain copy; 16 streams of 20000 tokens, 40 query heads
-// on 8, 3 tokens each (15 rows a key head, 437 MB) in 105 us, 64 %: there half of
-// the issue slots are taken, by chains of 8 warps per CTA that split every
-// weight into its parts.
+// on 8, 3 tokens each (15 rows a key head, 437 MB) in 102 us, 66 %: there each
+// page is a chain of score, vote, exponential, parts, store and product, and
+// four of them (two CTAs with two groups) run on an SM at a time.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -88,7 +88,7 @@ struct FewBarriers {
 struct FewLayout {
   static constexpr int kRingOff = 0;
   static constexpr int kQOff = kFewRing * kPageBytes;                  // Q^T's operand: rows of 128 channels, part by part
-  static constexpr int kPOff = kQOff + kQParts * few_cols(kFewRows, 1) * 128;  // P^T's: rows of 128 keys, two buffers
+  static constexpr int kPOff = kQOff + kQParts * few_cols(kFewRows, 1) * 128;  // P^T's two buffers
   static constexpr int kPBytes = few_cols(kFewRows, kPParts) * 128;
   static constexpr int kBarOff = kPOff + 2 * kPBytes;
   static constexpr int kDynSmem = kBarOff + static_cast<int>(sizeof(FewBarriers)) + 1024;
@@ -99,11 +99,24 @@ static_assert(2 * (FewLayout::kDynSmem + 1024) <= 233472, "shared memory budget"
 // Tensor memory: S^T in two buffers of 16 columns, O^T in up to 64.
 constexpr uint32_t kFewCols = 128, kSBuf = 32, kOCol = 64;
 
-// kind::f8f6f4, A e4m3, B e5m2, fp32 accumulation, M = 128; V is A with its
-// channels (M) contiguous.
-__host__ __device__ constexpr uint32_t idesc_f8(int N, bool a_mn_major) {
-  return (1u << 4) | (0u << 7) | (1u << 10) | ((a_mn_major ? 1u : 0u) << 15) | (static_cast<uint32_t>(N >> 3) << 17) |
+// kind::f8f6f4, A e4m3, B e5m2, fp32 accumulation, M = 128; with mn_major A (V)
+// has its channels and B (P^T) its rows contiguous.
+__host__ __device__ constexpr uint32_t idesc_f8(int N, bool mn_major) {
+  return (1u << 4) | (0u << 7) | (1u << 10) | ((mn_major ? 3u : 0u) << 15) | (static_cast<uint32_t>(N >> 3) << 17) |
          (8u << 24);
+}
+
+// P^T as operand B with its rows contiguous and no swizzle: planes of 16 rows,
+// a plane 16 bytes of each of the page's keys. A thread, which holds one key's
+// weights, then writes them 16 at a time and consecutive lanes write
+// consecutive bytes (byte by byte into rows of keys, 32 stores a page: 104 us
+// instead of 102 for 15 rows).
+constexpr int kPPlane = kPage * 16;
+__device__ __forceinline__ uint64_t desc_p(uint32_t saddr) {
+  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) |
+         static_cast<uint64_t>(128 >> 4) << 16 |      // from 8 keys to the next
+         static_cast<uint64_t>(kPPlane >> 4) << 32 |  // from 16 rows to the next
+         1ull << 46;
 }
 
 __device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
@@ -280,7 +293,7 @@ __global__ void __launch_bounds__(few_threads(G), 2)
       uint32_t stage = 0, phase = 0, turn = 0, stretch = 0;
       const uint64_t ring0 = smem_desc_sw128(sbase + L::kRingOff, 16, 1024);
       const uint64_t q0 = smem_desc_sw128(sbase + L::kQOff, 16, 1024);
-      const uint64_t p0 = smem_desc_sw128(sbase + L::kPOff, 16, 1024);
+      const uint64_t p0 = desc_p(sbase + L::kPOff);
       constexpr uint32_t kIdescS = idesc_f8(kQCols, false), kIdescO = idesc_f8(kPCols, true);
       bool ok = true;
       auto wait = [&](uint64_t* b, uint32_t parity) {
@@ -316,11 +329,11 @@ __global__ void __launch_bounds__(few_threads(G), 2)
           if (!(ok = wait(&bar.p_full[turn & 1], (turn >> 1) & 1))) break;
           if (!(ok = wait(&bar.full[stage], phase))) break;
           tc_fence_after();
-          // 4 steps of 32 keys: 32 rows of V (4 KB), 32 bytes of a row of P^T
+          // 4 steps of 32 keys: 32 rows of V (4 KB), 512 bytes of a plane of P^T
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             mma_f8(tmem + kOCol, ring0 + stage * (kPageBytes >> 4) + k * (4096 >> 4),
-                   p0 + (turn & 1) * (L::kPBytes >> 4) + k * 2, kIdescO, (i > 0 || k > 0) ? 1u : 0u);
+                   p0 + (turn & 1) * (L::kPBytes >> 4) + k * (512 >> 4), kIdescO, (i > 0 || k > 0) ? 1u : 0u);
           mma_commit(&bar.pv_done);
           if (i + 1 == s.count) mma_commit(&bar.o_full);
           ring_next();
@@ -485,28 +498,43 @@ __global__ void __launch_bounds__(few_threads(G), 2)
           }
           named_bar_sync(4 + g, 128);  // top has been read
         }
-        // P^T as operand B: row part * RG + r of a group, keys contiguous. An e5m2 value is
-        // the upper byte of an fp16 value, so the parts are that byte of the
-        // fp16 weight, of what remains, and so on, the last one rounded; two
-        // rows at a time.
-        uint8_t* pt = smem + L::kPOff + (turn & 1) * L::kPBytes + g * kPParts * RG * 128;
-        static_assert(G == 1 || kPParts * RG % 8 == 0, "a group's rows start a swizzle period");
+        // P^T's row part * RG + r of a group. An e5m2 value is the upper byte of
+        // an fp16 value, so the parts are that byte of the fp16 weight, of what
+        // remains, and so on, the last one rounded; two rows at a time.
+        constexpr int kOne = RG == 1;
+        uint32_t x[(RG + 1) / 2][kPParts];  // bytes 1 and 3: rows r and r + 1
 #pragma unroll
         for (int r = 0; r < RG; r += 2) {
-          constexpr int kOne = RG == 1;
           const float w0 = ex2_approx(d[r] + vref.log), w1 = kOne ? 0.f : ex2_approx(d[r + 1 - kOne] + vref.log);
           l[r] = __fmaf_rn(w0, vref.inv, l[r]);
           if (!kOne) l[r + 1 - kOne] = __fmaf_rn(w1, vref.inv, l[r + 1 - kOne]);
           __half2 rest = __floats2half2_rn(w0, w1);
 #pragma unroll
-          for (int part_i = 0; part_i < kPParts; ++part_i) {
-            uint32_t x = *reinterpret_cast<const uint32_t*>(&rest);
-            if (part_i + 1 == kPParts) x += 0x00800080u;
-            x &= 0xff00ff00u;
-            if (part_i + 1 < kPParts) rest = __hsub2(rest, *reinterpret_cast<const __half2*>(&x));
-            const int row = part_i * RG + r;
-            pt[row * 128 + (key ^ ((row & 7) << 4))] = static_cast<uint8_t>(x >> 8);
-            if (!kOne) pt[(row + 1) * 128 + (key ^ (((row + 1) & 7) << 4))] = static_cast<uint8_t>(x >> 24);
+          for (int i = 0; i < kPParts; ++i) {
+            uint32_t& y = x[r / 2][i];
+            y = *reinterpret_cast<const uint32_t*>(&rest);
+            if (i + 1 == kPParts) y += 0x00800080u;
+            if (i + 1 < kPParts) {
+              y &= 0xff00ff00u;
+              rest = __hsub2(rest, *reinterpret_cast<const __half2*>(&y));
+            }
+          }
+        }
+        uint8_t* pt = smem + L::kPOff + (turn & 1) * L::kPBytes + g * (kPParts * RG / 16) * kPPlane + key * 16;
+        if constexpr (kOne) {
+          const uint32_t y0 = __byte_perm(x[0][0], x[0][1], 0x51), y1 = __byte_perm(x[0][2], x[0][3], 0x51);
+          *reinterpret_cast<uint32_t*>(pt) = __byte_perm(y0, y1, 0x5410);
+        } else {
+          static_assert(kOne || RG == 4 || RG == 8, "16 rows and parts fill 16 bytes");
+#pragma unroll
+          for (int j = 0; j < kPParts * RG / 16; ++j) {
+            uint32_t y[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int row = j * 16 + e * 4, i = row / RG, r = row % RG / 2;
+              y[e] = __byte_perm(x[r][i], x[r + 1][i], 0x7531);
+            }
+            *reinterpret_cast<uint4*>(pt + j * kPPlane) = make_uint4(y[0], y[1], y[2], y[3]);
           }
         }
         fence_proxy_async();
