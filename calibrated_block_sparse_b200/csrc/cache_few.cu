@@ -28,8 +28,10 @@
 //   warp  1    MMA issuer: S^T of the next page before O^T of this one
 //   4 warps    softmax; thread = key of the page = TMEM lane of S^T, and
 //              channel = TMEM lane of O^T at the end
-// More than 8 rows are shared out to two such groups of 4 warps, 8 rows each:
-// the softmax of 16 rows in one thread is a chain of ~4000 cycles a page.
+// More than 4 rows are shared out to two such groups of 4 warps, 4 or 8 rows
+// each: the softmax of 16 rows in one thread is a chain of ~4000 cycles a page
+// (8 rows of 30000 keys, 2 streams: 34 us in one group, 32 in two; 15 rows in
+// four groups, whose registers do not fit: 110 us against 102).
 // The running maximum of a row moves only if it grew by more than 2^4, which a
 // page finds out with one vote of a group's warps.
 //
@@ -184,6 +186,7 @@ __global__ void __launch_bounds__(few_threads(G), 2)
                      const __grid_constant__ CacheAttnParams p, bool whole, float* part) {
   using L = FewLayout;
   constexpr int RB = RG * G, kAll = 128 * G;
+  static_assert(few_threads(G) / 32 <= sizeof(FewBarriers::walk) / sizeof(Walk), "a walk per warp");
   constexpr int kQCols = few_cols(RG * G, 1), kPCols = few_cols(RG * G, kPParts);
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -610,7 +613,7 @@ int launch_few_rows(const CUtensorMap& mk, const CUtensorMap& mv, const CacheAtt
                     float* ws, cudaStream_t stream) {
   if (plan.rows <= 1) return launch_few<SW, 1, 1>(mk, mv, p, plan, ws, stream);
   if (plan.rows <= 4) return launch_few<SW, 4, 1>(mk, mv, p, plan, ws, stream);
-  if (plan.rows <= 8) return launch_few<SW, 8, 1>(mk, mv, p, plan, ws, stream);
+  if (plan.rows <= 8) return launch_few<SW, 4, 2>(mk, mv, p, plan, ws, stream);
   return launch_few<SW, 8, 2>(mk, mv, p, plan, ws, stream);
 }
 
