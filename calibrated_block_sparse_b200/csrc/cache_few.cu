@@ -31,13 +31,13 @@
 // More than 4 rows are shared out to two such groups of 4 warps, 4 or 8 rows
 // each: the softmax of 16 rows in one thread is a chain of ~4000 cycles a page
 // (8 rows of 30000 keys, 2 streams: 34 us in one group, 32 in two; 15 rows in
-// four groups, whose registers do not fit: 110 us against 102).
+// four groups, whose registers do not fit: 8 us more than in two).
 // The running maximum of a row moves only if it grew by more than 2^4, which a
 // page finds out with one vote of a group's warps.
 //
 // Measured on B200: one token of 40 heads over 32760 cached (335 MB) in 60 us,
 // 86 % of the rate of a plain copy; 16 streams of 20000 tokens, 40 query heads
-// on 8, 3 tokens each (15 rows a key head, 437 MB) in 102 us, 66 %: there each
+// on 8, 3 tokens each (15 rows a key head, 437 MB) in 99 us, 68 %: there each
 // page is a chain of score, vote, exponential, parts, store and product, and
 // four of them (two CTAs with two groups) run on an SM at a time.
 #include <cuda.h>
@@ -111,8 +111,8 @@ __host__ __device__ constexpr uint32_t idesc_f8(int N, bool mn_major) {
 // P^T as operand B with its rows contiguous and no swizzle: planes of 16 rows,
 // a plane 16 bytes of each of the page's keys. A thread, which holds one key's
 // weights, then writes them 16 at a time and consecutive lanes write
-// consecutive bytes (byte by byte into rows of keys, 32 stores a page: 104 us
-// instead of 102 for 15 rows).
+// consecutive bytes (byte by byte into rows of keys, 32 stores a page: 2 us
+// more with 15 rows).
 constexpr int kPPlane = kPage * 16;
 __device__ __forceinline__ uint64_t desc_p(uint32_t saddr) {
   return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) |
@@ -214,25 +214,18 @@ __global__ void __launch_bounds__(few_threads(G), 2)
     fence_barrier_init();
   }
   if (warp == 1) tmem_alloc(&bar.tmem_base, kFewCols);
+  {  // the lists are on their way while the barriers and tensor memory are made
+    Walk walk;
+    walk.start(p, whole, lane);
+    if (lane == 0) bar.walk[warp] = walk;
+    __syncwarp();
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, bar.tmem_base, 0);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  // streams that do not fit are reported once
-  if (blockIdx.x == 0 && warp == 0)
-    for (int b = lane; b < p.batch; b += 32) {
-      const Stream st = stream_of(p.tok_start, p.kv_len, b, p.n, p.table_stride);
-      if (!stream_fits(p, st)) record_error(p.status, CALIBATT_ERR_CSR);
-    }
-
-  {
-    Walk walk;
-    walk.start(p, whole, lane);
-    if (lane == 0) bar.walk[warp] = walk;
-    __syncwarp();
-  }
   // for all lanes of a warp, or its lane 0 alone
   auto next_stretch = [&](Stretch& s, unsigned lanes) -> bool {
     Walk walk = bar.walk[warp];
@@ -284,7 +277,14 @@ __global__ void __launch_bounds__(few_threads(G), 2)
         }
       }
     }
+    // streams that do not fit are reported once
+    if (blockIdx.x == 0)
+      for (int b = lane; b < p.batch; b += 32) {
+        const Stream st = stream_of(p.tok_start, p.kv_len, b, p.n, p.table_stride);
+        if (!stream_fits(p, st)) record_error(p.status, CALIBATT_ERR_CSR);
+      }
     // no copy may still be landing when the CTA leaves
+    __syncwarp();
     if (lane == 0)
       for (int i = used > kFewRing ? used - kFewRing : 0; i < used; ++i) {
         volatile int never = 0;
