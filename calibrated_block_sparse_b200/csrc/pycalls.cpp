@@ -8,7 +8,7 @@
 // accepts every case and names every fault, makes it again.
 //
 // Measured: one token's rotation 10.8 -> 6.0 us a call, its cache write 8.9 ->
-// 4.1, its attention over 333 tokens 13.8 -> 10.2.
+// 4.1, its attention over 333 tokens 13.8 -> 10.2 (of which 8.2 were the kernel's).
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAFunctions.h>
