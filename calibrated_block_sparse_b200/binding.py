@@ -894,6 +894,8 @@ def rope_fwd(q, k, plan, grid=None, start=(0, 0, 0), pos=None, q_out=None, k_out
     any strides by their positions: a grid (H, W) whose first token is at
     `start` (time, height, width), or pos, int32 [n][3]. Returns them as
     [heads][n][128], the layout of the attention calls."""
+    if not isinstance(plan, RopePlan):
+        raise TypeError("plan must be a RopePlan")
     if stream is None:
         out = (_fast or _load_fast()).rope(True, q, k, ctypes.addressof(plan), grid, start, pos, q_out, k_out)
         if out is not None:
@@ -904,6 +906,8 @@ def rope_fwd(q, k, plan, grid=None, start=(0, 0, 0), pos=None, q_out=None, k_out
 def rope_bwd(dq_out, dk_out, plan, grid=None, start=(0, 0, 0), pos=None, dq=None, dk=None, stream=None):
     """Gradients of rope_fwd's inputs, [n][heads][128], from those of its
     outputs, [heads][n][128] of any strides (expanded ones too)."""
+    if not isinstance(plan, RopePlan):
+        raise TypeError("plan must be a RopePlan")
     if stream is None:
         out = (_fast or _load_fast()).rope(False, dq_out, dk_out, ctypes.addressof(plan), grid, start, pos, dq, dk)
         if out is not None:

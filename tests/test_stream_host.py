@@ -146,6 +146,10 @@ def test_binding_wants_cuda_tensors(binding):
     x = torch.zeros((3, 2, 128), dtype=torch.bfloat16)
     with pytest.raises(TypeError):
         binding.rope_fwd(x, x, binding.rope_plan(), grid=(1, 3))
+    for call in (binding.rope_fwd, binding.rope_bwd):
+        for plan in (None, 7, ctypes.c_int32(1)):
+            with pytest.raises(TypeError):
+                call(x, x, plan, grid=(1, 3))
     with pytest.raises(TypeError):
         binding.cache_write(x, x, None, None, None, None, None, None, None)
     with pytest.raises(TypeError):
