@@ -616,6 +616,24 @@ def test_frame_streams_match_the_calls_and_the_oracle(binding, so):
     assert st.lengths == [0, done[1]] and st.free_pages > free
 
 
+def test_dropped_pages_are_used_anew(binding):
+    """A stream on pages that another one has left, at far larger scales, gives what it gives on fresh pages."""
+    from calibrated_block_sparse_b200.stream import FrameStreams
+    g = _gen(92)
+    made = [FrameStreams(batch=2, heads=2, kv_heads=2, H=5, W=6, pages=5) for _ in range(2)]
+    big = (_randn(g, 530, 6, 128) * 1000).cuda()
+    made[0].step(big[:, :2], big[:, 2:4], big[:, 4:], new=[330, 200])
+    made[0].drop(0)
+    made[0].drop(1)
+    for new in ([140, 0], [1, 257], [30, 2]):
+        x = _randn(g, sum(new), 6, 128).cuda()
+        got = [st.step(x[:, :2], x[:, 2:4], x[:, 4:], new=new, causal_unit=30) for st in made]
+        for a, b in zip(*got):
+            assert torch.equal(a, b)
+    assert made[0].free_pages == made[1].free_pages == 0
+    assert binding.get_status() == 0
+
+
 def test_the_compiled_calls_and_ctypes_give_the_same(binding, monkeypatch):
     g = _gen(61)
     x = _randn(g, 40, 6, 128).cuda()
