@@ -599,16 +599,15 @@ __global__ void __launch_bounds__(kMidThreads, 1)
           l_run = l_run * alpha + ((s01.x + s01.y) + (s23.x + s23.y)) * vref.inv;
         }
       }
-      // the stretch's products are complete, the other slot's too, for the
-      // exchange below uses Q's tile
-      if (active) wait_warp(&bar.o_full[s], n_o[s] & 1);
-      if (active) ++n_o[s];
-      if (second) {
-        wait_warp(&bar.o_full[s ^ 1], n_o[s ^ 1] & 1);
-        ++n_o[s ^ 1];
-      } else if (s == 1) {
-        ++n_o[0];  // slot 0's alone
-      }
+      // The stretch's products are complete, of both slots that have some: the
+      // exchange below uses Q's tile. A slot without pages waits for the other
+      // one all the same, which is still writing Q there or multiplying it.
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+        if (x == 0 || second) {
+          wait_warp(&bar.o_full[x], n_o[x] & 1);
+          ++n_o[x];
+        }
       tc_fence_after();
       const bool done = ok && *abort_flag == 0;
       // A row's shares of the stretch, two slots by KS copies, are added up

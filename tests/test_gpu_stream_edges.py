@@ -1,0 +1,57 @@
+"""Streaming operators on the GPU where an ordering of warps, a border of the
+number formats or an unusual call decides the result."""
+import numpy as np
+import pytest
+import torch
+
+from gpu_util import bf16_to_f64
+from test_gpu_stream import Cache, _attn_close, _gen, _i32, _p_err, _randn, _starts, binding, so  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------------------- repeats
+
+@pytest.mark.parametrize("rows", [17, 32, 33, 64, 65, 128])
+@pytest.mark.parametrize("lens", [[1], [128], [100, 128, 1], [300], [129, 2000, 60], [700, 700]])
+def test_mid_rows_repeat_bit_for_bit(binding, so, rows, lens):
+    """Stretches of one page, where one of the two slots has no work, and of several: the same call many times."""
+    g = _gen(rows + sum(lens))
+    hk = 3
+    c = Cache(len(lens), hk, -(-max(lens) // 128), seed=rows)
+    new = [rows] * len(lens)
+    q = _randn(g, hk, sum(new), 128) * 0.5
+    args = (q.cuda(), *c.dev, _i32(_starts(new)), _i32(lens), c.table)
+    kw = dict(max_new=rows, max_kv=max(lens), scale=0.05)
+    o, lse = binding.cache_attn_fwd(*args, **kw)
+    ref = so.cache_attention(bf16_to_f64(q), c.k_h, c.v_h, c.ks_h, c.vs_h, _starts(new), lens, c.table_h, 0.05)
+    _attn_close(o, lse, ref, q, c, lens, 0.05, _p_err(new, hk, hk))
+    outs = [binding.cache_attn_fwd(*args, **kw) for _ in range(300)]
+    assert all(torch.equal(o, a) and torch.equal(lse, b) for a, b in outs)
+    # shares that leave single pages: the plan is made for another length, and every CTA gets a page or two
+    if max(lens) > 128:
+        kw["max_kv"] = 128 * 40
+        many = [binding.cache_attn_fwd(*args, **kw) for _ in range(100)]
+        assert all(torch.equal(many[0][0], a) and torch.equal(many[0][1], b) for a, b in many)
+        _attn_close(*many[0], ref, q, c, lens, 0.05, _p_err(new, hk, hk))
+    assert binding.get_status() == 0
+
+
+@pytest.mark.parametrize("rows", [(17, 1), (40, 33), (90, 128)])
+def test_mid_rows_at_once_with_others(binding, rows):
+    """One-page stretches on two streams at the same time, each with outputs of its own: as one after the other."""
+    g = _gen(sum(rows))
+    c = Cache(4, 8, 2, seed=9)
+    lens, calls = _i32([100, 128, 256, 129]), []
+    for m in rows:
+        q = (_randn(g, 8, 4 * m, 128) * 0.5).cuda()
+        calls.append((q, *c.dev, _i32(_starts([m] * 4)), lens, c.table))
+    want = [binding.cache_attn_fwd(*a, max_new=m) for a, m in zip(calls, rows)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in rows]
+    for _ in range(50):
+        got = [binding.cache_attn_fwd(*a, max_new=m, stream=st) for a, m, st in zip(calls, rows, streams)]
+        torch.cuda.synchronize()
+        for x, y in zip(want, got):
+            assert torch.equal(x[0], y[0]) and torch.equal(x[1], y[1])
+    assert binding.get_status() == 0
