@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(kWriteThreads, 5) cache_write_kernel(const __g
   if (st.n_new == 0) return;
   const int begin = st.len - st.n_new;  // position of the first new token
   const int pg = begin / kPage + static_cast<int>(blockIdx.y);
-  if (pg * kPage >= st.len) return;
+  if (static_cast<int64_t>(pg) * kPage >= st.len) return;  // pages that max_new allows for may pass 32 bits
   const int page = __ldg(p.table + static_cast<int64_t>(b) * p.table_stride + pg);
   if (page < 0 || page >= p.n_pages) {
     if (threadIdx.x == 0) record_error(p.status, CALIBATT_ERR_CSR);

@@ -14,6 +14,9 @@
 namespace calibatt {
 
 constexpr int kPage = 128;  // tokens per cache page
+// Tokens of a stream: the kernels round a length up to whole pages and look a
+// page ahead in 32 bits.
+constexpr int kMaxTokens = INT32_MAX - 2 * kPage + 1;
 
 // New tokens [t0, t0 + n_new) of stream b and the tokens its cache holds.
 struct Stream {
@@ -27,7 +30,8 @@ __device__ __forceinline__ Stream stream_of(const int32_t* tok_start, const int3
   s.t0 = __ldg(tok_start + b);
   const int t1 = __ldg(tok_start + b + 1);
   s.len = __ldg(kv_len + b);
-  s.bad = s.t0 < 0 || t1 < s.t0 || t1 > n || s.len < 0 || s.len > static_cast<int64_t>(table_stride) * kPage;
+  s.bad = s.t0 < 0 || t1 < s.t0 || t1 > n || s.len < 0 || s.len > kMaxTokens ||
+          s.len > static_cast<int64_t>(table_stride) * kPage;
   s.n_new = t1 - s.t0;
   return s;
 }

@@ -369,7 +369,7 @@ int calibatt_rope_bwd(const calibatt_rope_plan* plan, const calibatt_bf16* dq_ou
  * they were changed; the host gives bounds (max_new: new tokens of one stream;
  * max_kv: cached tokens of one stream). A stream whose lists do not fit (a
  * negative or decreasing start, more than max_new or n tokens, more cached
- * tokens than its table names) is left out and a page outside [0, n_pages) is
+ * tokens than its table names or than 2^31 - 256) is left out and a page outside [0, n_pages) is
  * skipped; both are reported as CALIBATT_ERR_CSR through calibatt_get_status. */
 
 /* Appends the new tokens' keys and values to the cache. Per page and head,

@@ -55,3 +55,58 @@ def test_mid_rows_at_once_with_others(binding, rows):
         for x, y in zip(want, got):
             assert torch.equal(x[0], y[0]) and torch.equal(x[1], y[1])
     assert binding.get_status() == 0
+
+
+# ---------------------------------------------------------------------------- lengths next to 2^31
+
+MOST = 2 ** 31 - 256  # tokens of one stream
+
+
+@pytest.fixture(scope="module")
+def longest():
+    """A pool of two pages, named by a table that is wide enough for 2^31 tokens."""
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    k8 = torch.zeros((2, 1, 128, 128), dtype=torch.uint8, device="cuda")
+    v8 = torch.full_like(k8, 0x38)  # 1.0
+    scales = [torch.ones((2, 1), device="cuda") for _ in range(2)]
+    return k8, v8, *scales, torch.zeros((1, 1 << 24), dtype=torch.int32, device="cuda")
+
+
+def test_writing_next_to_2_31_tokens(binding):
+    """One token at the last position of a stream, beside another stream with so many new ones that the grid's pages
+    would reach behind 2^31 tokens for the first."""
+    n = 1 + 599
+    pool = [torch.zeros((8, 1, 128, 128), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    cache = pool + [torch.ones((8, 1), device="cuda") for _ in range(2)]
+    table = torch.zeros((2, 1 << 24), dtype=torch.int32, device="cuda")
+    table[0, MOST // 128 - 1] = 1
+    table[1, :5] = torch.arange(2, 7, dtype=torch.int32)
+    x = torch.full((n, 1, 128), 2.0, dtype=torch.bfloat16, device="cuda")
+    binding.cache_write(x, x, *cache, _i32([0, 1, n]), _i32([MOST, n - 1]), table, max_new=n - 1)
+    assert binding.get_status() == 0
+    for c, s in (cache[::2], cache[1::2]):
+        value = c.view(torch.float8_e4m3fn).float()[:, 0, :, 0] * s
+        want = torch.zeros((8, 128), device="cuda")
+        want[1, 127] = 2.0
+        want[2:7].view(-1)[:n - 1] = 2.0
+        assert torch.equal(value, want)
+    for much in (MOST + 1, 2 ** 31 - 128, 2 ** 31 - 1):
+        before = [y.clone() for y in cache]
+        binding.cache_write(x[:1], x[:1], *cache, _i32([0, 1, 1]), _i32([much, 0]), table)
+        assert binding.get_status() == -2
+        assert all(torch.equal(y, z) for y, z in zip(cache, before))
+
+
+@pytest.mark.parametrize("rows", [1, 20, 140])
+def test_attention_next_to_2_31_tokens(binding, longest, rows):
+    """Equal scores and values of 1: o = 1, lse = ln of the length (21.5, to a few steps of 2^-19 in fp32)."""
+    *cache, table = longest
+    q = torch.ones((1, rows, 128), dtype=torch.bfloat16, device="cuda")
+    o, lse = binding.cache_attn_fwd(q, *cache, _i32([0, rows]), _i32([MOST]), table, max_kv=MOST)
+    assert binding.get_status() == 0
+    assert torch.all(o == 1.0) and torch.all((lse.double() - np.log(MOST)).abs() < 2.0 ** -16)
+    for much in (MOST + 1, 2 ** 31 - 1):
+        o.fill_(7.0)
+        binding.cache_attn_fwd(q, *cache, _i32([0, rows]), _i32([much]), table, max_kv=MOST, o=o)
+        assert binding.get_status() == -2 and torch.all(o == 7.0)
