@@ -129,7 +129,11 @@ struct VRef {
       ref = now;
       ref_inv = 1.f / ref;
     }
-    const float f = vs * ref_inv;
+    // At 2^-40 P, 2^14 times that at most (kLog and a stale maximum), rounds to
+    // zero already: under half of fp16's smallest value. Further down it would
+    // stay so, but f and its reciprocal would leave fp32's range and make the
+    // sum of the weights NaN.
+    const float f = fmaxf(vs * ref_inv, 9.094947017729282e-13f);
     float l2, r;
     asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(l2) : "f"(f));
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(f));

@@ -407,7 +407,9 @@ size_t calibatt_cache_attn_workspace_size(int batch, int heads_q, int heads_kv, 
  *   ws   : device scratch of calibatt_cache_attn_workspace_size bytes, 16-byte
  *          aligned; calls that may run at the same time need one each
  * Rows of tokens that belong to no stream are not written. New tokens may
- * outnumber the cached ones when causal_unit = 0. */
+ * outnumber the cached ones when causal_unit = 0. Outputs are summed in units
+ * of the largest value scales met: pages whose value scale is less than 2^-70
+ * of another page's may count as zeros in o (lse counts them in full). */
 int calibatt_cache_attn_fwd(const calibatt_bf16* q, int heads_q, int heads_kv, int n, int d, float scale,
                             int causal_unit, const int32_t* tok_start, const int32_t* kv_len, int batch, int max_new,
                             int max_kv, const int32_t* table, int table_stride, int n_pages, const uint8_t* k8,

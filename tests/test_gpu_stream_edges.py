@@ -110,3 +110,32 @@ def test_attention_next_to_2_31_tokens(binding, longest, rows):
         o.fill_(7.0)
         binding.cache_attn_fwd(q, *cache, _i32([0, rows]), _i32([much]), table, max_kv=MOST, o=o)
         assert binding.get_status() == -2 and torch.all(o == 7.0)
+
+
+# ---------------------------------------------------------------------------- borders of the value scales
+
+ROWS = [1, 6, 15, 20, 50, 100, 140, 300]  # every kernel and variant
+
+
+@pytest.mark.parametrize("rows", ROWS)
+@pytest.mark.parametrize("exps", [(-117, 100, -8), (100, -117, -8), (-8, 100, -117), (100, -8, -117),
+                                  (-117, -117, 60), (110, 0, -110), (20, -100, 20), (30, -12, -60)])
+@pytest.mark.parametrize("unit", [0, 1])
+def test_value_scales_far_apart(binding, so, rows, exps, unit):
+    """Pages whose value scales lie up to 2^236 apart (a page of zeros has 2^-117): the weights of all of them count
+    in the sum, and no output becomes NaN or infinite."""
+    lens = 384
+    c = Cache(1, 1, 3, seed=rows)
+    c.vs_h[c.table_h[0], 0] = [2.0 ** e for e in exps]
+    for page, e in zip(c.table_h[0], exps):
+        if e == -117:
+            c.v_h[page] = 0
+    c.up()
+    q = _randn(_gen(rows), 1, rows, 128)
+    ref = so.cache_attention(bf16_to_f64(q), c.k_h, c.v_h, c.ks_h, c.vs_h, [0, rows], [lens], c.table_h, 0.05, unit)
+    args = (q.cuda(), *c.dev, _i32([0, rows]), _i32([lens]), c.table)
+    for max_kv in (lens, 4096):  # in one piece, and split
+        o, lse = binding.cache_attn_fwd(*args, max_kv=max_kv, causal_unit=unit, scale=0.05)
+        assert torch.isfinite(o).all() and torch.isfinite(lse).all()
+        _attn_close(o, lse, ref, q, c, [lens], 0.05, _p_err([rows], 1, 1))
+    assert binding.get_status() == 0
