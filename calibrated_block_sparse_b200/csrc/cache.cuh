@@ -227,21 +227,22 @@ struct PageWindow {
   }
 };
 
-// Normalises and stores a row's four channels of a lane; no key seen: 0 and -inf.
+// Stores a row's four channels of a lane; no key seen: 0 and -inf.
 __device__ __forceinline__ void store_row(const CacheAttnParams& p, int64_t at, int lane, float mx, float sum,
                                           const float4& o) {
   const bool some = sum != 0.f;
-  const float inv = some ? 1.f / sum : 0.f;
-  uint2 w = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+  uint2 w = make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
   if (!some) w = make_uint2(0, 0);
   *reinterpret_cast<uint2*>(p.o + at * 128 + lane * 4) = w;
   if (p.lse && lane == 0) p.lse[at] = some ? (mx + log2f(sum)) * 0.6931471805599453f : -INFINITY;
 }
 
 // Joins one row's partial results (a warp): those of parts c0 .. c1 - 1 for
-// which `slot` gives an address, each [rows][128] outputs, then maximum (log2
-// units) and sum per row. The lanes fetch 32 parts' maxima and sums at a time;
-// the outputs are then loaded independently of each other.
+// which `slot` gives an address, each [rows][128] outputs, divided by their
+// weights' sum, then maximum (log2 units) and sum per row. The lanes fetch 32
+// parts' maxima and sums at a time; the outputs are then loaded independently
+// of each other. What is kept is always a mean of values, so it fits fp32
+// where their sum might not.
 template <class Slot>
 __device__ __forceinline__ void join_row(const CacheAttnParams& p, int64_t at, int lane, int c0, int c1,
                                          const Slot& slot, int64_t row, int64_t rows) {
@@ -255,12 +256,14 @@ __device__ __forceinline__ void join_row(const CacheAttnParams& p, int64_t at, i
 #pragma unroll
     for (int i = 16; i > 0; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
     const float now = fmaxf(mx, top), use = now == -INFINITY ? 0.f : now;
-    const float keep = ex2_approx(mx - use), w = ex2_approx(ml.x - use);
+    const float before = sum * ex2_approx(mx - use), part = ml.y * ex2_approx(ml.x - use);
     mx = now;
-    float add = ml.y * w;
+    float add = part;
 #pragma unroll
     for (int i = 16; i > 0; i >>= 1) add += __shfl_xor_sync(0xffffffffu, add, i);
-    sum = sum * keep + add;
+    sum = before + add;
+    const float inv = sum != 0.f ? 1.f / sum : 0.f;
+    const float keep = before * inv, w = part * inv;
     o.x *= keep;
     o.y *= keep;
     o.z *= keep;

@@ -4,7 +4,7 @@
 // Like with fewer rows the cache's pages are one list, stream by stream, key
 // head by key head, cut into equal shares whatever the streams' lengths are,
 // one CTA per SM. A stretch of a share that is not all of its stream's pages
-// leaves maximum, sum and unnormalised output in the workspace, and
+// leaves maximum, sum and output in the workspace, and
 // cache_join_kernel joins them.
 //
 // CTA (512 threads, persistent), one tile of 128 / KS query rows, KS times over:
@@ -625,9 +625,10 @@ __global__ void __launch_bounds__(kMidThreads, 1)
         const float2 x = ml[i * kRows + row];
         l += x.y * ex2_approx(x.x - use);
       }
-      const float factor = ex2_approx(m_run - use) * vref.unit();
       const bool some = l != 0.f;
-      const float inv = some ? 1.f / l : 0.f;
+      // divided by the sum before the unit is multiplied in: a mean of values
+      // fits fp32 where their sum might not
+      const float factor = ex2_approx(m_run - use) * (some ? 1.f / l : 0.f), unit = vref.unit();
       const bool complete = np == seg.pages;
       float* out = part_of(part, blockIdx.x, seg.pg0 > 0, kMidRows);
       if (done && row_valid && share == 0) {
@@ -646,7 +647,7 @@ __global__ void __launch_bounds__(kMidThreads, 1)
           uint32_t o[32];
           tmem_ld32_wait(oc + cc * 32, o);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) joined[(share * 32 + e) * kRows + row] = __uint_as_float(o[e]) * factor;
+          for (int e = 0; e < 32; ++e) joined[(share * 32 + e) * kRows + row] = __uint_as_float(o[e]) * factor * unit;
         }
         named_bar_sync(1, 256);
         if (!done || !row_valid) continue;
@@ -685,8 +686,7 @@ __global__ void __launch_bounds__(kMidThreads, 1)
           uint2* dst = reinterpret_cast<uint2*>(p.o + at * 128 + ch);
 #pragma unroll
           for (int e = 0; e < kCh / 4; ++e)
-            dst[e] = some ? make_uint2(pack_bf16x2(x[4 * e] * inv, x[4 * e + 1] * inv),
-                                       pack_bf16x2(x[4 * e + 2] * inv, x[4 * e + 3] * inv))
+            dst[e] = some ? make_uint2(pack_bf16x2(x[4 * e], x[4 * e + 1]), pack_bf16x2(x[4 * e + 2], x[4 * e + 3]))
                           : make_uint2(0, 0);
         }
       }

@@ -119,7 +119,8 @@ ROWS = [1, 6, 15, 20, 50, 100, 140, 300]  # every kernel and variant
 
 @pytest.mark.parametrize("rows", ROWS)
 @pytest.mark.parametrize("exps", [(-117, 100, -8), (100, -117, -8), (-8, 100, -117), (100, -8, -117),
-                                  (-117, -117, 60), (110, 0, -110), (20, -100, 20), (30, -12, -60)])
+                                  (-117, -117, 60), (110, 0, -110), (20, -100, 20), (30, -12, -60),
+                                  (119, -117, -117), (119, 119, 119)])
 @pytest.mark.parametrize("unit", [0, 1])
 def test_value_scales_far_apart(binding, so, rows, exps, unit):
     """Pages whose value scales lie up to 2^236 apart (a page of zeros has 2^-117): the weights of all of them count
@@ -138,4 +139,21 @@ def test_value_scales_far_apart(binding, so, rows, exps, unit):
         o, lse = binding.cache_attn_fwd(*args, max_kv=max_kv, causal_unit=unit, scale=0.05)
         assert torch.isfinite(o).all() and torch.isfinite(lse).all()
         _attn_close(o, lse, ref, q, c, [lens], 0.05, _p_err([rows], 1, 1))
+    assert binding.get_status() == 0
+
+
+@pytest.mark.parametrize("rows", ROWS)
+def test_values_next_to_the_largest(binding, rows):
+    """1000 values of 2^127 and of -2^127 each: their mean is inside bf16's range, their sum is not inside fp32's."""
+    x = torch.full((1000, 1, 128), 2.0 ** 127, dtype=torch.bfloat16, device="cuda")
+    x[:, :, 1::2] = -2.0 ** 127
+    k8, v8 = (torch.zeros((8, 1, 128, 128), dtype=torch.float8_e4m3fn, device="cuda") for _ in range(2))
+    ks, vs = (torch.ones((8, 1), device="cuda") for _ in range(2))
+    table = torch.arange(8, dtype=torch.int32, device="cuda")[None]
+    binding.cache_write(torch.zeros_like(x), x, k8, v8, ks, vs, _i32([0, 1000]), _i32([1000]), table)
+    q = _randn(_gen(1), 1, rows, 128).cuda()
+    for max_kv in (128, 1000, 1 << 16):
+        o, lse = binding.cache_attn_fwd(q, k8, v8, ks, vs, _i32([0, rows]), _i32([1000]), table, max_kv=max_kv)
+        assert torch.equal(o, x[:1, 0].expand(1, rows, 128))
+        assert torch.all((lse - np.log(1000)).abs() < 1e-5)
     assert binding.get_status() == 0
