@@ -141,7 +141,14 @@ struct VRef {
     inv = kUnit * r;
     return ratio;
   }
-  __device__ __forceinline__ float unit() const { return ref * kUnit; }
+  // Outputs leave the units of the reference before they are divided by their
+  // weights' sum, and a sum of values next to the largest leaves fp32's range
+  // although their mean is inside it. From a reference of 1 on, outputs and sums
+  // are therefore kept times 2^-40 (2^31 keys with weights up to 2^8, twice)
+  // and the maximum is 40 more: the same row in other units.
+  __device__ __forceinline__ float damp() const { return ref > 1.f ? 9.094947017729282e-13f : 1.f; }
+  __device__ __forceinline__ float raise() const { return ref > 1.f ? 40.f : 0.f; }
+  __device__ __forceinline__ float unit() const { return ref * kUnit * damp(); }
 };
 
 // Tile t of the ring's order -> (V?, page of the range): K0 V0 K1 V1 ..., or
@@ -227,22 +234,21 @@ struct PageWindow {
   }
 };
 
-// Stores a row's four channels of a lane; no key seen: 0 and -inf.
+// Normalises and stores a row's four channels of a lane; no key seen: 0 and -inf.
 __device__ __forceinline__ void store_row(const CacheAttnParams& p, int64_t at, int lane, float mx, float sum,
                                           const float4& o) {
   const bool some = sum != 0.f;
-  uint2 w = make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+  const float inv = some ? 1.f / sum : 0.f;
+  uint2 w = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
   if (!some) w = make_uint2(0, 0);
   *reinterpret_cast<uint2*>(p.o + at * 128 + lane * 4) = w;
   if (p.lse && lane == 0) p.lse[at] = some ? (mx + log2f(sum)) * 0.6931471805599453f : -INFINITY;
 }
 
 // Joins one row's partial results (a warp): those of parts c0 .. c1 - 1 for
-// which `slot` gives an address, each [rows][128] outputs, divided by their
-// weights' sum, then maximum (log2 units) and sum per row. The lanes fetch 32
-// parts' maxima and sums at a time; the outputs are then loaded independently
-// of each other. What is kept is always a mean of values, so it fits fp32
-// where their sum might not.
+// which `slot` gives an address, each [rows][128] outputs, then maximum (log2
+// units) and sum per row. The lanes fetch 32 parts' maxima and sums at a time;
+// the outputs are then loaded independently of each other.
 template <class Slot>
 __device__ __forceinline__ void join_row(const CacheAttnParams& p, int64_t at, int lane, int c0, int c1,
                                          const Slot& slot, int64_t row, int64_t rows) {
@@ -256,14 +262,12 @@ __device__ __forceinline__ void join_row(const CacheAttnParams& p, int64_t at, i
 #pragma unroll
     for (int i = 16; i > 0; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
     const float now = fmaxf(mx, top), use = now == -INFINITY ? 0.f : now;
-    const float before = sum * ex2_approx(mx - use), part = ml.y * ex2_approx(ml.x - use);
+    const float keep = ex2_approx(mx - use), w = ex2_approx(ml.x - use);
     mx = now;
-    float add = part;
+    float add = ml.y * w;
 #pragma unroll
     for (int i = 16; i > 0; i >>= 1) add += __shfl_xor_sync(0xffffffffu, add, i);
-    sum = before + add;
-    const float inv = sum != 0.f ? 1.f / sum : 0.f;
-    const float keep = before * inv, w = part * inv;
+    sum = sum * keep + add;
     o.x *= keep;
     o.y *= keep;
     o.z *= keep;

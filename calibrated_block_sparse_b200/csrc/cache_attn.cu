@@ -7,8 +7,8 @@
 // for all of them: up to 16 rows by cache_few.cu, bound by the cache's bytes,
 // up to 128 by cache_mid.cu, more by cache_tile.cu, bound by the tensor core
 // and the softmax beside it. All split the cache over CTAs along its length; a
-// part leaves its maximum, sum and output in a workspace, and a second kernel
-// joins them. This file holds the entry points, the plan
+// part leaves its running maximum, sum and unnormalised output in a workspace,
+// and a second kernel joins them. This file holds the entry points, the plan
 // and the join.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

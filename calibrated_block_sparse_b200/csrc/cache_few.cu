@@ -5,7 +5,7 @@
 // key head by key head, cut into equal shares: two CTAs per SM, whatever the
 // streams' lengths are (they are read on the device), so no SM waits for a
 // long stream. A stretch of a share that is not all of its stream's pages
-// leaves maximum, sum and output in the workspace, and
+// leaves maximum, sum and unnormalised output in the workspace, and
 // cache_join_kernel joins them.
 //
 // The tensor core multiplies the cache's bytes as they are: a page is the
@@ -554,7 +554,7 @@ __global__ void __launch_bounds__(few_threads(G), 2)
       for (int r = 0; r < RG; ++r) {
 #pragma unroll
         for (int x = 16; x > 0; x >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], x);
-        if (lane == 0) bar.sum[quarter][r0 + r] = l[r];
+        if (lane == 0) bar.sum[quarter][r0 + r] = l[r] * vref.damp();
       }
       named_bar_sync(1, kAll);
       const bool complete = s.count == s.pages;
@@ -566,18 +566,18 @@ __global__ void __launch_bounds__(few_threads(G), 2)
           const int r = r0 + rr;
           if (r >= rows) break;
           const float sum = (bar.sum[0][r] + bar.sum[1][r]) + (bar.sum[2][r] + bar.sum[3][r]);
-          const bool some = sum != 0.f;
-          // the values' mean fits fp32 where their sum might not
-          float x = some ? o[rr] * (1.f / sum) * vref.unit() : 0.f;
-          if (some && patch && stretch_nan(p, s, bar.limit[r], least, key)) x = NAN;
+          float x = o[rr] * vref.unit();
+          if (patch && stretch_nan(p, s, bar.limit[r], least, key)) x = NAN;
           if (complete) {
             const int64_t at = static_cast<int64_t>(s.head * p.group + r % p.group) * p.n + s.st.t0 + r / p.group;
-            p.o[at * 128 + key] = __float2bfloat16_rn(x);
-            if (p.lse && key == 0) p.lse[at] = some ? (m[rr] + log2f(sum)) * kLn2 : -INFINITY;
+            const bool some = sum != 0.f;
+            p.o[at * 128 + key] = __float2bfloat16_rn(some ? x / sum : 0.f);
+            if (p.lse && key == 0) p.lse[at] = some ? (m[rr] + vref.raise() + log2f(sum)) * kLn2 : -INFINITY;
           } else {
-            out[r * 128 + key] = x;
+            out[r * 128 + key] = sum != 0.f ? x : 0.f;
             if (key == 0)
-              *reinterpret_cast<float2*>(out + kFewRows * 128 + 2 * r) = make_float2(some ? m[rr] : -INFINITY, sum);
+              *reinterpret_cast<float2*>(out + kFewRows * 128 + 2 * r) =
+                  make_float2(sum != 0.f ? m[rr] + vref.raise() : -INFINITY, sum);
           }
         }
       }

@@ -122,8 +122,7 @@ struct Walk {
 
 // A stretch that is not all of its stream's pages: a CTA has two at most, its
 // first, which begins inside the stream's pages, and its last, which begins
-// with them. Per row 128 outputs, divided by their weights' sum, then maximum
-// (log2 units) and sum of all rows.
+// with them. Per row 128 outputs, then maximum (log2 units) and sum of all rows.
 __host__ __device__ constexpr int part_floats(int rows) { return rows * 130; }
 __device__ __forceinline__ float* part_of(float* part, int cta, bool inside, int rows) {
   return part + (2 * static_cast<int64_t>(cta) + (inside ? 0 : 1)) * part_floats(rows);

@@ -4,7 +4,7 @@
 // Like with fewer rows the cache's pages are one list, stream by stream, key
 // head by key head, cut into equal shares whatever the streams' lengths are,
 // one CTA per SM. A stretch of a share that is not all of its stream's pages
-// leaves maximum, sum and output in the workspace, and
+// leaves maximum, sum and unnormalised output in the workspace, and
 // cache_join_kernel joins them.
 //
 // CTA (512 threads, persistent), one tile of 128 / KS query rows, KS times over:
@@ -77,6 +77,7 @@ struct Segment {
   int pg0, np;
   int pages;      // of the stream
   int number;     // of the stretch in its share
+  int seconds;    // stretches of several pages before it
 };
 
 struct MidLayout {
@@ -274,7 +275,7 @@ __global__ void __launch_bounds__(kMidThreads, 1)
           const Stream st = stream_of(p.tok_start, p.kv_len, b, p.n, p.table_stride);
           if (!stream_fits(p, st)) record_error(p.status, CALIBATT_ERR_CSR);
         }
-      int k = 0;
+      int k = 0, seconds = 0;
       bool ok = true;
       Walk walk;
       walk.start(p, whole, lane);
@@ -298,10 +299,12 @@ __global__ void __launch_bounds__(kMidThreads, 1)
               seg.np = s.count;
               seg.pages = s.pages;
               seg.number = k;
+              seg.seconds = seconds;
             }
             mbar_arrive(&bar.seg_full[k % kSegs]);
           }
         }
+        if (more && s.count > 1) ++seconds;
         ok = __shfl_sync(0xffffffffu, ok, 0);
       }
     } else if (warp == 13) {
@@ -441,7 +444,7 @@ __global__ void __launch_bounds__(kMidThreads, 1)
     const int row = tm_row % kRows, copy = tm_row / kRows;
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t sc = tmem + lane_off + s * 128, oc = tmem + lane_off + 256 + s * 128;
-    uint32_t n_s = 0, n_o[2] = {0, 0};
+    uint32_t n_s = 0;
     // after a failed wait a segment is finished without waiting or touching
     // tensor memory, so that the warps still meet at its barriers
     bool ok = true;  // warp-uniform
@@ -602,14 +605,12 @@ __global__ void __launch_bounds__(kMidThreads, 1)
       // The stretch's products are complete, of both slots that have some: the
       // exchange below uses Q's tile. A slot without pages waits for the other
       // one all the same, which is still writing Q there or multiplying it.
-#pragma unroll
-      for (int x = 0; x < 2; ++x)
-        if (x == 0 || second) {
-          wait_warp(&bar.o_full[x], n_o[x] & 1);
-          ++n_o[x];
-        }
+      wait_warp(&bar.o_full[0], k & 1);  // slot 0 has a page of every stretch
+      if (second) wait_warp(&bar.o_full[1], seg.seconds & 1);
       tc_fence_after();
       const bool done = ok && *abort_flag == 0;
+      m_run += vref.raise();
+      l_run *= vref.damp();
       // A row's shares of the stretch, two slots by KS copies, are added up
       // through Q's tile, 32 channels at a time and 16 / KS of them by each of
       // the threads that hold a share: [share][channel][row].
@@ -625,10 +626,9 @@ __global__ void __launch_bounds__(kMidThreads, 1)
         const float2 x = ml[i * kRows + row];
         l += x.y * ex2_approx(x.x - use);
       }
+      const float factor = ex2_approx(m_run - use) * vref.unit();
       const bool some = l != 0.f;
-      // divided by the sum before the unit is multiplied in: a mean of values
-      // fits fp32 where their sum might not
-      const float factor = ex2_approx(m_run - use) * (some ? 1.f / l : 0.f), unit = vref.unit();
+      const float inv = some ? 1.f / l : 0.f;
       const bool complete = np == seg.pages;
       float* out = part_of(part, blockIdx.x, seg.pg0 > 0, kMidRows);
       if (done && row_valid && share == 0) {
@@ -647,7 +647,7 @@ __global__ void __launch_bounds__(kMidThreads, 1)
           uint32_t o[32];
           tmem_ld32_wait(oc + cc * 32, o);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) joined[(share * 32 + e) * kRows + row] = __uint_as_float(o[e]) * factor * unit;
+          for (int e = 0; e < 32; ++e) joined[(share * 32 + e) * kRows + row] = __uint_as_float(o[e]) * factor;
         }
         named_bar_sync(1, 256);
         if (!done || !row_valid) continue;
@@ -686,7 +686,8 @@ __global__ void __launch_bounds__(kMidThreads, 1)
           uint2* dst = reinterpret_cast<uint2*>(p.o + at * 128 + ch);
 #pragma unroll
           for (int e = 0; e < kCh / 4; ++e)
-            dst[e] = some ? make_uint2(pack_bf16x2(x[4 * e], x[4 * e + 1]), pack_bf16x2(x[4 * e + 2], x[4 * e + 3]))
+            dst[e] = some ? make_uint2(pack_bf16x2(x[4 * e] * inv, x[4 * e + 1] * inv),
+                                       pack_bf16x2(x[4 * e + 2] * inv, x[4 * e + 3] * inv))
                           : make_uint2(0, 0);
         }
       }

@@ -485,9 +485,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     // ---------------------------------------------------------- results
     const bool done = ok && *abort_flag == 0;
     const float unit = vref.unit();
+    m_run += vref.raise();
+    l_run *= vref.damp();
     if (done && active) {
       const bool some = np > 0 && l_run != 0.f;
-      const float inv = some ? 1.f / l_run : 0.f;  // before the unit: a mean fits fp32 where a sum might not
+      const float inv = some ? 1.f / l_run : 0.f;
       float* out = part + static_cast<int64_t>(behind) * part_floats(kTileRows);  // with splits
       if (row_valid) {
         if (splits > 1)
@@ -506,7 +508,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           for (int e = 0; e < 32; ++e) o[e] = 0;
         }
 #pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * inv * unit);
+        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * unit);
         if (patch && row_valid) {
           // NaN values that were taken out of pages that not every row sees whole
           uint32_t bad = 0;
@@ -531,7 +533,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           uint32_t pk[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e)
-            pk[e] = some ? pack_bf16x2(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1])) : 0u;
+            pk[e] = some ? pack_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv) : 0u;
           store_row_chunk(p.o + at * 128 + cc * 32, pk);
         }
       }
