@@ -219,6 +219,16 @@ int check_shape(int batch, int heads_q, int heads_kv, int n, int max_new, int ma
   return CALIBATT_OK;
 }
 
+// Memory that a call reads or writes.
+struct Span {
+  const void* at;
+  size_t bytes;
+};
+bool meet(const Span& a, const Span& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.at), y = reinterpret_cast<uintptr_t>(b.at);
+  return a.at && b.at && x < y + b.bytes && y < x + a.bytes;
+}
+
 size_t workspace_bytes(const CachePlan& c) {
   if (c.rows <= kMidRows) {
     if (c.share.whole) return 0;
@@ -267,6 +277,17 @@ int calibatt_cache_attn_fwd(const calibatt_bf16* q, int heads_q, int heads_kv, i
   if (!plan.fits) return CALIBATT_ERR_UNSUPPORTED;
   const size_t need = workspace_bytes(plan);
   if (need > 0 && (!ws || ws_bytes < need)) return CALIBATT_ERR_ARG;
+  // a stream's parts are written while other CTAs still read
+  const size_t rows = static_cast<size_t>(heads_q) * n, pages = static_cast<size_t>(n_pages) * heads_kv;
+  const Span written[] = {{o, rows * 256}, {lse, rows * 4}, {need > 0 ? ws : nullptr, need}};
+  const Span read[] = {{q, rows * 256}, {k8, pages * kPage * 128}, {v8, pages * kPage * 128},
+                       {k_scale, pages * 4}, {v_scale, pages * 4}};
+  for (int i = 0; i < 3; ++i) {
+    for (const Span& r : read)
+      if (meet(written[i], r)) return CALIBATT_ERR_ARG;
+    for (int j = 0; j < i; ++j)
+      if (meet(written[i], written[j])) return CALIBATT_ERR_ARG;
+  }
   CacheAttnParams p{};
   p.status = status_word();
   if (!p.status) return CALIBATT_ERR_CUDA;

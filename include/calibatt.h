@@ -406,6 +406,7 @@ size_t calibatt_cache_attn_workspace_size(int batch, int heads_q, int heads_kv, 
  *            planned for; longer streams are still attended to in full
  *   ws   : device scratch of calibatt_cache_attn_workspace_size bytes, 16-byte
  *          aligned; calls that may run at the same time need one each
+ * o, lse and the workspace may not overlap each other or an input (refused).
  * Rows of tokens that belong to no stream are not written. New tokens may
  * outnumber the cached ones when causal_unit = 0. Outputs are summed in units
  * of the largest value scales met: pages whose value scale is less than 2^-70

@@ -161,3 +161,18 @@ def test_frame_streams_refuse_bad_shapes():
     for bad in (dict(batch=0), dict(heads=3), dict(kv_heads=0), dict(H=0), dict(pages=0)):
         with pytest.raises(ValueError):
             FrameStreams(**{**dict(batch=1, heads=4, kv_heads=2, H=2, W=3, pages=4), **bad})
+
+
+def test_cache_attn_refuses_outputs_over_its_inputs(binding):
+    """Parts of a stream are read by several CTAs while others already write: o and lse have memory of their own."""
+    size = 2 * 8 * 10 * 128  # bytes of q and o
+    apart = dict(q=FAKE, o=FAKE + (1 << 20), lse=FAKE + (2 << 20))
+    for bad in (dict(o=FAKE), dict(o=FAKE + size - 16), dict(q=FAKE + 256, o=FAKE), dict(lse=FAKE + size - 4),
+                dict(lse=FAKE + (1 << 20) + 64), dict(lse=FAKE - 4 * 8 * 10 + 4), dict(k8=FAKE + (1 << 20) - 16),
+                dict(v8=FAKE + (1 << 20) + size - 16), dict(v8=FAKE + (2 << 20))):
+        a = {**apart, **dict(k8=FAKE + (3 << 20), v8=FAKE + (3 << 20)), **bad}
+        assert _attn(binding, **a) == ARG, bad
+    # and the workspace
+    need = binding.cache_attn_workspace_size(2, 8, 4, 10, 5, 100000)
+    for ws in (FAKE, FAKE + (1 << 20), FAKE + (2 << 20), FAKE + (1 << 20) - need + 16):
+        assert _attn(binding, max_kv=100000, k8=FAKE + (3 << 28), v8=FAKE + (3 << 28), ws=ws, wsb=need, **apart) == ARG
