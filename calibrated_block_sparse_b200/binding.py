@@ -752,6 +752,14 @@ _PAIRINGS = {"interleaved": 0, "halves": 1}
 _LADDERS = {"axis": 0, "shared": 1}
 
 
+def _int32(x, name):
+    """A whole number that ctypes hands on as it is: it drops what is above 32 bits."""
+    x = index_of(x)
+    if not -1 << 31 <= x < 1 << 31:
+        raise ValueError(f"{name} must be a number of 32 bits")
+    return x
+
+
 def rope_plan(dims=(44, 42, 42), theta=10000.0, pairing="interleaved", ladder="axis") -> RopePlan:
     """Plan of a rotation of dims[0], dims[1], dims[2] channels by the time,
     height and width position (calibatt_rope_plan_init)."""
@@ -759,8 +767,10 @@ def rope_plan(dims=(44, 42, 42), theta=10000.0, pairing="interleaved", ladder="a
         raise ValueError("dims must name the channels of three axes")
     if pairing not in _PAIRINGS or ladder not in _LADDERS:
         raise ValueError(f"pairing must be one of {sorted(_PAIRINGS)}, ladder one of {sorted(_LADDERS)}")
+    if any(int(x) != x for x in dims):
+        raise ValueError("dims must be whole numbers of channels")
     plan = RopePlan()
-    d = (ctypes.c_int32 * 3)(*[int(x) for x in dims])
+    d = (ctypes.c_int32 * 3)(*[_int32(int(x), "dims") for x in dims])
     _check(load().calibatt_rope_plan_init(d, float(theta), _PAIRINGS[pairing], _LADDERS[ladder], ctypes.byref(plan)),
            "calibatt_rope_plan_init")
     return plan
@@ -869,7 +879,7 @@ def _rope(forward, q, k, plan, grid, start, pos, q_out, k_out, stream):
     if pos is None:
         if grid is None:
             raise ValueError("give the positions as a grid (H, W) or as a tensor pos [n][3]")
-        H, W = grid
+        H, W = (_int32(x, "grid") for x in grid)
         pos_ptr = None
     else:
         if grid is not None:
@@ -878,8 +888,9 @@ def _rope(forward, q, k, plan, grid, start, pos, q_out, k_out, stream):
         if pos.shape != (n, 3):
             raise ValueError(f"pos must be [{n}][3]")
         H, W, pos_ptr = 0, 0, pos.data_ptr()
-    if len(start) != 3 or any(not -1 << 31 <= index_of(x) < 1 << 31 for x in start):
-        raise ValueError("start must be three numbers of 32 bits")
+    if len(start) != 3:
+        raise ValueError("start must be three numbers")
+    start = [_int32(x, "start") for x in start]
     fn = load().calibatt_rope_fwd if forward else load().calibatt_rope_bwd
     rc = fn(ctypes.byref(plan), q.data_ptr(), st[tok], st[hd], heads, k_ptr, kst[tok], kst[hd], heads_k, n, HEAD_DIM,
             pos_ptr, H, W, (ctypes.c_int32 * 3)(*start), q_out.data_ptr(), ost[hd], ost[tok], k_out_ptr, kost[hd],
@@ -964,7 +975,7 @@ def cache_write(k, v, k8, v8, k_scale, v_scale, tok_start, kv_len, table, max_ne
         raise ValueError(f"the cache has {cache_heads} heads, k has {heads}")
     rc = load().calibatt_cache_write(
         k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], heads, n, HEAD_DIM, tok_start.data_ptr(),
-        kv_len.data_ptr(), batch, n if max_new is None else index_of(max_new), table.data_ptr(), width, pages,
+        kv_len.data_ptr(), batch, n if max_new is None else _int32(max_new, "max_new"), table.data_ptr(), width, pages,
         k8.data_ptr(), v8.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
         _current_raw_stream(index) if stream is None else stream.cuda_stream)
     if rc:
@@ -972,8 +983,13 @@ def cache_write(k, v, k8, v8, k_scale, v_scale, tok_start, kv_len, table, max_ne
 
 
 def cache_attn_workspace_size(batch, heads_q, heads_kv, n, max_new, max_kv) -> int:
-    return load().calibatt_cache_attn_workspace_size(int(batch), int(heads_q), int(heads_kv), int(n), int(max_new),
-                                                     int(max_kv))
+    return load().calibatt_cache_attn_workspace_size(
+        _int32(batch, "batch"), _int32(heads_q, "heads_q"), _int32(heads_kv, "heads_kv"), _int32(n, "n"),
+        _int32(max_new, "max_new"), _int32(max_kv, "max_kv"))
+
+
+def _table_tokens(width):
+    return min(width * BLOCK, (1 << 31) - 1)
 
 
 def cache_attn_workspace(q, k8, table, max_new=None, max_kv=None):
@@ -981,7 +997,7 @@ def cache_attn_workspace(q, k8, table, max_new=None, max_kv=None):
     heads_q, n = _bhnd(q)
     with torch.cuda.device(q.device):
         need = cache_attn_workspace_size(table.shape[0], heads_q, k8.shape[1], n, n if max_new is None else max_new,
-                                         table.shape[1] * BLOCK if max_kv is None else max_kv)
+                                         _table_tokens(table.shape[1]) if max_kv is None else max_kv)
     return torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
 
 
@@ -1019,8 +1035,8 @@ def cache_attn_fwd(q, k8, v8, k_scale, v_scale, tok_start, kv_len, table, max_ne
             raise ValueError(f"lse must be [{heads_q}][{n}]")
     elif want_lse:
         lse = _new(q, (heads_q, n), torch.float32, stream)
-    max_new = n if max_new is None else index_of(max_new)
-    max_kv = width * BLOCK if max_kv is None else index_of(max_kv)
+    max_new = n if max_new is None else _int32(max_new, "max_new")
+    max_kv = _table_tokens(width) if max_kv is None else _int32(max_kv, "max_kv")
     if ws is not None:
         _want(ws, torch.uint8, "ws", index)
         ws_bytes = ws.numel()
@@ -1029,10 +1045,10 @@ def cache_attn_fwd(q, k8, v8, k_scale, v_scale, tok_start, kv_len, table, max_ne
         if ws_bytes:
             ws = _new(q, (ws_bytes,), torch.uint8, stream)
     rc = load().calibatt_cache_attn_fwd(
-        q.data_ptr(), heads_q, heads_kv, n, HEAD_DIM, _SCALE if scale is None else float(scale), index_of(causal_unit),
-        tok_start.data_ptr(), kv_len.data_ptr(), batch, max_new, max_kv, table.data_ptr(), width, pages, k8.data_ptr(),
-        v8.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), o.data_ptr(), None if lse is None else lse.data_ptr(),
-        None if ws is None else ws.data_ptr(), ws_bytes,
+        q.data_ptr(), heads_q, heads_kv, n, HEAD_DIM, _SCALE if scale is None else float(scale),
+        _int32(causal_unit, "causal_unit"), tok_start.data_ptr(), kv_len.data_ptr(), batch, max_new, max_kv,
+        table.data_ptr(), width, pages, k8.data_ptr(), v8.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+        o.data_ptr(), None if lse is None else lse.data_ptr(), None if ws is None else ws.data_ptr(), ws_bytes,
         _current_raw_stream(index) if stream is None else stream.cuda_stream)
     if rc:
         _check(rc, "calibatt_cache_attn_fwd")

@@ -15,6 +15,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <climits>
 #include <cmath>
 #include <exception>
@@ -230,7 +231,7 @@ PyObject* cache_attn(PyObject*, PyObject* const* a, Py_ssize_t argc) {
     const int heads = small(q.size(0)), n = small(q.size(1));
     const Cache c = cache(a + 1, device);
     const int max_new = a[8] == Py_None ? n : number(a[8]);
-    const int max_kv = a[9] == Py_None ? small(c.width * kPage) : number(a[9]);
+    const int max_kv = a[9] == Py_None ? static_cast<int>(std::min<int64_t>(c.width * kPage, INT_MAX)) : number(a[9]);
     const int unit = number(a[10]);
     float scale = 1.f / std::sqrt(static_cast<float>(CALIBATT_HEAD_DIM));
     if (a[14] != Py_None) {

@@ -157,3 +157,44 @@ def test_values_next_to_the_largest(binding, rows):
         assert torch.equal(o, x[:1, 0].expand(1, rows, 128))
         assert torch.all((lse - np.log(1000)).abs() < 1e-5)
     assert binding.get_status() == 0
+
+
+# ---------------------------------------------------------------------------- unusual calls
+
+def test_numbers_beyond_32_bits_are_refused(binding):
+    """They would reach the library without their upper bits: a causal unit of 2^32 as none at all."""
+    c = Cache(1, 1, 2, seed=1)
+    x = torch.zeros((3, 1, 128), dtype=torch.bfloat16, device="cuda")
+    q, lists = x.transpose(0, 1).contiguous(), (_i32([0, 3]), _i32([200]), c.table)
+    before = [t.clone() for t in c.dev]
+    for kw in (dict(causal_unit=1 << 32), dict(max_new=(1 << 32) + 3), dict(max_kv=(1 << 32) + 256),
+               dict(causal_unit=-(1 << 32) + 1)):
+        with pytest.raises(ValueError):
+            binding.cache_attn_fwd(q, *c.dev, *lists, **kw)
+    with pytest.raises(ValueError):
+        binding.cache_write(x, x, *c.dev, *lists, max_new=(1 << 32) + 3)
+    with pytest.raises(ValueError):
+        binding.cache_attn_workspace(q, c.k, c.table, max_kv=(1 << 32) + 256)
+    for grid, start in ((((1 << 32) + 2, 2), (0, 0, 0)), ((2, (1 << 32) + 2), (0, 0, 0)), ((2, 2), (1 << 32, 0, 0))):
+        with pytest.raises(ValueError):
+            binding.rope_fwd(x, None, binding.rope_plan(), grid=grid, start=start)
+    assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(c.dev, before))
+    # numpy's numbers are taken like Python's
+    a = binding.cache_attn_fwd(q, *c.dev, *lists, max_new=np.int64(3), max_kv=np.int32(256), causal_unit=np.int64(2))
+    b = binding.cache_attn_fwd(q, *c.dev, *lists, max_new=3, max_kv=256, causal_unit=2)
+    assert all(torch.equal(s, t) for s, t in zip(a, b))
+    a = binding.rope_fwd(x, None, binding.rope_plan(), grid=np.array([2, 2]), start=np.array([1, 2, 3]))
+    b = binding.rope_fwd(x, None, binding.rope_plan(), grid=(2, 2), start=(1, 2, 3))
+    assert torch.equal(a[0], b[0])
+    assert binding.get_status() == 0
+
+
+def test_default_bound_of_a_table_for_2_31_tokens(binding, longest):
+    """A table that names more tokens than 32 bits count is no reason to refuse a short stream."""
+    *cache, table = longest
+    q = torch.ones((1, 1, 128), dtype=torch.bfloat16, device="cuda")
+    o, lse = binding.cache_attn_fwd(q, *cache, _i32([0, 1]), _i32([300]), table)
+    assert torch.all(o == 1.0) and torch.all((lse - np.log(300)).abs() < 1e-5)
+    ws = binding.cache_attn_workspace(q, cache[0], table)
+    again, _ = binding.cache_attn_fwd(q, *cache, _i32([0, 1]), _i32([300]), table, ws=ws)
+    assert torch.equal(o, again) and binding.get_status() == 0

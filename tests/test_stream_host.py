@@ -176,3 +176,17 @@ def test_cache_attn_refuses_outputs_over_its_inputs(binding):
     need = binding.cache_attn_workspace_size(2, 8, 4, 10, 5, 100000)
     for ws in (FAKE, FAKE + (1 << 20), FAKE + (2 << 20), FAKE + (1 << 20) - need + 16):
         assert _attn(binding, max_kv=100000, k8=FAKE + (3 << 28), v8=FAKE + (3 << 28), ws=ws, wsb=need, **apart) == ARG
+
+
+def test_numbers_beyond_32_bits_are_refused(binding):
+    """They would reach the library without their upper bits."""
+    for dims in (((1 << 32) + 44, 42, 42), (44, 42, 42 - (1 << 32)), (44, 42.5, 42)):
+        with pytest.raises(ValueError):
+            binding.rope_plan(dims)
+    for i in range(6):
+        a = [2, 8, 4, 10, 5, 100000]
+        a[i] += 1 << 32
+        with pytest.raises(ValueError):
+            binding.cache_attn_workspace_size(*a)
+    with pytest.raises(TypeError):
+        binding.cache_attn_workspace_size(2, 8, 4, 10, 5.5, 100000)
