@@ -900,17 +900,64 @@ def _rope(forward, q, k, plan, grid, start, pos, q_out, k_out, stream):
     return q_out, k_out
 
 
+def _asks_gradient(*tensors):
+    return torch.is_grad_enabled() and any(isinstance(t, torch.Tensor) and t.requires_grad for t in tensors)
+
+
+class _RopeGradient(torch.autograd.Function):
+    """rope_fwd and rope_bwd, each the other's gradient."""
+
+    @staticmethod
+    def forward(ctx, forward, plan, grid, start, pos, q, k):
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(pos)
+        ctx.how = forward, RopePlan.from_buffer_copy(plan), grid, start
+        return (rope_fwd if forward else rope_bwd)(q, k, plan, grid=grid, start=start, pos=pos)
+
+    @staticmethod
+    def backward(ctx, dq, dk):
+        forward, plan, grid, start = ctx.how
+        pos, = ctx.saved_tensors
+        back = rope_bwd if forward else rope_fwd
+        dq, dk = (_as_rows(d) if want else None for d, want in zip((dq, dk), ctx.needs_input_grad[5:]))
+        if dq is None and dk is not None:
+            dk, _ = back(dk, None, plan, grid=grid, start=start, pos=pos)
+        elif dq is not None:
+            dq, dk = back(dq, dk, plan, grid=grid, start=start, pos=pos)
+        return None, None, None, None, None, dq, dk
+
+
+def _as_rows(d):
+    """A gradient in a layout that the rotation reads (an expanded number has no row of channels)."""
+    if d is None or (d.stride(2) == 1 and not d.stride(0) % 8 and not d.stride(1) % 8 and not d.data_ptr() % 16):
+        return d
+    return d.clone(memory_format=torch.contiguous_format)
+
+
+def _rope_gradient(forward, q, k, plan, grid, start, pos, given, stream):
+    if any(t is not None for t in given):
+        raise ValueError("outputs cannot be given where a gradient is asked for")
+    args = (forward, plan, None if grid is None else tuple(grid), tuple(start), pos, q, k)
+    if stream is None:
+        return _RopeGradient.apply(*args)
+    with torch.cuda.stream(stream):  # its gradient follows there
+        return _RopeGradient.apply(*args)
+
+
 def rope_fwd(q, k, plan, grid=None, start=(0, 0, 0), pos=None, q_out=None, k_out=None, stream=None):
     """Rotates queries [n][heads][128] and keys [n][heads_k][128] (or None) of
     any strides by their positions: a grid (H, W) whose first token is at
     `start` (time, height, width), or pos, int32 [n][3]. Returns them as
-    [heads][n][128], the layout of the attention calls."""
+    [heads][n][128], the layout of the attention calls. Under autograd the
+    gradient is rope_bwd's (and cannot be had with q_out or k_out given)."""
     if not isinstance(plan, RopePlan):
         raise TypeError("plan must be a RopePlan")
     if stream is None:
         out = (_fast or _load_fast()).rope(True, q, k, ctypes.addressof(plan), grid, start, pos, q_out, k_out)
         if out is not None:
             return out
+    if _asks_gradient(q, k):
+        return _rope_gradient(True, q, k, plan, grid, start, pos, (q_out, k_out), stream)
     return _rope(True, q, k, plan, grid, start, pos, q_out, k_out, stream)
 
 
@@ -923,6 +970,8 @@ def rope_bwd(dq_out, dk_out, plan, grid=None, start=(0, 0, 0), pos=None, dq=None
         out = (_fast or _load_fast()).rope(False, dq_out, dk_out, ctypes.addressof(plan), grid, start, pos, dq, dk)
         if out is not None:
             return out
+    if _asks_gradient(dq_out, dk_out):
+        return _rope_gradient(False, dq_out, dk_out, plan, grid, start, pos, (dq, dk), stream)
     return _rope(False, dq_out, dk_out, plan, grid, start, pos, dq, dk, stream)
 
 
@@ -957,7 +1006,7 @@ def _cache_args(k8, v8, k_scale, v_scale, tok_start, kv_len, table, index):
 def cache_write(k, v, k8, v8, k_scale, v_scale, tok_start, kv_len, table, max_new=None, stream=None):
     """Appends keys and values [n][heads][128] (any strides) of the batch's new
     tokens to the paged 8-bit cache (calibatt_cache_write). max_new: the most
-    new tokens of one stream (default: n)."""
+    new tokens of one stream (default: n). No gradient flows into the cache."""
     if stream is None and (_fast or _load_fast()).cache_write(k, v, k8, v8, k_scale, v_scale, tok_start, kv_len, table,
                                                               max_new):
         return
@@ -1006,7 +1055,8 @@ def cache_attn_fwd(q, k8, v8, k_scale, v_scale, tok_start, kv_len, table, max_ne
     """Attention of the new tokens' queries [heads][n][128] over the paged
     8-bit cache (calibatt_cache_attn_fwd); returns (o, lse). Rows of tokens
     that belong to no stream keep what o and lse hold. max_new, max_kv: the
-    most new and cached tokens of one stream (default: n, the table's width)."""
+    most new and cached tokens of one stream (default: n, the table's width).
+    The outputs have no gradient."""
     if stream is None:
         out = (_fast or _load_fast()).cache_attn(q, k8, v8, k_scale, v_scale, tok_start, kv_len, table, max_new, max_kv,
                                                  causal_unit, o, lse, ws, scale, want_lse)

@@ -74,7 +74,8 @@ class FrameStreams:
         [heads][n]. Tokens are frames of H x W in order; a stream goes on where
         its last step ended, inside a frame if need be. causal_unit: as in
         binding.cache_attn_fwd (H * W: a token sees its own frame and earlier
-        ones; 0: all tokens of its stream, those of this step too)."""
+        ones; 0: all tokens of its stream, those of this step too). Made for
+        generating: the outputs have no gradient."""
         n = q.shape[0]
         if new is None and self.batch == 1:
             new = [n]
@@ -95,7 +96,8 @@ class FrameStreams:
         else:
             t = torch.cat([torch.arange(a, a + m) for a, m in zip(self.lengths, new)])
             where = dict(pos=torch.stack([t // hw, t % hw // self.W, t % self.W], 1).to(torch.int32).to(dev))
-        q, k = binding.rope_fwd(q, k, self.plan, **where)
+        with torch.no_grad():
+            q, k = binding.rope_fwd(q, k, self.plan, **where)
         lengths = [a + m for a, m in zip(self.lengths, new)]
         start = torch.tensor([0] + new, dtype=torch.int32).cumsum(0, dtype=torch.int32).to(dev)
         length = torch.tensor(lengths, dtype=torch.int32).to(dev)

@@ -5,7 +5,8 @@ import pytest
 import torch
 
 from gpu_util import bf16_to_f64
-from test_gpu_stream import Cache, _attn_close, _gen, _i32, _p_err, _randn, _starts, binding, so  # noqa: F401
+from test_gpu_stream import (Cache, _attn_close, _gen, _grid_pos, _i32, _p_err, _randn, _rope_close, _starts,  # noqa: F401
+                             binding, so)
 
 pytestmark = pytest.mark.gpu
 
@@ -198,3 +199,124 @@ def test_default_bound_of_a_table_for_2_31_tokens(binding, longest):
     ws = binding.cache_attn_workspace(q, cache[0], table)
     again, _ = binding.cache_attn_fwd(q, *cache, _i32([0, 1]), _i32([300]), table, ws=ws)
     assert torch.equal(o, again) and binding.get_status() == 0
+
+
+# ---------------------------------------------------------------------------- rotary positions and autograd
+
+@pytest.fixture(params=["compiled", "ctypes"])
+def calls(request, binding, monkeypatch):
+    monkeypatch.setattr(binding, "_fast", binding._load_fast() if request.param == "compiled" else binding._NoFast)
+    return binding
+
+
+@pytest.mark.parametrize("pairing", ["interleaved", "halves"])
+@pytest.mark.parametrize("given", ["grid", "pos"])
+def test_rope_under_autograd(calls, so, pairing, given):
+    """Slices of a fused projection that asks for a gradient: the formula's gradient, bit for bit rope_bwd's."""
+    g = _gen(31)
+    n, hq, hk, plan = 77, 4, 2, calls.rope_plan(pairing=pairing)
+    pos = torch.randint(-50, 5000, (n, 3), generator=g).int()
+    where = dict(pos=pos.cuda()) if given == "pos" else dict(grid=(5, 7), start=(3, 0, 1))
+    if given == "grid":
+        pos = torch.from_numpy(_grid_pos(n, 5, 7, (3, 0, 1)))
+    x = _randn(g, n, hq + hk, 128).cuda().requires_grad_()
+    qo, ko = calls.rope_fwd(x[:, :hq], x[:, hq:], plan, **where)
+    plain = calls.rope_fwd(x[:, :hq].detach(), x[:, hq:].detach(), plan, **where)
+    assert torch.equal(qo, plain[0]) and torch.equal(ko, plain[1])
+    assert qo.requires_grad and ko.requires_grad and not plain[0].requires_grad
+    dq, dk = _randn(g, hq, n, 128).cuda(), _randn(g, hk, n, 128).cuda()
+    before = bytes(plan)
+    plan.turns[0] = 0.25  # the gradient is that of the call, whatever becomes of its plan
+    torch.autograd.backward([qo, ko], [dq, dk])
+    plan = type(plan).from_buffer_copy(before)
+    want = torch.cat(calls.rope_bwd(dq, dk, plan, **where), 1)
+    assert torch.equal(x.grad, want)
+    both = bf16_to_f64(torch.cat([dq, dk]).transpose(0, 1))
+    _rope_close(bf16_to_f64(x.grad), so.rope(both, pos.numpy(), (44, 42, 42), pairing=pairing, inverse=True), both)
+
+
+def test_rope_autograd_of_one_output_and_odd_gradients(calls):
+    g = _gen(32)
+    plan = calls.rope_plan()
+    q, k = (_randn(g, 9, h, 128).cuda().requires_grad_() for h in (3, 2))
+    ones = lambda h: torch.ones((h, 9, 128), dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    back = calls.rope_bwd(ones(3), ones(2), plan, grid=(3, 3))
+    fwd = lambda *a, **kw: calls.rope_fwd(*a, plan, grid=(3, 3), **kw)  # noqa: E731
+    # one output alone is used; gradients that are one expanded number, or lie channel by channel
+    assert torch.equal(torch.autograd.grad(fwd(q, k)[1].sum(), k)[0], back[1])
+    assert torch.equal(torch.autograd.grad(fwd(q, k)[0].sum(), q)[0], back[0])
+    assert torch.autograd.grad(fwd(q, k)[1].sum(), q, allow_unused=True)[0] is None
+    assert torch.equal(torch.autograd.grad(fwd(q, None)[0].sum(), q)[0], back[0])
+    assert torch.equal(torch.autograd.grad(fwd(q.detach(), k)[1].sum(), k)[0], back[1])
+    odd = _randn(g, 128, 9, 3).cuda().permute(2, 1, 0)
+    got, = torch.autograd.grad(fwd(q, k)[0], q, odd)
+    assert torch.equal(got, calls.rope_bwd(odd.contiguous(), None, plan, grid=(3, 3))[0])
+    shifted = torch.empty(3 * 9 * 128 + 1, dtype=torch.bfloat16, device="cuda")[1:].view(3, 9, 128).copy_(odd)
+    got2, = torch.autograd.grad(fwd(q, k)[0], q, shifted)
+    assert torch.equal(got, got2)
+    # the gradient's own gradient is the rotation
+    dq = ones(3).requires_grad_()
+    gq, = torch.autograd.grad(fwd(q, None)[0], q, dq, create_graph=True)
+    w = _randn(g, 9, 3, 128).cuda()
+    assert torch.equal(torch.autograd.grad(gq, dq, w)[0], fwd(w, None)[0])
+    direct, _ = calls.rope_bwd(dq, None, plan, grid=(3, 3))
+    assert torch.equal(torch.autograd.grad(direct, dq, w)[0], fwd(w, None)[0])
+
+
+def test_rope_autograd_refusals_streams_and_no_grad(calls):
+    g = _gen(33)
+    plan = calls.rope_plan()
+    q = _randn(g, 6, 2, 128).cuda().requires_grad_()
+    out = torch.empty((2, 6, 128), dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(ValueError, match="gradient"):
+        calls.rope_fwd(q, None, plan, grid=(2, 3), q_out=out)
+    with torch.no_grad():
+        want = calls.rope_fwd(q, None, plan, grid=(2, 3), q_out=out)[0]
+        assert want is out or want.data_ptr() == out.data_ptr()
+        assert not calls.rope_fwd(q, None, plan, grid=(2, 3))[0].requires_grad
+    with torch.inference_mode():
+        assert torch.equal(calls.rope_fwd(q, None, plan, grid=(2, 3))[0], out)
+    # positions that are changed between the rotation and its gradient
+    pos = torch.ones((6, 3), dtype=torch.int32, device="cuda")
+    y, _ = calls.rope_fwd(q, None, plan, pos=pos)
+    pos += 1
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.sum().backward()
+    # on a stream of its own: the gradient follows it there
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    y, _ = calls.rope_fwd(q, None, plan, grid=(2, 3), stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(y, out)
+    dy = _randn(g, 2, 6, 128).cuda()
+    got, = torch.autograd.grad(y, q, dy)
+    assert torch.equal(got, calls.rope_bwd(dy, None, plan, grid=(2, 3))[0])
+
+
+def test_rope_autograd_in_a_captured_graph(calls):
+    g = _gen(34)
+    plan = calls.rope_plan()
+    q, k = (_randn(g, 8, h, 128).cuda().requires_grad_() for h in (3, 1))
+    pos = torch.zeros((8, 3), dtype=torch.int32, device="cuda")
+    dq, dk = (torch.empty((h, 8, 128), dtype=torch.bfloat16, device="cuda") for h in (3, 1))
+
+    def step():
+        outs = calls.rope_fwd(q, k, plan, pos=pos)
+        return outs + torch.autograd.grad(outs, (q, k), (dq, dk))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for seed in range(3):
+        with torch.no_grad():
+            for t in (q, k, dq, dk):
+                t.copy_(_randn(g, *t.shape))
+            pos.copy_(torch.randint(0, 99, (8, 3), generator=g).int())
+        graph.replay()
+        for a, b in zip(got, step()):
+            assert torch.equal(a, b)
