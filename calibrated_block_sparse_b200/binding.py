@@ -1044,9 +1044,11 @@ def _table_tokens(width):
 def cache_attn_workspace(q, k8, table, max_new=None, max_kv=None):
     """Workspace of cache_attn_fwd for these tensors (None when none is needed)."""
     heads_q, n = _bhnd(q)
-    with torch.cuda.device(q.device):
-        need = cache_attn_workspace_size(table.shape[0], heads_q, k8.shape[1], n, n if max_new is None else max_new,
-                                         _table_tokens(table.shape[1]) if max_kv is None else max_kv)
+    if torch.cuda.current_device() != q.get_device():
+        with torch.cuda.device(q.device):
+            return cache_attn_workspace(q, k8, table, max_new, max_kv)
+    need = cache_attn_workspace_size(table.shape[0], heads_q, k8.shape[1], n, n if max_new is None else max_new,
+                                     _table_tokens(table.shape[1]) if max_kv is None else max_kv)
     return torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
 
 

@@ -15,6 +15,9 @@ cache_attn_fwd); this class keeps the page table and the streams' lengths.
 """
 from __future__ import annotations
 
+from itertools import accumulate
+from operator import index
+
 import torch
 
 from . import binding
@@ -26,15 +29,17 @@ class FrameStreams:
     """Cache and positions of `batch` streams of H x W frames.
 
     pages: pages of 128 tokens shared by the streams; max_tokens: the most
-    tokens of one stream (default: all pages). A step that needs more pages
-    than are free, or makes a stream longer than max_tokens, is refused before
-    anything is changed. A step copies its lists from the host; a captured graph
+    tokens of one stream (default: all pages). A step that is refused (it needs
+    more pages than are free, makes a stream longer than max_tokens, gets
+    tensors or a causal_unit that do not fit) changes nothing. A step copies its lists from the host; a captured graph
     calls the binding's functions with lists of its own on the device.
     """
 
     def __init__(self, batch, heads, kv_heads, H, W, pages, max_tokens=None, plan=None, device=None):
         if min(batch, heads, kv_heads, H, W, pages) < 1 or heads % kv_heads:
             raise ValueError("batch, heads, kv_heads, H, W and pages must be positive, heads a multiple of kv_heads")
+        if max(batch, heads) > 65535:
+            raise ValueError("batch and heads must be at most 65535")
         self.batch, self.heads, self.kv_heads, self.H, self.W = batch, heads, kv_heads, H, W
         self.plan = binding.rope_plan() if plan is None else plan
         dev = torch.device("cuda" if device is None else device)
@@ -53,19 +58,19 @@ class FrameStreams:
     def free_pages(self):
         return len(self._free)
 
-    def _extend(self, new):
-        """Pages for new[b] more tokens of each stream."""
-        need = [-(-(n + m) // PAGE) - len(p) for n, m, p in zip(self.lengths, new, self._owned)]
-        if any(-(-(n + m) // PAGE) > self.width for n, m in zip(self.lengths, new)):
+    def _pages(self, new):
+        """Pages that new[b] more tokens of each stream need, as they would be taken."""
+        lengths = [n + m for n, m in zip(self.lengths, new)]
+        if any(-(-n // PAGE) > self.width for n in lengths):
             raise ValueError(f"a stream would be longer than its {self.width * PAGE} tokens")
+        need = [-(-n // PAGE) - len(p) for n, p in zip(lengths, self._owned)]
         if sum(need) > len(self._free):
             raise RuntimeError(f"{sum(need)} pages are needed, {len(self._free)} are free")
-        for b, count in enumerate(need):
-            if count > 0:
-                got = [self._free.pop() for _ in range(count)]
-                at = len(self._owned[b])
-                self._owned[b] += got
-                self.table[b, at:at + count] = torch.tensor(got, dtype=torch.int32, device=self.table.device)
+        at, got = len(self._free), []
+        for count in need:
+            got.append(self._free[at - count:at][::-1])
+            at -= count
+        return got
 
     def step(self, q, k, v, new=None, causal_unit=0):
         """Takes the new tokens' queries [n][heads][128], keys and values
@@ -85,26 +90,45 @@ class FrameStreams:
         rest = binding.HEAD_DIM,
         if q.shape != (n, self.heads) + rest or k.shape != (n, self.kv_heads) + rest or v.shape != k.shape:
             raise ValueError(f"q must be [{n}][{self.heads}][{rest[0]}], k and v [{n}][{self.kv_heads}][{rest[0]}]")
-        for t, name in ((q, "q"), (k, "k"), (v, "v")):
-            if t.dtype != torch.bfloat16 or t.device != self.k8.device or t.stride(2) != 1:
-                raise ValueError(f"{name} must be bfloat16 on {self.k8.device} with contiguous channels")
-        self._extend(new)
         dev = self.k8.device
+        for t, name in ((q, "q"), (k, "k"), (v, "v")):
+            strides = t.stride()
+            if t.dtype != torch.bfloat16 or t.device != dev or strides[2] != 1:
+                raise ValueError(f"{name} must be bfloat16 on {dev} with contiguous channels")
+            if n > 0 and (t.data_ptr() % 16 or strides[0] % 8 or strides[1] % 8):
+                raise ValueError(f"{name} must begin on 16 bytes, and so must its rows")
+        causal_unit = index(causal_unit)
+        if not 0 <= causal_unit < 1 << 31:
+            raise ValueError("causal_unit must be a number of tokens, or 0")
+        rows = max(new) * (self.heads // self.kv_heads)  # the attention's limits
+        if rows >= 1 << 30 or max(1, -(-rows // 256)) * self.batch * self.kv_heads >= 1 << 30:
+            raise ValueError("more tokens than one step takes")
+        got = self._pages(new)
         hw = self.H * self.W
+        lengths = [a + m for a, m in zip(self.lengths, new)]
+        lists = torch.tensor([0, *accumulate(new), *lengths], dtype=torch.int32)
         if self.batch == 1 and self.lengths[0] % hw == 0:
             where = dict(grid=(self.H, self.W), start=(self.lengths[0] // hw, 0, 0))
+            start, length = lists.to(dev).split((self.batch + 1, self.batch))
         else:
             t = torch.cat([torch.arange(a, a + m) for a, m in zip(self.lengths, new)])
-            where = dict(pos=torch.stack([t // hw, t % hw // self.W, t % self.W], 1).to(torch.int32).to(dev))
-        with torch.no_grad():
-            q, k = binding.rope_fwd(q, k, self.plan, **where)
-        lengths = [a + m for a, m in zip(self.lengths, new)]
-        start = torch.tensor([0] + new, dtype=torch.int32).cumsum(0, dtype=torch.int32).to(dev)
-        length = torch.tensor(lengths, dtype=torch.int32).to(dev)
+            pos = torch.stack([t // hw, t % hw // self.W, t % self.W], 1).to(torch.int32)
+            lists = torch.cat([pos.view(-1), lists]).to(dev)  # one copy
+            pos, start, length = lists.split((3 * n, self.batch + 1, self.batch))
+            where = dict(pos=pos.view(n, 3))
+        q, k = binding.rope_fwd(q.detach(), k.detach(), self.plan, **where)
+        for b, pages in enumerate(got):
+            if pages:
+                at = len(self._owned[b])
+                self.table[b, at:at + len(pages)] = torch.tensor(pages, dtype=torch.int32, device=dev)
+        # nothing that the arguments or the host's state decide is refused from here on
         binding.cache_write(k.transpose(0, 1), v, self.k8, self.v8, self.k_scale, self.v_scale, start, length,
                             self.table, max_new=max(new))
         out = binding.cache_attn_fwd(q, self.k8, self.v8, self.k_scale, self.v_scale, start, length, self.table,
                                      max_new=max(new), max_kv=max(lengths), causal_unit=causal_unit)
+        del self._free[len(self._free) - sum(map(len, got)):]
+        for pages, owned in zip(got, self._owned):
+            owned += pages
         self.lengths = lengths
         return out
 

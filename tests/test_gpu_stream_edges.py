@@ -320,3 +320,36 @@ def test_rope_autograd_in_a_captured_graph(calls):
         graph.replay()
         for a, b in zip(got, step()):
             assert torch.equal(a, b)
+
+
+# ---------------------------------------------------------------------------- refused steps
+
+def test_a_refused_step_leaves_the_cache_as_it_was(binding):
+    from calibrated_block_sparse_b200.stream import FrameStreams
+    g = _gen(41)
+    made = [FrameStreams(batch=2, heads=2, kv_heads=1, H=4, W=5, pages=8) for _ in range(2)]
+    x = _randn(g, 100, 4, 128).cuda()
+    for st in made:
+        st.step(x[:, :2], x[:, 2:3], x[:, 3:], new=[60, 40])
+    st = made[0]
+    free, was = st.free_pages, [t.clone() for t in (st.k8, st.v8, st.k_scale, st.v_scale, st.table)]
+    y = (_randn(g, 300, 4, 128) * 1000).cuda()  # larger: the scales of the begun pages would grow
+    wide = torch.zeros((300, 4, 132), dtype=torch.bfloat16, device="cuda")[:, :, :128]
+    odd = torch.zeros(300 * 128 + 1, dtype=torch.bfloat16, device="cuda")[1:].view(300, 1, 128)
+    refused = [dict(causal_unit=-1), dict(causal_unit=1 << 32), dict(causal_unit=0.5), dict(v=odd), dict(k=wide[:, :1]),
+               dict(q=wide[:, :2]), dict(v=wide[:, :1])]
+    for kw in refused:
+        a = {**dict(q=y[:, :2], k=y[:, 2:3], v=y[:, 3:]), **kw}
+        with pytest.raises((TypeError, ValueError, RuntimeError)):
+            st.step(**a, new=[200, 100])
+        assert st.lengths == [60, 40] and st.free_pages == free, kw
+    st.plan.pairs = 65
+    with pytest.raises(binding.CalibattError):
+        st.step(y[:, :2], y[:, 2:3], y[:, 3:], new=[200, 100])
+    st.plan.pairs = 64
+    assert st.lengths == [60, 40] and st.free_pages == free
+    for a, b in zip(was, (st.k8, st.v8, st.k_scale, st.v_scale, st.table)):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    outs = [s.step(x[:, :2], x[:, 2:3], x[:, 3:], new=[70, 30], causal_unit=20) for s in made]
+    assert all(torch.equal(a, b) for a, b in zip(*outs))
+    assert binding.get_status() == 0

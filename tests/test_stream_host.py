@@ -190,3 +190,65 @@ def test_numbers_beyond_32_bits_are_refused(binding):
             binding.cache_attn_workspace_size(*a)
     with pytest.raises(TypeError):
         binding.cache_attn_workspace_size(2, 8, 4, 10, 5.5, 100000)
+
+
+def _streams(**kw):
+    from calibrated_block_sparse_b200.stream import FrameStreams
+    return FrameStreams(**{**dict(batch=2, heads=4, kv_heads=2, H=2, W=3, pages=6, device="cpu"), **kw})
+
+
+def _state(st):
+    return ([t.view(torch.uint8).clone() for t in (st.k8, st.v8, st.k_scale, st.v_scale, st.table)], list(st.lengths),
+            st.free_pages, [list(p) for p in st._owned], list(st._free))
+
+
+def _unchanged(st, was):
+    now = _state(st)
+    return all(torch.equal(a, b) for a, b in zip(now[0], was[0])) and now[1:] == was[1:]
+
+
+def _tokens(n, odd=None):
+    """q, k, v of n tokens; odd: the one that does not begin on 16 bytes."""
+    make = lambda h, o: torch.zeros(n * h * 128 + 1, dtype=torch.bfloat16)[int(o):][:n * h * 128].view(n, h, 128)  # noqa: E731
+    return [make(h, name == odd) for h, name in ((4, "q"), (2, "k"), (2, "v"))]
+
+
+def test_a_refused_step_changes_nothing(binding, monkeypatch):
+    st = _streams()
+    fake = lambda *a, **kw: None  # noqa: E731
+    monkeypatch.setattr(binding, "rope_fwd", lambda q, k, plan, **kw: (q.transpose(0, 1), k.transpose(0, 1)))
+    monkeypatch.setattr(binding, "cache_write", fake)
+    monkeypatch.setattr(binding, "cache_attn_fwd", fake)
+    st.step(*_tokens(200), new=[130, 70])
+    assert st.lengths == [130, 70] and st.free_pages == 3
+    was = _state(st)
+    for unit in (-1, 1 << 31, 1.5, "6", None):
+        with pytest.raises((TypeError, ValueError)):
+            st.step(*_tokens(200), new=[130, 70], causal_unit=unit)
+        assert _unchanged(st, was), unit
+    for odd in "qkv":
+        with pytest.raises(ValueError):
+            st.step(*_tokens(200, odd), new=[130, 70])
+        assert _unchanged(st, was), odd
+    # whatever the rotation, the write or an allocation raises
+    for name, error in (("rope_fwd", binding.CalibattError(-1)), ("cache_write", binding.CalibattError(-5)),
+                        ("cache_attn_fwd", MemoryError())):
+        with monkeypatch.context() as m:
+            def fail(*a, **kw):
+                raise error
+            m.setattr(binding, name, fail)
+            with pytest.raises(type(error)):
+                st.step(*_tokens(200), new=[130, 70])
+        now = _state(st)
+        assert now[1:] == was[1:], name
+    # and the next one goes on as if nothing had been
+    st.step(*_tokens(200), new=[130, 70])
+    assert st.lengths == [260, 140] and st.free_pages == 1
+    assert sorted(sum(st._owned, st._free)) == list(range(6))
+    assert st.table[0, :3].tolist() == st._owned[0] and st.table[1, :2].tolist() == st._owned[1]
+
+
+def test_frame_streams_refuse_more_than_the_library_takes():
+    for bad in (dict(batch=65536), dict(heads=65536, kv_heads=65536)):
+        with pytest.raises(ValueError):
+            _streams(**{**dict(pages=1), **bad})
