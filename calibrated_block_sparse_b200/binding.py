@@ -13,6 +13,7 @@ import importlib.util
 import math
 import os
 import threading
+import warnings
 from operator import index as index_of
 
 import numpy as np
@@ -816,7 +817,7 @@ def _new(like, shape, dtype, stream):
 
 
 class _NoFast:
-    """In the place of the compiled calls where they were not built."""
+    """In the place of the compiled calls where they were not built, or do not fit."""
     rope = cache_write = cache_attn = staticmethod(lambda *args: None)
 
 
@@ -830,11 +831,21 @@ def _load_fast():
     global _fast
     lib, fast = load(), _NoFast
     if os.path.exists(_build.PYCALLS):
-        spec = importlib.util.spec_from_file_location("_pycalls", _build.PYCALLS)
-        fast = importlib.util.module_from_spec(spec)
-        spec.loader.exec_module(fast)
-        fast.bind(*(ctypes.cast(getattr(lib, f"calibatt_{x}"), ctypes.c_void_p).value
-                    for x in ("rope_fwd", "rope_bwd", "cache_write", "cache_attn_fwd", "cache_attn_workspace_size")))
+        try:
+            spec = importlib.util.spec_from_file_location("_pycalls", _build.PYCALLS)
+            made = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(made)
+            built = getattr(made, "torch", "of another version")
+            if built != str(torch.__version__):
+                raise ImportError(f"built against torch {built}")
+            if not made.bind(*(ctypes.cast(getattr(lib, f"calibatt_{x}"), ctypes.c_void_p).value
+                               for x in ("rope_fwd", "rope_bwd", "cache_write", "cache_attn_fwd",
+                                         "cache_attn_workspace_size", "version"))):
+                raise ImportError(f"built against another version of the library than {library_path()}")
+            fast = made
+        except ImportError as e:
+            warnings.warn(f"{_build.PYCALLS} does not fit ({e}): the streaming calls go through ctypes; rebuild it with "
+                          "python -m calibrated_block_sparse_b200.build", RuntimeWarning)
     _fast = fast
     return fast
 

@@ -8,11 +8,13 @@ from __future__ import annotations
 import glob
 import importlib.util
 import os
+import re
 import shutil
 import subprocess
 import sys
 import sysconfig
 import tempfile
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -35,7 +37,7 @@ def sources():
 
 
 def needs_build() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or (not os.path.exists(PYCALLS) and pycalls_command(LIB, "") is not None):
         return True
     t = os.path.getmtime(LIB)
     deps = sources() + [os.path.join(CSRC, "pycalls.cpp")] + glob.glob(os.path.join(CSRC, "*.cuh")) + \
@@ -56,6 +58,16 @@ def build(force: bool = False, ptxas_verbose: bool = False, jobs: int = 4, out_p
         flags += ["-Xptxas", "-v"]
     flags += [f"-D{d}" for d in defines]
     pycalls = start_pycalls(cc) if out_path is None else None
+    try:
+        return _build(cc, flags, jobs, target, pycalls)
+    finally:
+        if pycalls is not None:
+            pycalls[0].wait()
+            if os.path.exists(pycalls[1]):
+                os.remove(pycalls[1])
+
+
+def _build(cc, flags, jobs, target, pycalls):
     with tempfile.TemporaryDirectory(prefix="calibatt_build_") as tmp:
         objs = []
         procs = []
@@ -72,18 +84,30 @@ def build(force: bool = False, ptxas_verbose: bool = False, jobs: int = 4, out_p
         out = target + f".tmp{os.getpid()}"
         subprocess.check_call([cc, *ARCH, "-shared", "-o", out, *objs, "-lcudart_static", "-ldl", "-lpthread",
                                "-lrt"])
+        if target == LIB and os.path.exists(PYCALLS):
+            # it calls the library by address: one of another build may pass other arguments
+            os.remove(PYCALLS)
         os.replace(out, target)
     if pycalls is not None:
         process, made = pycalls
-        if process.wait() != 0:
-            raise RuntimeError("compiling pycalls.cpp failed")
-        os.replace(made, PYCALLS)
+        if process.wait() == 0:
+            os.replace(made, PYCALLS)
+        else:
+            warnings.warn("compiling pycalls.cpp failed: the streaming calls go through ctypes", RuntimeWarning)
     return target
 
 
 def start_pycalls(cc):
     """Starts compiling csrc/pycalls.cpp: the process and the file it makes, or
-    None without a C++ compiler or the headers of Python or torch."""
+    None where it cannot be made."""
+    out = PYCALLS + f".tmp{os.getpid()}"
+    command = pycalls_command(cc, out)
+    return None if command is None else (subprocess.Popen(command), out)
+
+
+def pycalls_command(cc, out):
+    """The compiler's call for csrc/pycalls.cpp, or None without a C++ compiler
+    or the headers of Python or torch."""
     gxx, include = shutil.which("g++") or shutil.which("c++"), sysconfig.get_paths()["include"]
     spec = importlib.util.find_spec("torch")
     if gxx is None or spec is None or not os.path.exists(os.path.join(include, "Python.h")):
@@ -91,13 +115,14 @@ def start_pycalls(cc):
     torch = spec.submodule_search_locations[0]
     if not os.path.exists(os.path.join(torch, "include", "torch", "csrc", "autograd", "python_variable.h")):
         return None
-    out = PYCALLS + f".tmp{os.getpid()}"
+    with open(os.path.join(torch, "version.py")) as f:
+        version = re.search(r"__version__ = ['\"]([^'\"]+)['\"]", f.read()).group(1)
     headers = [include, INCLUDE, os.path.join(torch, "include"),
                os.path.join(torch, "include", "torch", "csrc", "api", "include"),
                os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(cc))), "include")]
-    return subprocess.Popen([gxx, "-O2", "-std=c++17", "-Wall", "-fPIC", "-shared", *(f"-I{x}" for x in headers),
-                             os.path.join(CSRC, "pycalls.cpp"), "-o", out, "-L" + os.path.join(torch, "lib"), "-lc10",
-                             "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]), out
+    return [gxx, "-O2", "-std=c++17", "-Wall", "-fPIC", "-shared", f'-DCALIBATT_TORCH="{version}"',
+            *(f"-I{x}" for x in headers), os.path.join(CSRC, "pycalls.cpp"), "-o", out,
+            "-L" + os.path.join(torch, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
 
 
 if __name__ == "__main__":

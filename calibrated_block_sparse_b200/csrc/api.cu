@@ -138,7 +138,7 @@ const char* calibatt_strerror(int code) {
   }
 }
 
-int calibatt_version(void) { return 201; }
+int calibatt_version(void) { return CALIBATT_VERSION; }
 
 int calibatt_set_wait_limit(double seconds) {
   if (std::isnan(seconds) || seconds > 60.0) return CALIBATT_ERR_ARG;

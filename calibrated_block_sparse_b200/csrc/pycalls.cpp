@@ -30,7 +30,7 @@ decltype(&calibatt_rope_fwd) rope_fwd;
 decltype(&calibatt_rope_bwd) rope_bwd;
 decltype(&calibatt_cache_write) write_fn;
 decltype(&calibatt_cache_attn_fwd) attn_fn;
-decltype(&calibatt_cache_attn_workspace_size) attn_ws;
+decltype(&calibatt_cache_attn_workspace_size) attn_ws;  // all or none: see bind
 
 constexpr int64_t kPage = 128;
 
@@ -285,17 +285,23 @@ PyObject* cache_attn(PyObject*, PyObject* const* a, Py_ssize_t argc) {
   });
 }
 
-// The addresses of the loaded library's functions, in the order of the variables above.
+// The addresses of the loaded library's functions, in the order of the
+// variables above, then of calibatt_version. A library of another version may
+// want other arguments: False, and every call is left to the Python code.
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  void* at[5] = {};
-  for (Py_ssize_t i = 0; i < n && i < 5; ++i) at[i] = PyLong_AsVoidPtr(a[i]);
+  void* at[6] = {};
+  for (Py_ssize_t i = 0; i < n && i < 6; ++i) at[i] = PyLong_AsVoidPtr(a[i]);
   if (PyErr_Occurred()) return nullptr;
+  const auto version = reinterpret_cast<decltype(&calibatt_version)>(at[5]);
+  const bool fits = version != nullptr && version() == CALIBATT_VERSION;
+  if (!fits)
+    for (void*& x : at) x = nullptr;
   rope_fwd = reinterpret_cast<decltype(rope_fwd)>(at[0]);
   rope_bwd = reinterpret_cast<decltype(rope_bwd)>(at[1]);
   write_fn = reinterpret_cast<decltype(write_fn)>(at[2]);
   attn_fn = reinterpret_cast<decltype(attn_fn)>(at[3]);
   attn_ws = reinterpret_cast<decltype(attn_ws)>(at[4]);
-  Py_RETURN_NONE;
+  return PyBool_FromLong(fits);
 }
 
 template <PyObject* (*F)(PyObject*, PyObject* const*, Py_ssize_t)>
@@ -306,11 +312,15 @@ PyMethodDef method(const char* name, const char* doc) {
 PyMethodDef methods[] = {method<rope>("rope", "calibatt_rope_fwd or _bwd, or None"),
                          method<cache_write>("cache_write", "calibatt_cache_write, or None"),
                          method<cache_attn>("cache_attn", "calibatt_cache_attn_fwd, or None"),
-                         method<bind>("bind", "addresses of the library's functions"),
+                         method<bind>("bind", "addresses of the library's functions; whether they fit"),
                          {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_pycalls", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__pycalls() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__pycalls() {
+  PyObject* m = PyModule_Create(&module);
+  if (m && PyModule_AddStringConstant(m, "torch", CALIBATT_TORCH) != 0) Py_CLEAR(m);  // what it was built against
+  return m;
+}

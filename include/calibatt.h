@@ -54,6 +54,7 @@ typedef enum calibatt_status {
   CALIBATT_ERR_CAPACITY = -7     /* nnz exceeds the caller's col_idx capacity */
 } calibatt_status;
 
+#define CALIBATT_VERSION 202 /* what calibatt_version() of a library that fits this header gives */
 #define CALIBATT_BLOCK 128
 #define CALIBATT_HEAD_DIM 128
 #define CALIBATT_MAX_CALIB_NB 1024

@@ -252,3 +252,83 @@ def test_frame_streams_refuse_more_than_the_library_takes():
     for bad in (dict(batch=65536), dict(heads=65536, kv_heads=65536)):
         with pytest.raises(ValueError):
             _streams(**{**dict(pages=1), **bad})
+
+
+@pytest.fixture
+def tree(tmp_path, monkeypatch):
+    """A build of one small source into a folder of its own."""
+    from calibrated_block_sparse_b200 import build
+    src = tmp_path / "small.cu"
+    src.write_text("extern \"C\" int small(void) { return 1; }\n")
+    monkeypatch.setattr(build, "sources", lambda: [str(src)])
+    for name in ("LIB", "PYCALLS"):
+        path = tmp_path / (name + ".so")
+        path.write_text("old")
+        monkeypatch.setattr(build, name, str(path))
+    return build, tmp_path, src
+
+
+def _module(build, path, code):
+    """In the place of the module's compiler: a process that writes the module, or fails."""
+    import subprocess
+    import sys
+    text = f"open({str(path)!r}, 'w').write('new'); raise SystemExit({code})"
+    return lambda cc: (subprocess.Popen([sys.executable, "-c", text]), str(path))
+
+
+@pytest.mark.parametrize("made", [True, False, None])
+def test_a_module_of_another_build_does_not_stay(tree, monkeypatch, made):
+    """The compiled calls call the library by address: an old module beside a new library would pass old arguments."""
+    build, path, _ = tree
+    monkeypatch.setattr(build, "start_pycalls",
+                        (lambda cc: None) if made is None else _module(build, path / "tmp.so", 0 if made else 1))
+    build.build(force=True)
+    assert (path / "LIB.so").read_bytes()[:4] == b"\x7fELF"
+    if made:
+        assert (path / "PYCALLS.so").read_text() == "new"
+    else:
+        assert not (path / "PYCALLS.so").exists()
+    assert not (path / "tmp.so").exists()
+
+
+def test_a_failed_build_leaves_both_as_they_were(tree, monkeypatch):
+    build, path, src = tree
+    src.write_text("this is no source\n")
+    monkeypatch.setattr(build, "start_pycalls", _module(build, path / "tmp.so", 0))
+    with pytest.raises(RuntimeError):
+        build.build(force=True)
+    assert (path / "LIB.so").read_text() == (path / "PYCALLS.so").read_text() == "old"
+    assert not (path / "tmp.so").exists()
+
+
+def test_a_missing_module_is_built(binding, monkeypatch):
+    from calibrated_block_sparse_b200 import build
+    assert not build.needs_build()
+    monkeypatch.setattr(build, "PYCALLS", build.PYCALLS + ".none")
+    assert build.needs_build()
+    monkeypatch.setattr(build.shutil, "which", lambda name: None)  # no compiler: the calls go through ctypes
+    assert not build.needs_build()
+
+
+def test_a_module_that_does_not_fit_is_not_used(binding, tmp_path, monkeypatch):
+    from calibrated_block_sparse_b200 import build
+    monkeypatch.setattr(binding, "_fast", None)
+    with monkeypatch.context() as m:
+        broken = tmp_path / "broken.so"
+        broken.write_text("no module")
+        m.setattr(build, "PYCALLS", str(broken))
+        with pytest.warns(RuntimeWarning):
+            assert binding._load_fast() is binding._NoFast
+    with monkeypatch.context() as m:
+        m.setattr(torch, "__version__", "0.0.0")
+        with pytest.warns(RuntimeWarning):
+            assert binding._load_fast() is binding._NoFast
+    with monkeypatch.context() as m:
+        m.setattr(build, "PYCALLS", str(tmp_path / "none.so"))
+        assert binding._load_fast() is binding._NoFast
+    # a library of another version
+    fast = binding._load_fast()
+    assert fast is not binding._NoFast
+    other = ctypes.CFUNCTYPE(ctypes.c_int)(lambda: binding.load().calibatt_version() + 1)
+    assert fast.bind(*[ctypes.cast(other, P).value] * 6) is False
+    assert binding._load_fast() is not binding._NoFast  # bound again
