@@ -86,6 +86,28 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// fp16 operands, fp32 accumulation (operand formats 0); V has its channels (N) contiguous.
+constexpr uint32_t kIdescQK = (1u << 4) | (16u << 17) | (8u << 24);
+constexpr uint32_t kIdescPVh = kIdescQK | (1u << 16);
+
+__device__ __forceinline__ void st_shared16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+// 16 e4m3 values as two 16-byte chunks j, j + 1 of fp16 of row r, with the
+// 128-byte swizzle (chunk j is at j ^ (r & 7)).
+__device__ __forceinline__ void store_half(uint32_t row_addr, int r, int j, const uint4& w) {
+  const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+  uint32_t h[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    h[2 * i] = e4m3x2_to_half2(x[i] & 0xffffu);
+    h[2 * i + 1] = e4m3x2_to_half2(x[i] >> 16);
+  }
+  st_shared16(row_addr + ((j ^ (r & 7)) << 4), h[0], h[1], h[2], h[3]);
+  st_shared16(row_addr + (((j + 1) ^ (r & 7)) << 4), h[4], h[5], h[6], h[7]);
+}
+
 // One row's power of two: 2^(to - x) for a largest magnitude in [2^x, 2^(x+1)).
 __device__ __forceinline__ float row_shrink(float amax, int to) {
   const int x = (__float_as_int(amax) >> 23) - 127;  // amax >= 0; NaN and inf: 128
@@ -322,9 +344,8 @@ int launch_cache_attn_mid(const CacheAttnParams& p, const SharePlan& plan, void*
 int launch_cache_join(const CacheAttnParams& p, const SharePlan& plan, const float* part, int cap,
                       cudaStream_t stream);
 
-// Many rows: tiles of 256 rows, the pages of each cut into `splits`.
-// More rows: tiles of them; those behind the first `whole` are split over the
-// keys and joined.
+// More rows: tiles of 256 of them; those behind the first `whole` are split over
+// the keys and joined.
 struct TilePlan {
   int tiles;  // of a stream and key head, at most
   int chunk;  // (stream, key head) pairs whose tiles are taken together

@@ -32,6 +32,8 @@
 // each: the softmax of 16 rows in one thread is a chain of ~4000 cycles a page
 // (8 rows of 30000 keys, 2 streams: 34 us in one group, 32 in two; 15 rows in
 // four groups, whose registers do not fit: 8 us more than in two).
+// Two CTAs of 320 threads leave 96 registers a thread: with 8 rows a group
+// ptxas spills 100 bytes, with 1 and 4 rows none.
 // The running maximum of a row moves only if it grew by more than 2^4, which a
 // page finds out with one vote of a group's warps.
 //

@@ -30,9 +30,10 @@
 // on 8, 5 new tokens each in 132 us, half of the DRAM rate (150 us without the
 // copies; 148 us with K as an 8-bit operand and Q in three parts, which are 12
 // products instead of 8; 132 us with a second warpgroup of converters).
-// The register split leaves the issuer without spills; a spill there is read
-// back through an L1 that the tiles have flushed (measured at 40 registers:
-// ~350 cycles per MMA).
+// The register split keeps the issuer's loop in registers; a spill there is
+// read back through an L1 that the tiles have flushed (measured at 40
+// registers: ~350 cycles per MMA). ptxas spills 24 bytes with one copy of the
+// rows, none with two and four.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -106,28 +107,6 @@ struct MidBarriers {
 
 constexpr int kMidSmem = MidLayout::kBarOff + static_cast<int>(sizeof(MidBarriers)) + 1024;
 static_assert(kMidSmem <= 232448, "shared memory budget");
-
-// fp16 operands, fp32 accumulation (operand formats 0); V has its channels (N) contiguous.
-constexpr uint32_t kIdescQK = (1u << 4) | (16u << 17) | (8u << 24);
-constexpr uint32_t kIdescPVh = kIdescQK | (1u << 16);
-
-__device__ __forceinline__ void st_shared16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
-}
-
-// 16 e4m3 values as two 16-byte chunks j, j + 1 of fp16 of row r, with the
-// 128-byte swizzle (chunk j is at j ^ (r & 7)).
-__device__ __forceinline__ void store_half(uint32_t row_addr, int r, int j, const uint4& w) {
-  const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-  uint32_t h[8];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    h[2 * i] = e4m3x2_to_half2(x[i] & 0xffffu);
-    h[2 * i + 1] = e4m3x2_to_half2(x[i] >> 16);
-  }
-  st_shared16(row_addr + ((j ^ (r & 7)) << 4), h[0], h[1], h[2], h[3]);
-  st_shared16(row_addr + (((j + 1) ^ (r & 7)) << 4), h[4], h[5], h[6], h[7]);
-}
 
 __device__ __forceinline__ void tmem_ld_scores(uint32_t at, float (&s)[32]) {
   tmem_ld32_wait(at, reinterpret_cast<uint32_t(&)[32]>(s));

@@ -27,8 +27,9 @@
 // for nothing); three streams of four frames, causal by frames, in 460 us,
 // 0.53. Slower: exponentials on the FMA pipe (1/8 to 3/8 of them: 2 to 13 %),
 // one hand-over of P instead of two (5 %) or four (2.5 %), e4m3 tiles by TMA
-// (15 %), 176/96/64 registers (15 %), a persistent grid with equal shares (its
-// bookkeeping spilled the issuer's registers: 3 times as slow).
+// (15 %), 176/96/64 registers (15 %; with this split ptxas spills 4 bytes), a
+// persistent grid with equal shares (its bookkeeping spilled the issuer's
+// registers: 3 times as slow).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -83,28 +84,6 @@ struct TileLayout {
   static constexpr int kDynSmem = kBytes + 1024;
 };
 static_assert(TileLayout::kDynSmem <= 232448, "shared memory budget");
-
-// fp16 operands, fp32 accumulation (operand formats 0); V has its channels (N) contiguous.
-constexpr uint32_t kIdescQK = (1u << 4) | (16u << 17) | (8u << 24);
-constexpr uint32_t kIdescPVh = kIdescQK | (1u << 16);
-
-__device__ __forceinline__ void st_shared16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
-}
-
-// 16 e4m3 values as two 16-byte chunks j, j + 1 of fp16 of row r, with the
-// 128-byte swizzle (chunk j is at j ^ (r & 7)).
-__device__ __forceinline__ void store_half(uint32_t row_addr, int r, int j, const uint4& w) {
-  const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-  uint32_t h[8];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    h[2 * i] = e4m3x2_to_half2(x[i] & 0xffffu);
-    h[2 * i + 1] = e4m3x2_to_half2(x[i] >> 16);
-  }
-  st_shared16(row_addr + ((j ^ (r & 7)) << 4), h[0], h[1], h[2], h[3]);
-  st_shared16(row_addr + (((j + 1) ^ (r & 7)) << 4), h[4], h[5], h[6], h[7]);
-}
 
 // Tiles are taken rank by rank for a chunk of (stream, key head) pairs. Under a
 // causal mask the tiles with most keys have the lowest ranks, so the last ones
